@@ -339,6 +339,57 @@ flce_status flce_forward_noalloc(const void* X, const void* W, const int32_t* ta
                                  float label_smoothing, float zloss_scale, flce_reduction red,
                                  float* loss, float* lse, struct CUstream_st* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Block norm: the norms after and before a transformer block, fused with the block's gate
+ * and residual scale (the last one makes the hidden states X of the head).
+ *   u = x                             (post_weight NULL)
+ *     = Norm(x; post_weight, post_bias)
+ *   h = residual + scale * act(gate) * u          (residual or gate may be NULL)
+ *   y = Norm(h; weight, bias)                     (weight NULL: no y)
+ *   Norm(v) = v / sqrt(mean(v^2) + eps) * (w + weight_offset) + b                 (RMS)
+ *           = (v - mean(v)) / sqrt(var(v) + eps) * (w + weight_offset) + b        (LAYER)
+ * Rows of D columns; x, residual, gate, dh and dy have a row stride (elements, >= D) and unit
+ * column stride, the outputs are contiguous. x and y have one type, residual and h x's type
+ * or fp32, the gate one of the two, each parameter any type. gate [gate_rows, D]: gate row g
+ * belongs to rows g*N/gate_rows ... (1: a gate for each channel; N: one for each row).
+ * Statistics and sums are in 32 bits, y is computed from the unrounded h. h may be the
+ * residual's own buffer; the other outputs may not overlap the inputs. D up to 32768; any
+ * alignment to the elements is taken, rows aligned to eight elements are faster. */
+typedef enum { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_F16 = 1, FLCE_DTYPE_F32 = 2 } flce_dtype;
+typedef enum { FLCE_NORM_RMS = 0, FLCE_NORM_LAYER = 1 } flce_norm;
+typedef enum { FLCE_GATE_LINEAR = 0, FLCE_GATE_SIGMOID = 1, FLCE_GATE_TANH = 2 } flce_gate_activation;
+
+typedef struct {
+  int64_t N, D, gate_rows; /* gate_rows: 0 without a gate, else a divisor of N */
+  const void *x, *residual, *gate, *post_weight, *post_bias, *weight, *bias;
+  int64_t ld_x, ld_residual, ld_gate;
+  int32_t x_dtype, residual_dtype, gate_dtype, post_weight_dtype, post_bias_dtype, weight_dtype, bias_dtype;
+  int32_t norm, gate_activation;
+  float eps, scale, weight_offset;
+} flce_block_norm_desc;
+
+/* Outputs of the backward pass, each NULL where it is not wanted: dx in x's type, dresidual
+ * in the residual's, dgate [gate_rows, D] and the parameters' in their own. */
+typedef struct {
+  void *dx, *dresidual, *dgate, *dpost_weight, *dpost_bias, *dweight, *dbias;
+} flce_block_norm_grads;
+
+/* Forward. stats fp32 [4, N] (mean and reciprocal deviation of both norms) is what the
+ * backward pass needs; NULL where there is none. */
+flce_status flce_block_norm_forward(const flce_block_norm_desc* desc, void* h, void* y, float* stats,
+                                    struct CUstream_st* stream);
+
+/* Workspace bytes of the backward pass (0 for invalid sizes). */
+size_t flce_block_norm_workspace_size(int64_t N, int64_t D, int64_t gate_rows);
+
+/* Backward: h and stats from the forward, dh the gradient of h, dy that of y (either may be
+ * NULL, not both). The parameters' gradients are sums in a fixed order: the same inputs give
+ * the same bits. workspace: 256-byte aligned. */
+flce_status flce_block_norm_backward(const flce_block_norm_desc* desc, const void* h, const float* stats,
+                                     const void* dh, int64_t ld_dh, const void* dy, int64_t ld_dy,
+                                     const flce_block_norm_grads* grads, void* workspace, size_t ws_bytes,
+                                     struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif

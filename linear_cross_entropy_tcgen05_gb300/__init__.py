@@ -46,7 +46,8 @@ EXPORTED_SYMBOLS = ("flce_workspace_size", "flce_forward", "flce_backward", "flc
                     "flce_backward_ex", "flce_forward_backward", "flce_shard_stats", "flce_combine_shards",
                     "flce_last_error_detail", "flce_shard_stats_ex", "flce_kernel_launches",
                     "flce_selftest_wait_timeout", "flce_backward_band_width", "flce_profile_gemms",
-                    "flce_profile_read")
+                    "flce_profile_read", "flce_block_norm_forward", "flce_block_norm_backward",
+                    "flce_block_norm_workspace_size")
 GEMM_KINDS = ("forward", "gradient", "dW", "dX")  # the order of flce_profile_read's arrays
 
 
@@ -157,6 +158,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.flce_shard_stats_ex.restype = ctypes.c_int
     lib.flce_combine_shards.argtypes = [vp, i32, vp, i64, i64, i32, f32, f32, ctypes.c_int, vp, vp, vp, sz, vp]
     lib.flce_combine_shards.restype = ctypes.c_int
+    for ops in (norm_ops,):
+        ops.declare(lib)
     if path is None:
         _LIB = lib
     return lib
@@ -506,3 +509,10 @@ class FusedLinearCrossEntropyLoss(torch.nn.Module):
         acc = metrics["accuracy"][0] if self.return_token_accuracy else None
         pred = metrics["predicted"] if self.return_predicted_tokens else None
         return loss, acc, pred
+
+
+# the operators around the loss, each a module over the same library
+from . import norm_ops  # noqa: E402
+from .norm_ops import *  # noqa: E402,F401,F403
+
+__all__ += norm_ops.__all__

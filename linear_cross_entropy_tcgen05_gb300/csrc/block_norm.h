@@ -1,0 +1,70 @@
+// block_norm.h -- parameter block and launchers of the block norm (norms after and before a
+// transformer block fused with its gate and residual scale). Not part of the public ABI.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace flce {
+
+// A row is worked on by bn_threads(D) threads of eight columns each: at most 640 a block,
+// beyond that the blocks of a cluster (up to 8) share the row.
+constexpr int kBnMaxThreads = 640;
+constexpr int kBnMaxCluster = 8;
+constexpr int64_t kBnMaxD = 32768;
+
+struct BlockNormShape {
+  int cluster;          // blocks that share a row
+  int threads_per_row;  // in one block; a multiple of 32
+  int rows_per_block;   // row groups of a block, each with rows of its own
+};
+
+struct BlockNormParams {
+  const void *x, *residual, *gate, *w1, *b1, *w2, *b2;  // 1: after the block, 2: before the next
+  void *h, *y;
+  float* stats;  // [4][N] mean1, rstd1, mean2, rstd2; null: not kept
+  int64_t ld_x, ld_residual, ld_gate;
+  int64_t N;
+  int D;
+  int64_t gate_group;  // rows per gate row
+  int w1_dt, b1_dt, w2_dt, b2_dt;
+  int gate_res_type;   // the gate has the residual's type (else x's)
+  int act, layer;
+  float eps, scale, w_off;
+  // rows of a worker (row group), forward and backward
+  int64_t chunk_rows;
+  // backward
+  const void *h_in, *dh, *dy;
+  int64_t ld_dh, ld_dy;
+  void *dx, *dres, *dgate;
+  int64_t chunks, chunks_per_group, group_rows;  // chunks never cross a gate group
+  int gate_full;                                 // a gate row for each row: dgate is written row by row
+  float* part[4];    // dw1, db1, dw2, db2 partial sums [blocks][D], or null
+  float* part_gate;  // [chunks][D], or null (dgate written directly when a group is one chunk)
+};
+
+// Which accumulators the backward kernel keeps in registers.
+enum BnFeature : int { BN_POST = 1, BN_GATE = 2, BN_BIAS = 4, BN_ALL = 7 };
+
+cudaError_t bn_forward_bf16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, unsigned blocks, cudaStream_t);
+cudaError_t bn_forward_f16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, unsigned blocks, cudaStream_t);
+cudaError_t bn_forward_f32(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, unsigned blocks, cudaStream_t);
+cudaError_t bn_backward_bf16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
+cudaError_t bn_backward_f16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
+cudaError_t bn_backward_f32(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
+
+// out[s][j] = sum over rows of segment s of part[s * rows + r][j], for up to five arrays.
+struct BnSum {
+  const float* part;
+  void* out;
+  int64_t segments, rows;
+  int dt;
+};
+struct BnSums {
+  BnSum a[5];
+  int n, D;
+};
+cudaError_t bn_column_sums(const BnSums& s, cudaStream_t stream);
+
+}  // namespace flce

@@ -1,0 +1,18 @@
+// block_norm_f16.cu -- the block norm's kernels for f16 activations (f16 or fp32 residual stream).
+#include "block_norm_kernels.cuh"
+
+namespace flce {
+
+cudaError_t bn_forward_f16(const BlockNormParams& p, const BlockNormShape& s, bool res_f32, bool vec, unsigned blocks,
+                          cudaStream_t stream) {
+  return res_f32 ? bn_forward_typed<__half, float>(p, s, vec, blocks, stream)
+                 : bn_forward_typed<__half, __half>(p, s, vec, blocks, stream);
+}
+
+cudaError_t bn_backward_f16(const BlockNormParams& p, const BlockNormShape& s, bool res_f32, bool vec, int feat,
+                           unsigned blocks, cudaStream_t stream) {
+  return res_f32 ? bn_backward_typed<__half, float>(p, s, vec, feat, blocks, stream)
+                 : bn_backward_typed<__half, __half>(p, s, vec, feat, blocks, stream);
+}
+
+}  // namespace flce

@@ -31,6 +31,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/flce.h"
+#include "flce_host.h"
 #include "flce_internal.h"
 
 using namespace flce;
@@ -377,6 +378,25 @@ void pick_forward_schedule(int64_t n_tiles, int64_t v_tiles, int64_t D, FwdParam
   } while (0)
 
 }  // namespace
+
+namespace flce {
+
+flce_status api_device(int* sms, int* dev) { return current_device(sms, dev); }
+
+flce_status api_check_memory(int dev, const char* name, const void* p) {
+  return check_device_memory(dev, {{name, p}});
+}
+
+void api_note_error(const char* what, const char* why) { note_error(what, why); }
+
+flce_status api_cuda(const char* what, cudaError_t e) {
+  if (e == cudaSuccess) return FLCE_OK;
+  note_cuda_error(what, e);
+  cudaGetLastError();
+  return FLCE_ERR_CUDA;
+}
+
+}  // namespace flce
 
 extern "C" {
 

@@ -1,0 +1,273 @@
+"""The block norm: norms after and before a transformer block, fused with the block's gate and
+residual scale. ``block_norm`` is the differentiable call; ``flce_block_norm_forward`` and
+``flce_block_norm_backward`` marshal device tensors to the C ABI (include/flce.h), which has
+the formulas."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+__all__ = ["block_norm", "BlockNormFunction", "BlockNorm", "FlceBlockNormDesc", "FlceBlockNormGrads",
+           "flce_block_norm_forward", "flce_block_norm_backward", "flce_block_norm_workspace_size", "DTYPES", "NORMS",
+           "GATE_ACTIVATIONS"]
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # flce_dtype
+NORMS = {"rms": 0, "layer": 1}  # flce_norm
+GATE_ACTIVATIONS = {"none": 0, "sigmoid": 1, "tanh": 2}  # flce_gate_activation
+
+_VP, _I64, _I32, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+
+
+class FlceBlockNormDesc(ctypes.Structure):
+    """Mirror of ``flce_block_norm_desc`` in include/flce.h."""
+
+    _fields_ = ([(n, _I64) for n in ("N", "D", "gate_rows")]
+                + [(n, _VP) for n in ("x", "residual", "gate", "post_weight", "post_bias", "weight", "bias")]
+                + [(n, _I64) for n in ("ld_x", "ld_residual", "ld_gate")]
+                + [(n, _I32) for n in ("x_dtype", "residual_dtype", "gate_dtype", "post_weight_dtype",
+                                       "post_bias_dtype", "weight_dtype", "bias_dtype", "norm", "gate_activation")]
+                + [(n, _F32) for n in ("eps", "scale", "weight_offset")])
+
+
+class FlceBlockNormGrads(ctypes.Structure):
+    """Mirror of ``flce_block_norm_grads`` in include/flce.h."""
+
+    _fields_ = [(n, _VP) for n in ("dx", "dresidual", "dgate", "dpost_weight", "dpost_bias", "dweight", "dbias")]
+
+
+def declare(lib) -> None:
+    """Argument types of this module's entry points."""
+    desc, grads, sz, i = ctypes.POINTER(FlceBlockNormDesc), ctypes.POINTER(FlceBlockNormGrads), ctypes.c_size_t, ctypes.c_int
+    lib.flce_block_norm_forward.argtypes, lib.flce_block_norm_forward.restype = [desc, _VP, _VP, _VP, _VP], i
+    lib.flce_block_norm_workspace_size.argtypes, lib.flce_block_norm_workspace_size.restype = [_I64, _I64, _I64], sz
+    lib.flce_block_norm_backward.argtypes = [desc, _VP, _VP, _VP, _I64, _VP, _I64, grads, _VP, sz, _VP]
+    lib.flce_block_norm_backward.restype = i
+
+
+from . import _check, _nbytes, _ptr, _stream, load_library  # noqa: E402  (defined before this module is imported)
+
+
+def flce_block_norm_workspace_size(N: int, D: int, gate_rows: int = 0) -> int:
+    """Workspace bytes of flce_block_norm_backward."""
+    return int(load_library().flce_block_norm_workspace_size(N, D, gate_rows))
+
+
+def flce_block_norm_forward(desc: FlceBlockNormDesc, h, y, stats=None, stream=None, raise_on_error: bool = True) -> int:
+    """Call flce_block_norm_forward; returns the status."""
+    st = load_library().flce_block_norm_forward(ctypes.byref(desc), _ptr(h), _ptr(y), _ptr(stats), _stream(stream))
+    if raise_on_error:
+        _check(st, "flce_block_norm_forward")
+    return st
+
+
+def flce_block_norm_backward(desc: FlceBlockNormDesc, h, stats, dh, dy, grads: FlceBlockNormGrads, workspace,
+                             stream=None, raise_on_error: bool = True) -> int:
+    """Call flce_block_norm_backward (dh and dy [N, D] with unit column stride, or None)."""
+    st = load_library().flce_block_norm_backward(
+        ctypes.byref(desc), _ptr(h), _ptr(stats), _ptr(dh), 0 if dh is None else _row_stride(dh), _ptr(dy),
+        0 if dy is None else _row_stride(dy), ctypes.byref(grads), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    if raise_on_error:
+        _check(st, "flce_block_norm_backward")
+    return st
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _rows(t, D: int, name: str):
+    """t as [rows, D] without a copy."""
+    if t.dim() == 2 and (t.stride(1) == 1 or D == 1):
+        return t
+    if t.dim() != 2 and (t.stride(-1) == 1 or D == 1):
+        try:
+            return t.view(-1, D)
+        except RuntimeError:
+            pass
+    raise ValueError(f"{name} must have unit stride along its last dimension and one stride between its rows")
+
+
+def _gate_rows(gate, x) -> int:
+    """Rows of the gate: it is shared by all rows ([D]), by equal runs of rows ([G, D], or x's
+    shape with ones between the leading dimensions and the last), or has one for each."""
+    D = x.shape[-1]
+    if gate.dim() == 0 or gate.shape[-1] != D:
+        raise ValueError(f"gate must end with {D} columns, got {tuple(gate.shape)}")
+    rows = gate.numel() // D if D else 0
+    if gate.dim() == 1 or gate.shape == x.shape:
+        return rows
+    if x.dim() == 2 and gate.dim() == 2:
+        if rows > 0 and x.shape[0] % rows == 0:
+            return rows
+    elif gate.dim() == x.dim():
+        k = gate.dim() - 1
+        while k > 0 and gate.shape[k - 1] == 1:
+            k -= 1
+        if gate.shape[:k] == x.shape[:k]:
+            return rows
+    raise ValueError(f"gate {tuple(gate.shape)} does not group the rows of x {tuple(x.shape)}")
+
+
+def _describe(x, residual, weight, bias, post_weight, post_bias, gate, norm, eps, scale, gate_activation,
+              weight_offset):
+    """The descriptor of a call and x's rows; raises on what the library cannot take."""
+    if x.dtype not in DTYPES:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have at least one column")
+    D, dev = x.shape[-1], x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a CUDA tensor")
+    d = FlceBlockNormDesc()
+    rows = _rows(x, D, "x")
+    d.N, d.D, d.x, d.ld_x, d.x_dtype = rows.shape[0], D, x.data_ptr(), _row_stride(rows), DTYPES[x.dtype]
+    d.residual_dtype = d.x_dtype
+    if residual is not None:
+        if residual.shape != x.shape or residual.device != dev:
+            raise ValueError(f"residual must have x's shape {tuple(x.shape)} and device, got {tuple(residual.shape)}")
+        if residual.dtype != x.dtype and residual.dtype != torch.float32:
+            raise TypeError(f"residual must have x's type or float32, got {residual.dtype}")
+        r = _rows(residual, D, "residual")
+        d.residual, d.ld_residual, d.residual_dtype = residual.data_ptr(), _row_stride(r), DTYPES[residual.dtype]
+    if gate is not None:
+        if gate.device != dev:
+            raise ValueError("gate must be on x's device")
+        d.gate_rows = _gate_rows(gate, x)
+        if gate.dtype not in DTYPES or DTYPES[gate.dtype] not in (d.x_dtype, d.residual_dtype):
+            raise TypeError(f"gate must have x's or the residual's type, got {gate.dtype}")
+        g = _rows(gate if gate.dim() > 1 else gate.unsqueeze(0), D, "gate")
+        d.gate, d.ld_gate, d.gate_dtype = gate.data_ptr(), _row_stride(g), DTYPES[gate.dtype]
+    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        if t.shape != (D,) or t.device != dev:
+            raise ValueError(f"{name} must be [{D}] on x's device, got {tuple(t.shape)}")
+        if t.dtype not in DTYPES:
+            raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        setattr(d, name, t.data_ptr())
+        setattr(d, name + "_dtype", DTYPES[t.dtype])
+    if bias is not None and weight is None or post_bias is not None and post_weight is None:
+        raise ValueError("a bias needs its weight")
+    if norm not in NORMS:
+        raise ValueError(f"norm must be one of {sorted(NORMS)}")
+    if gate_activation not in GATE_ACTIVATIONS:
+        raise ValueError(f"gate_activation must be one of {sorted(GATE_ACTIVATIONS)}")
+    d.norm, d.gate_activation = NORMS[norm], GATE_ACTIVATIONS[gate_activation]
+    d.eps, d.scale, d.weight_offset = eps, scale, weight_offset
+    return d
+
+
+def _forward(d, x, h_dtype, want_y: bool, want_stats: bool):
+    h = torch.empty(x.shape, dtype=h_dtype, device=x.device)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_y else None
+    stats = torch.empty((4, d.N), dtype=torch.float32, device=x.device) if want_stats else None
+    if d.N > 0:
+        if x.device.index == torch.cuda.current_device():
+            flce_block_norm_forward(d, h, y, stats)
+        else:  # the library works on the current device and the current stream: make them x's
+            with torch.cuda.device(x.device):
+                flce_block_norm_forward(d, h, y, stats)
+    return h, y, stats
+
+
+class BlockNormFunction(torch.autograd.Function):
+    """(h, y) of the block norm with fused gradients; see ``block_norm``."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, post_weight, post_bias, gate, norm, eps, scale, gate_activation,
+                weight_offset):
+        opts = (norm, eps, scale, gate_activation, weight_offset)
+        d = _describe(x, residual, weight, bias, post_weight, post_bias, gate, *opts)
+        h, y, stats = _forward(d, x, x.dtype if residual is None else residual.dtype, weight is not None, True)
+        # the residual's values are not needed again, only its type (h has it)
+        ctx.save_for_backward(x, weight, bias, post_weight, post_bias, gate, h, stats)
+        ctx.opts = opts
+        ctx.set_materialize_grads(False)
+        return h, y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh, dy):
+        x, weight, bias, post_weight, post_bias, gate, h, stats = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        if dh is None and dy is None:
+            return (None,) * 12
+        with torch.cuda.device(x.device):
+            D = x.shape[-1]
+            d = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
+            out = {"dx": torch.empty_like(x, memory_format=torch.contiguous_format) if want[0] else None,
+                   "dresidual": torch.empty_like(h) if want[1] else None}
+            for i, (name, t) in enumerate((("dweight", weight), ("dbias", bias), ("dpost_weight", post_weight),
+                                           ("dpost_bias", post_bias), ("dgate", gate))):
+                out[name] = torch.empty(t.shape, dtype=t.dtype, device=t.device) if want[2 + i] else None
+            if d.N == 0:
+                for t in out.values():
+                    if t is not None:
+                        t.zero_()
+            else:
+                # gradients may come with any strides (expanded ones, say): rows are made of those
+                dh, dy = (t if t is None else t.reshape(-1, D) for t in (dh, dy))
+                dh, dy = (t if t is None or (t.stride(1) == 1 and _row_stride(t) >= D) else t.contiguous()
+                          for t in (dh, dy))
+                dh = dh if dh is None or dh.dtype == h.dtype else dh.to(h.dtype)
+                dy = dy if dy is None or dy.dtype == x.dtype else dy.to(x.dtype)
+                ws = torch.empty(flce_block_norm_workspace_size(d.N, D, d.gate_rows), dtype=torch.uint8, device=x.device)
+                grads = FlceBlockNormGrads(**{k: _ptr(v) for k, v in out.items()})
+                flce_block_norm_backward(d, h, stats, dh, dy, grads, ws)
+        return (out["dx"], out["dresidual"], out["dweight"], out["dbias"], out["dpost_weight"], out["dpost_bias"],
+                out["dgate"], None, None, None, None, None)
+
+
+def block_norm(x, residual=None, weight=None, *, bias=None, post_weight=None, post_bias=None, gate=None,
+               gate_activation: str = "none", scale: float = 1.0, norm: str = "rms", eps: float = 1e-6,
+               weight_offset: float = 0.0):
+    """``(h, y)`` with ``h = residual + scale * act(gate) * u`` and ``y = Norm(h; weight, bias)``,
+    ``u = Norm(x; post_weight, post_bias)`` or ``x`` without a post_weight.
+
+    ``x`` [..., D] (bf16, f16 or f32) is a block's output, ``residual`` the stream it is added
+    to (x's type or f32; None: nothing is added), ``y`` the next block's or the head's input in
+    x's type (None without a ``weight``), ``h`` the new stream in the residual's type. ``gate``
+    (x's or the residual's type) has one row for all rows ([D]), one for each equal run of rows
+    ([G, D]; for x [B, T, D] also [B, 1, D]) or x's shape, and goes through
+    ``gate_activation`` ("none", "sigmoid", "tanh"). ``norm`` is "rms" or "layer"; weights are
+    used as ``weight + weight_offset``. D is at most 32768.
+
+    Differentiable in every tensor; a gradient has its input's type. With a 16-bit residual
+    stream the backward pass reads the rounded h.
+    """
+    args = (x, residual, weight, bias, post_weight, post_bias, gate)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args):
+        return BlockNormFunction.apply(*args, norm, eps, scale, gate_activation, weight_offset)
+    d = _describe(*args, norm, eps, scale, gate_activation, weight_offset)
+    h, y, _ = _forward(d, x, x.dtype if residual is None else residual.dtype, weight is not None, False)
+    return h, y
+
+
+class BlockNorm(torch.nn.Module):
+    """``block_norm`` with parameters of its own: a pre-norm (``weight``), and as asked a post-norm
+    (``post_weight``), a gate for each channel (``gate``, starting at ``gate_init``) and biases."""
+
+    def __init__(self, dim: int, norm: str = "rms", eps: float = 1e-6, scale: float = 1.0, post_norm: bool = False,
+                 gate_init: float | None = None, gate_activation: str = "none", bias: bool = False, device=None,
+                 dtype=None):
+        super().__init__()
+        if norm not in NORMS:
+            raise ValueError(f"norm must be one of {sorted(NORMS)}")
+        if gate_activation not in GATE_ACTIVATIONS:
+            raise ValueError(f"gate_activation must be one of {sorted(GATE_ACTIVATIONS)}")
+        kw = dict(device=device, dtype=dtype)
+        par = torch.nn.Parameter
+        self.norm, self.eps, self.scale, self.gate_activation = norm, float(eps), float(scale), gate_activation
+        self.weight = par(torch.ones(dim, **kw))
+        self.bias = par(torch.zeros(dim, **kw)) if bias else None
+        self.post_weight = par(torch.ones(dim, **kw)) if post_norm else None
+        self.post_bias = par(torch.zeros(dim, **kw)) if post_norm and bias else None
+        self.gate = par(torch.full((dim,), float(gate_init), **kw)) if gate_init is not None else None
+
+    def forward(self, x, residual=None):
+        return block_norm(x, residual, self.weight, bias=self.bias, post_weight=self.post_weight,
+                          post_bias=self.post_bias, gate=self.gate, gate_activation=self.gate_activation,
+                          scale=self.scale, norm=self.norm, eps=self.eps)
