@@ -390,6 +390,63 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* desc, const voi
                                      const flce_block_norm_grads* grads, void* workspace, size_t ws_bytes,
                                      struct CUstream_st* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Global gradient norm over many tensors, and clipping.
+ *   total = |grad_scale| * (sum over all elements of g^2)^(1/2)         (norm_type 2)
+ *         = |grad_scale| * max |g|                                      (norm_type infinity)
+ *   out   = g * grad_scale * min(1, max_norm / (total + eps))
+ * `tensors` is a host array, read before the call returns. A tensor is n elements in one run
+ * of memory; out may be grad (in place, the same type) or NULL (only the norm counts it); a
+ * buffer may not be listed twice. total_norm: device fp32 scalar. The sum of squares is held
+ * in 64 bits and added in a fixed order. A NaN norm makes every output NaN. The workspace is
+ * 256-byte aligned and needs no preparation. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t dtype, out_dtype; /* flce_dtype */
+} flce_grad_tensor;
+
+size_t flce_clip_grad_norm_workspace_size(int64_t count);
+
+flce_status flce_clip_grad_norm(const flce_grad_tensor* tensors, int64_t count, float max_norm, float norm_type,
+                                float eps, float grad_scale, float* total_norm, void* workspace, size_t ws_bytes,
+                                struct CUstream_st* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Beam search: selection over beams and vocabulary, and reordering of the states.
+ *
+ * flce_beam_select: of the K V candidates
+ *   s[k, v] = scores[b, k] + logits[b, k, v] - lse_v(logits[b, k, :])
+ * of each request b the M best, best first, the lowest k V + v first where they are equal:
+ * out_scores fp32, out_parents (k) and out_tokens (v) int32, each [B, M]. logits: element
+ * strides ld_batch and ld_beam, unit stride along V. A beam with finished[b, k] != 0 (NULL:
+ * none) has the one candidate (pad_token, scores[b, k]). A beam whose score or lse is not
+ * finite has none. What is no candidate has a score of -inf and comes last, lowest index
+ * first. Scores are compared in 64 bits. K <= 32, M <= 64, B K <= 65535. */
+size_t flce_beam_select_workspace_size(int64_t B, int64_t K, int64_t V, int64_t M);
+
+flce_status flce_beam_select(const void* logits, int32_t dtype, int64_t B, int64_t K, int64_t V, int64_t ld_batch,
+                             int64_t ld_beam, const float* scores, const uint8_t* finished, int32_t pad_token,
+                             int64_t M, float* out_scores, int32_t* out_parents, int32_t* out_tokens, void* workspace,
+                             size_t ws_bytes, struct CUstream_st* stream);
+
+/* A state of B K beams, as bytes: an inner run of inner_bytes and four outer dimensions (size 1
+ * where there are fewer) with byte strides. src == dst reorders in place (equal strides);
+ * else the two share no memory. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t beam_stride_src, beam_stride_dst, inner_bytes;
+  int64_t outer_size[4], outer_stride_src[4], outer_stride_dst[4];
+} flce_beam_state;
+
+/* dst[b K + j] = src[b K + parents[b, j]] for every state (a host array, read before the call
+ * returns) and outer index. parents: device int32, row stride ld_parents; one outside
+ * [0, K) leaves the beam's own state. K <= 32. */
+flce_status flce_beam_reorder(const flce_beam_state* states, int64_t count, const int32_t* parents, int64_t ld_parents,
+                              int64_t B, int64_t K, struct CUstream_st* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -47,7 +47,8 @@ EXPORTED_SYMBOLS = ("flce_workspace_size", "flce_forward", "flce_backward", "flc
                     "flce_last_error_detail", "flce_shard_stats_ex", "flce_kernel_launches",
                     "flce_selftest_wait_timeout", "flce_backward_band_width", "flce_profile_gemms",
                     "flce_profile_read", "flce_block_norm_forward", "flce_block_norm_backward",
-                    "flce_block_norm_workspace_size")
+                    "flce_block_norm_workspace_size", "flce_clip_grad_norm", "flce_clip_grad_norm_workspace_size",
+                    "flce_beam_select", "flce_beam_select_workspace_size", "flce_beam_reorder")
 GEMM_KINDS = ("forward", "gradient", "dW", "dX")  # the order of flce_profile_read's arrays
 
 
@@ -158,7 +159,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.flce_shard_stats_ex.restype = ctypes.c_int
     lib.flce_combine_shards.argtypes = [vp, i32, vp, i64, i64, i32, f32, f32, ctypes.c_int, vp, vp, vp, sz, vp]
     lib.flce_combine_shards.restype = ctypes.c_int
-    for ops in (norm_ops,):
+    for ops in (norm_ops, grad_ops, beam_ops):
         ops.declare(lib)
     if path is None:
         _LIB = lib
@@ -512,7 +513,9 @@ class FusedLinearCrossEntropyLoss(torch.nn.Module):
 
 
 # the operators around the loss, each a module over the same library
-from . import norm_ops  # noqa: E402
+from . import norm_ops, grad_ops, beam_ops  # noqa: E402
 from .norm_ops import *  # noqa: E402,F401,F403
+from .grad_ops import *  # noqa: E402,F401,F403
+from .beam_ops import *  # noqa: E402,F401,F403
 
-__all__ += norm_ops.__all__
+__all__ += norm_ops.__all__ + grad_ops.__all__ + beam_ops.__all__

@@ -20,7 +20,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libflce.so")
 
 SOURCES = ["flce_gemm.cu", "flce_small.cu", "flce_api.cu", "flce_noalloc.cu", "flce_block_norm.cu", "block_norm_bf16.cu",
-           "block_norm_f16.cu", "block_norm_f32.cu"]
+           "block_norm_f16.cu", "block_norm_f32.cu", "flce_grad_clip.cu", "flce_beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]
