@@ -374,8 +374,9 @@ typedef struct {
   void *dx, *dresidual, *dgate, *dpost_weight, *dpost_bias, *dweight, *dbias;
 } flce_block_norm_grads;
 
-/* Forward. stats fp32 [4, N] (mean and reciprocal deviation of both norms) is what the
- * backward pass needs; NULL where there is none. */
+/* Forward. stats fp32 [N, 4], 16-byte aligned (mean and reciprocal deviation of the norm after
+ * the block, then of the one before the next), is what the backward pass needs; NULL where
+ * there is none. */
 flce_status flce_block_norm_forward(const flce_block_norm_desc* desc, void* h, void* y, float* stats,
                                     struct CUstream_st* stream);
 

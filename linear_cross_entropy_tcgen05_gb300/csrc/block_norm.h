@@ -8,10 +8,11 @@
 
 namespace flce {
 
-// A row is worked on by bn_threads(D) threads of eight columns each: at most 640 a block,
+// A row is worked on by bn_threads(D) threads of eight columns each: at most 512 a block,
 // beyond that the blocks of a cluster (up to 8) share the row.
-constexpr int kBnMaxThreads = 640;
+constexpr int kBnMaxThreads = 512;
 constexpr int kBnMaxCluster = 8;
+constexpr int kBnSmemBytes = 212 << 10;  // shared memory for parameters and rows on their way in
 constexpr int64_t kBnMaxD = 32768;
 
 struct BlockNormShape {
@@ -23,7 +24,7 @@ struct BlockNormShape {
 struct BlockNormParams {
   const void *x, *residual, *gate, *w1, *b1, *w2, *b2;  // 1: after the block, 2: before the next
   void *h, *y;
-  float* stats;  // [4][N] mean1, rstd1, mean2, rstd2; null: not kept
+  float* stats;  // [N][4] mean1, rstd1, mean2, rstd2; null: not kept
   int64_t ld_x, ld_residual, ld_gate;
   int64_t N;
   int D;
@@ -44,12 +45,19 @@ struct BlockNormParams {
   float* part_gate;  // [chunks][D], or null (dgate written directly when a group is one chunk)
 };
 
-// Which accumulators the backward kernel keeps in registers.
-enum BnFeature : int { BN_POST = 1, BN_GATE = 2, BN_BIAS = 4, BN_ALL = 7 };
+// What the code of a kernel has: the norm after the block, a gate, and (FULL) the means
+// of layer norms and biases. A kernel takes what has less at run time.
+enum BnFeature : int { BN_POST = 1, BN_GATE = 2, BN_FULL = 4, BN_ALL = 7 };
+// Parameters that a kernel keeps in shared memory (the others have room for theirs in registers).
+__host__ __device__ constexpr int bn_shared_params(int feat, bool backward) {
+  if (!(feat & BN_FULL)) return 0;
+  if (!backward) return feat & BN_GATE ? 4 : 2;
+  return feat & BN_POST ? (feat & BN_GATE ? 3 : 2) : 1;
+}
 
-cudaError_t bn_forward_bf16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, unsigned blocks, cudaStream_t);
-cudaError_t bn_forward_f16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, unsigned blocks, cudaStream_t);
-cudaError_t bn_forward_f32(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, unsigned blocks, cudaStream_t);
+cudaError_t bn_forward_bf16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
+cudaError_t bn_forward_f16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
+cudaError_t bn_forward_f32(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
 cudaError_t bn_backward_bf16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
 cudaError_t bn_backward_f16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
 cudaError_t bn_backward_f32(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);

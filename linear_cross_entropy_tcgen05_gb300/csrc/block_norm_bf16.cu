@@ -3,10 +3,10 @@
 
 namespace flce {
 
-cudaError_t bn_forward_bf16(const BlockNormParams& p, const BlockNormShape& s, bool res_f32, bool vec, unsigned blocks,
+cudaError_t bn_forward_bf16(const BlockNormParams& p, const BlockNormShape& s, bool res_f32, bool vec, int feat, unsigned blocks,
                           cudaStream_t stream) {
-  return res_f32 ? bn_forward_typed<__nv_bfloat16, float>(p, s, vec, blocks, stream)
-                 : bn_forward_typed<__nv_bfloat16, __nv_bfloat16>(p, s, vec, blocks, stream);
+  return res_f32 ? bn_forward_typed<__nv_bfloat16, float>(p, s, vec, feat, blocks, stream)
+                 : bn_forward_typed<__nv_bfloat16, __nv_bfloat16>(p, s, vec, feat, blocks, stream);
 }
 
 cudaError_t bn_backward_bf16(const BlockNormParams& p, const BlockNormShape& s, bool res_f32, bool vec, int feat,

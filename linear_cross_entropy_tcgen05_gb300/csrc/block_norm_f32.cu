@@ -3,9 +3,9 @@
 
 namespace flce {
 
-cudaError_t bn_forward_f32(const BlockNormParams& p, const BlockNormShape& s, bool, bool vec, unsigned blocks,
+cudaError_t bn_forward_f32(const BlockNormParams& p, const BlockNormShape& s, bool, bool vec, int feat, unsigned blocks,
                            cudaStream_t stream) {
-  return bn_forward_typed<float, float>(p, s, vec, blocks, stream);
+  return bn_forward_typed<float, float>(p, s, vec, feat, blocks, stream);
 }
 
 cudaError_t bn_backward_f32(const BlockNormParams& p, const BlockNormShape& s, bool, bool vec, int feat,

@@ -17,60 +17,232 @@
 #include "flce_internal.h"
 #include "sm103_ptx.cuh"
 
+// The kernels' local functions: one that is not inlined would keep what it refers to in memory.
+#define FLCE_INLINE __attribute__((always_inline))
+
 namespace flce {
 namespace {
 
-// Sums over the threads of a row. Two scratch buffers take turns, so one barrier a sum is
-// enough: a buffer is written again only after the barrier of the sum between.
+// Rows that a row group works on together at most: they share the latency of their sums. Where
+// shared memory has no room for two batches of two rows, a batch is one row.
+// (Four in the forward pass measured slower: their copies come in bursts that leave the
+// memory idle between them, N = 65536, D = 4096 bf16: 537 us against 431.)
+constexpr int kBnRows = 2;
+
+// Rows are copied to shared memory (cp.async) some batches of kBnRows rows ahead. A thread
+// copies and reads only its own eight columns, so a batch is ready for it when its own copies
+// are: no barrier. A batch has, for each of its rows and tensors, planes of 16 bytes a thread.
+// Slots whose tensor or columns are not there are zeroed once and never copied to.
+struct RowRing {
+  uint32_t first, end;       // this thread's first plane of the ring's first batch, and past its last
+  int plane, row_bytes;      // bytes of a plane (16 a thread) and of a row's planes
+  uint32_t batch_bytes;
+
+  __device__ __forceinline__ void init(char* smem, int planes, int batches, int rows) {
+    plane = 16 * int(blockDim.x);
+    row_bytes = planes * plane;
+    batch_bytes = uint32_t(rows * row_bytes);
+    first = smem_addr(smem) + 16u * threadIdx.x;
+    end = first + uint32_t(batches) * batch_bytes;
+    for (uint32_t at = first; at < end; at += uint32_t(plane))
+      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+  }
+  __device__ __forceinline__ uint32_t after(uint32_t batch) const {
+    return batch + batch_bytes == end ? first : batch + batch_bytes;
+  }
+  template <typename T> __device__ __forceinline__ void copy(uint32_t row_at, int planes, const T* src) const {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T)) / 2; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(row_at + uint32_t((planes + i) * plane)),
+                   "l"(reinterpret_cast<const char*>(src) + 16 * i)
+                   : "memory");
+  }
+  template <typename T> __device__ __forceinline__ void get(uint32_t batch, int r, int planes, float2 (&f)[4]) const {
+    Raw8<T> v;
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T)) / 2; ++i)
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v.v[i].x), "=r"(v.v[i].y), "=r"(v.v[i].z), "=r"(v.v[i].w)
+                   : "r"(batch + uint32_t(r * row_bytes + (planes + i) * plane)));
+    unpack8(v, f);
+  }
+  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // Waits until all but the newest `left` batches have landed.
+  __device__ __forceinline__ static void wait(int left) {
+    switch (left) {
+      case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+      case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+      case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+      case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+      case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+      default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    }
+  }
+};
+constexpr int kBnMaxBatches = 6;
+
+// A tensor's rows, as the address of a thread's columns in the next row to be copied or written.
+template <typename T> struct RowPtr {
+  T* at;
+  int64_t step;
+  __device__ __forceinline__ RowPtr(const void* base, int64_t ld, int64_t row, int col)
+      : at(static_cast<T*>(const_cast<void*>(base)) + row * ld + col), step(ld) {}
+  __device__ __forceinline__ T* row(int r) const { return at + r * step; }
+  __device__ __forceinline__ void advance(int rows) { at += rows * step; }
+};
+
+// Sums over the threads of a row, of NV values at once (those of several rows: a sum is all
+// latency, about 500 cycles of shuffles, a barrier and reads, so rows share it). Within a warp
+// the values are spread over the lanes as they are added (NV / 2 + ... + 1 shuffles and one a
+// step after that, instead of five a value). Two scratch buffers take turns, so one barrier a
+// sum is enough: a buffer is written again only after the barrier of the sum between. Words
+// of warps that are not there stay zero.
 struct RowSum {
   float* buf;      // [2][kWords] of this row group
-  float* clus;     // [2][kBnMaxCluster][2] of this block
+  float* clus;     // [2][kBnMaxCluster][4] of this block
   int nw, warp, lane, bar, threads, cluster, turn;
-  static constexpr int kWords = 2 * kBnMaxThreads / 32;
+  static constexpr int kMaxValues = 8;
+  static constexpr int kWords = kMaxValues * kBnMaxThreads / 32;
+
+  // Sums over the warp: value i ends in lanes i * (32 / NV) ... of the result.
+  template <int NV> __device__ __forceinline__ float scatter_sum(const float (&v)[NV]) const {
+    static_assert(NV == 2 || NV == 4 || NV == 8, "values of a sum");
+    float s[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] = v[i];
+    int o = 16;
+#pragma unroll
+    for (int n = NV; n > 1; n /= 2, o /= 2) {
+      const bool high = (lane & o) != 0;
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) {
+        const float give = high ? s[i] : s[i + n / 2], keep = high ? s[i + n / 2] : s[i];
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+#pragma unroll
+    for (int k = 16 / NV; k > 0; k >>= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], k);
+    return s[0];
+  }
 
   template <int NV> __device__ __forceinline__ void sum(float (&v)[NV]) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    const float mine = scatter_sum(v);
     if (nw > 1) {
       float* b = buf + turn * kWords;
-      if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) b[warp * NV + i] = v[i];
-      }
+      if (lane % (32 / NV) == 0) b[warp * NV + lane / (32 / NV)] = mine;
       named_barrier_sync(uint32_t(bar), uint32_t(threads));
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = 0.f;
-      const int n4 = (nw * NV + 3) / 4;
-      for (int w = 0; w < n4; ++w) {
-        const float4 q = reinterpret_cast<const float4*>(b)[w];
-        const int left = nw * NV - 4 * w;  // words past the last warp hold another sum's values
-        if constexpr (NV == 1) {
-          v[0] += (q.x + (left > 1 ? q.y : 0.f)) + ((left > 2 ? q.z : 0.f) + (left > 3 ? q.w : 0.f));
+      if constexpr (NV <= 4) {
+        float2 lo = both(0.f), hi = both(0.f);
+        const int n4 = (nw * NV + 3) / 4;
+#pragma unroll 4
+        for (int w = 0; w < n4; ++w) {
+          const float4 q = reinterpret_cast<const float4*>(b)[w];
+          lo = add2(lo, make_float2(q.x, q.y));
+          hi = add2(hi, make_float2(q.z, q.w));
+        }
+        if constexpr (NV == 2) {
+          v[0] = lo.x + hi.x;
+          v[1] = lo.y + hi.y;
         } else {
-          v[0] += q.x + (left > 2 ? q.z : 0.f);
-          v[1] += q.y + (left > 2 ? q.w : 0.f);
+          v[0] = lo.x;
+          v[1] = lo.y;
+          v[2] = hi.x;
+          v[3] = hi.y;
+        }
+      } else {
+        float2 s2[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+#pragma unroll 4
+        for (int w = 0; w < nw; ++w) {
+          const float4 q = reinterpret_cast<const float4*>(b)[2 * w], u = reinterpret_cast<const float4*>(b)[2 * w + 1];
+          s2[0] = add2(s2[0], make_float2(q.x, q.y));
+          s2[1] = add2(s2[1], make_float2(q.z, q.w));
+          s2[2] = add2(s2[2], make_float2(u.x, u.y));
+          s2[3] = add2(s2[3], make_float2(u.z, u.w));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = s2[i].x;
+          v[2 * i + 1] = s2[i].y;
         }
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * (32 / NV));
     }
-    if (cluster > 1) {
-      float* c = clus + turn * (2 * kBnMaxCluster);
-      const int tid = warp * 32 + lane;
-      if (tid < cluster) {
-        const uint32_t at = map_shared_to_rank(smem_addr(c + cluster_ctarank() * 2), uint32_t(tid));
+    if (cluster > 1)
+      exchange(v);
+    else
+      turn ^= 1;
+  }
+
+  // Of the warps' column sums s and squared distances q from their own means (value i in lanes
+  // i * (32 / NR) ...): the rows' means and the squared distances from those. A warp has 256
+  // columns, but for one that has the row's last `part` ones.
+  template <int NR> __device__ __forceinline__ void merge(float s, float q, float inv_d, float (&mean)[NR], float (&dist)[NR]) {
+    static_assert(2 * NR <= kMaxValues, "values of a sum");
+    float* b = buf + turn * kWords;
+    if (nw > 1) {
+      if (lane % (32 / NR) == 0) reinterpret_cast<float2*>(b)[warp * NR + lane / (32 / NR)] = make_float2(s, q);
+      named_barrier_sync(uint32_t(bar), uint32_t(threads));
 #pragma unroll
-        for (int i = 0; i < NV; ++i) st_shared_cluster_u32(at + 4 * i, __float_as_uint(v[i]));
-      }
-      cluster_sync_all();
+      for (int i = 0; i < NR; ++i) mean[i] = dist[i] = 0.f;
+#pragma unroll 4
+      for (int w = 0; w < nw; ++w)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = 0.f;
-      for (int r = 0; r < cluster; ++r)
+        for (int i = 0; i < NR; i += 2) {
+          const float4 o = reinterpret_cast<const float4*>(b + w * 2 * NR)[i / 2];
+          mean[i] += o.x;
+          mean[i + 1] += o.z;
+        }
+    } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] += c[2 * r + i];
+      for (int i = 0; i < NR; ++i) mean[i] = __shfl_sync(0xffffffffu, s, i * (32 / NR));
     }
+    if (cluster > 1) exchange(mean);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) mean[i] *= inv_d;
+    if (nw > 1) {
+      auto add = [&](int w, float n, float inv_n) {
+#pragma unroll
+        for (int i = 0; i < NR; i += 2) {
+          const float4 o = reinterpret_cast<const float4*>(b + w * 2 * NR)[i / 2];
+          const float a = fmaf(o.x, inv_n, -mean[i]), c = fmaf(o.z, inv_n, -mean[i + 1]);
+          dist[i] += fmaf(n * a, a, o.y);
+          dist[i + 1] += fmaf(n * c, c, o.w);
+        }
+      };
+#pragma unroll 4
+      for (int w = 0; w < full; ++w) add(w, 256.f, 1.f / 256.f);
+      if (part > 0) add(full, float(part), part_inv);
+    } else {
+      // one warp: its mean is the row's
+#pragma unroll
+      for (int i = 0; i < NR; ++i) dist[i] = __shfl_sync(0xffffffffu, q, i * (32 / NR));
+    }
+    if (cluster > 1)
+      exchange(dist);
+    else
+      turn ^= 1;
+  }
+  // Sums over the blocks of the cluster; takes the next scratch buffer.
+  template <int NV> __device__ __forceinline__ void exchange(float (&v)[NV]) {
+    float* c = clus + turn * (kMaxValues * kBnMaxCluster);
+    const int tid = warp * 32 + lane;
+    if (tid < cluster) {
+      const uint32_t at = map_shared_to_rank(smem_addr(c + cluster_ctarank() * kMaxValues), uint32_t(tid));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) st_shared_cluster_u32(at + 4 * i, __float_as_uint(v[i]));
+    }
+    cluster_sync_all();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = 0.f;
+    for (int r = 0; r < cluster; ++r)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] += c[kMaxValues * r + i];
     turn ^= 1;
   }
+  int full, part;  // warps of this block with 256 columns, and the columns of the one after them
+  float part_inv;
 };
 
 struct RowThread {
@@ -90,57 +262,118 @@ __device__ __forceinline__ RowThread row_thread(int threads_per_row, int cluster
 }
 
 __device__ __forceinline__ float activate(float g, int act) {
-  return act == 0 ? g : act == 1 ? 1.f / (1.f + expf(-g)) : tanhf(g);
+  return act == 1 ? 1.f / (1.f + expf(-g)) : tanhf(g);
 }
 // derivative of the activation, from its value
 __device__ __forceinline__ float activate_d(float a, int act) {
   return act == 0 ? 1.f : act == 1 ? a * (1.f - a) : 1.f - a * a;
 }
 
+__device__ __forceinline__ void activate8(float2 (&a)[4], int act) {
+  if (act == 0) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = make_float2(activate(a[i].x, act), activate(a[i].y, act));
+}
+// derivatives of the activation, from its values
+__device__ __forceinline__ void derive8(const float2 (&a)[4], int act, float2 (&da)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) da[i] = make_float2(activate_d(a[i].x, act), activate_d(a[i].y, act));
+}
+
 template <typename TX, typename TR, bool VEC>
-__device__ __forceinline__ void load_gate(const BlockNormParams& p, int64_t grow, int col, float (&a)[8]) {
+__device__ __forceinline__ void load_gate(const BlockNormParams& p, int64_t grow, int col, float2 (&a)[4]) {
   if (p.gate_res_type)
     unpack8(load8<TR, VEC>(static_cast<const TR*>(p.gate) + grow * p.ld_gate, col, p.D), a);
   else
     unpack8(load8<TX, VEC>(static_cast<const TX*>(p.gate) + grow * p.ld_gate, col, p.D), a);
+  activate8(a, p.act);
+}
+
+// Parameters (zero past the row and where there are none), w + off; read once a block.
+template <bool VEC>
+__device__ __forceinline__ void load_weight(const void* w, int dt, float off, int col, int D, float2 (&f)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = activate(a[i], p.act);
-}
-
-__device__ __forceinline__ void load_weight(const void* w, int dt, float off, int col, int D, float (&f)[8]) {
-  load8_any(w, dt, 0, col, D, f);
+  for (int i = 0; i < 4; ++i) f[i] = both(0.f);
+  if (w == nullptr || col >= D) return;
+  if (dt == ELEM_F32)
+    unpack8(load8<float, VEC>(static_cast<const float*>(w), col, D), f);
+  else if (dt == ELEM_BF16)
+    unpack8(load8<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w), col, D), f);
+  else
+    unpack8(load8<__half, VEC>(static_cast<const __half*>(w), col, D), f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = col + i < D ? f[i] + off : 0.f;
+  for (int i = 0; i < 4; ++i)
+    f[i] = make_float2(col + 2 * i < D ? f[i].x + off : 0.f, col + 2 * i + 1 < D ? f[i].y + off : 0.f);
 }
 
-__device__ __forceinline__ float sum8(const float (&v)[8]) {
-  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-}
-
-// mean (0 for the RMS norm) and 1 / sqrt(mean of the squared distances from it + eps); the
-// distances are summed from the values themselves, so a large common offset costs nothing.
-__device__ __forceinline__ void row_stats(const float (&v)[8], int col, int D, bool layer, float eps, float inv_d,
-                                          RowSum& rs, float& mean, float& rstd) {
-  mean = 0.f;
-  if (layer) {
-    float s[1] = {sum8(v)};
-    rs.sum(s);
-    mean = s[0] * inv_d;
+// A parameter in shared memory, for the kernels with more of them than registers: two planes of
+// 16 bytes a thread of a row.
+struct SharedParam {
+  const float4* at;
+  int plane;
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
+    const float4 a = at[0], b = at[plane];
+    f[0] = make_float2(a.x, a.y);
+    f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y);
+    f[3] = make_float2(b.z, b.w);
   }
-  float q[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = v[i] - mean;
-    q[0] += col + i < D ? d * d : 0.f;
+};
+__device__ __forceinline__ SharedParam share_param(char* smem, int index, const RowThread& r, int threads_per_row,
+                                                   const float2 (&f)[4]) {
+  float4* at = reinterpret_cast<float4*>(smem) + 2 * index * threads_per_row + r.t;
+  if (r.group == 0) {
+    at[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    at[threads_per_row] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
   }
-  rs.sum(q);
-  rstd = rsqrtf(q[0] * inv_d + eps);
+  return SharedParam{at, threads_per_row};
 }
 
-__device__ __forceinline__ RowSum row_sum(float* scratch, const RowThread& r, int threads_per_row, int cluster) {
+// Eight values of a thread's own in shared memory (a gate, the sum of its gradient).
+struct OwnParam {
+  float4* at;
+  int plane;
+  __device__ __forceinline__ void get(float2 (&f)[4]) const { SharedParam{at, plane}.get(f); }
+  __device__ __forceinline__ void set(const float2 (&f)[4]) const {
+    at[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    at[plane] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+  }
+};
+
+__device__ __forceinline__ float sum8(const float2 (&v)[4]) {
+  const float2 s = add2(add2(v[0], v[1]), add2(v[2], v[3]));
+  return s.x + s.y;
+}
+__device__ __forceinline__ float dot8(const float2 (&a)[4], const float2 (&b)[4]) {
+  const float2 s = add2(fma2(a[1], b[1], mul2(a[0], b[0])), fma2(a[3], b[3], mul2(a[2], b[2])));
+  return s.x + s.y;
+}
+// Zeros in the columns past the row. VEC: a thread's columns are all in the row or all past it,
+// and what it reads there is zero already, so this is for what a mean was taken from.
+template <bool VEC> __device__ __forceinline__ void cut8(float2 (&v)[4], int col, int D) {
+  if constexpr (VEC) {
+    const float live = col < D ? 1.f : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(live));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(col + 2 * i < D ? v[i].x : 0.f, col + 2 * i + 1 < D ? v[i].y : 0.f);
+  }
+}
+
+// at most kBnMaxThreads / 64 row groups use barriers
+constexpr int kRowSumWords = 2 * RowSum::kMaxValues * kBnMaxCluster + kBnMaxThreads / 64 * 2 * RowSum::kWords;
+
+__device__ __forceinline__ RowSum row_sum(float* scratch, const RowThread& r, int threads_per_row, int cluster, int D) {
   RowSum rs;
+  const int cols = D - (r.col - 8 * r.t), most = 8 * threads_per_row;  // columns from this block's first on
+  rs.full = (cols < 0 ? 0 : cols < most ? cols : most) / 256;
+  rs.part = cols < 0 || cols >= most ? 0 : cols % 256;
+  rs.part_inv = rs.part > 0 ? 1.f / float(rs.part) : 0.f;
   rs.clus = scratch;
-  rs.buf = scratch + 4 * kBnMaxCluster + r.group * 2 * RowSum::kWords;
+  rs.buf = scratch + 2 * RowSum::kMaxValues * kBnMaxCluster + (threads_per_row > 32 ? r.group * 2 * RowSum::kWords : 0);
+  for (int i = int(threadIdx.x); i < kRowSumWords; i += int(blockDim.x)) scratch[i] = 0.f;
+  __syncthreads();
   rs.nw = threads_per_row / 32;
   rs.warp = r.t / 32;
   rs.lane = r.t % 32;
@@ -150,237 +383,695 @@ __device__ __forceinline__ RowSum row_sum(float* scratch, const RowThread& r, in
   rs.turn = 0;
   return rs;
 }
-constexpr int kRowSumWords = 4 * kBnMaxCluster + 8 * 2 * RowSum::kWords;  // at most 8 groups use barriers
 
-template <typename TX, typename TR, bool VEC>
+// Means (0 for the RMS norm) and 1 / sqrt(mean of the squared distances from it + eps) of R
+// rows; get(r, v) gives a row's eight values. A layer norm's warps first take the mean m_w and
+// the squared distances q_w from it over their own n_w columns; then q = sum q_w + n_w (m_w -
+// m)^2, so one sum over the row's warps is enough and a large common offset costs no precision.
+template <int R, bool VEC, bool LAYER, typename F>
+__device__ __forceinline__ void row_stats(F&& get, int col, int D, bool layer, float eps, float inv_d, RowSum& rs,
+                                          float (&mean)[R], float (&rstd)[R]) {
+  if (LAYER && layer) {
+    const float inv_n = rs.warp < rs.full ? 1.f / 256.f : rs.warp == rs.full ? rs.part_inv : 0.f;
+    float v1[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 v[4];
+      get(r, v);
+      v1[r] = sum8(v);
+    }
+    const float s = rs.scatter_sum(v1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 v[4];
+      get(r, v);
+      const float m = __shfl_sync(0xffffffffu, s, r * (32 / R)) * inv_n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = add2(v[i], both(-m));
+      cut8<VEC>(v, col, D);
+      v1[r] = dot8(v, v);
+    }
+    const float q = rs.scatter_sum(v1);
+    rs.merge(s, q, inv_d, mean, rstd);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 v[4];
+      get(r, v);
+      mean[r] = 0.f;
+      rstd[r] = dot8(v, v);
+    }
+    rs.sum(rstd);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) rstd[r] = rsqrtf(rstd[r] * inv_d + eps);
+}
+
+// What a kernel's code has: the norm after the block, a gate, and (FULL) the means of layer norms
+// and biases. A kernel takes what has less at run time.
+template <typename TX, typename TR, bool VEC, int FEAT>
 __global__ void __launch_bounds__(kBnMaxThreads)
-    flce_block_norm_forward_kernel(const BlockNormParams p, int threads_per_row, int cluster) {
+    flce_block_norm_forward_kernel(const __grid_constant__ BlockNormParams p, int threads_per_row, int cluster, int batches, int per) {
+  constexpr int R = kBnRows;
+  constexpr bool POST = (FEAT & BN_POST) != 0, GATE = (FEAT & BN_GATE) != 0, FULL = (FEAT & BN_FULL) != 0;
   __shared__ __align__(16) float scratch[kRowSumWords];
-  const RowThread r = row_thread(threads_per_row, cluster);
-  RowSum rs = row_sum(scratch, r, threads_per_row, cluster);
+  extern __shared__ __align__(16) char ring_smem[];
+  constexpr int kX = 0, kR = sizeof(TX) / 2, kG = kR + sizeof(TR) / 2;  // planes of x, residual and full gate
+  constexpr int kParams = bn_shared_params(FEAT, false);
+  const RowThread r0 = row_thread(threads_per_row, cluster);
+  RowSum rs = row_sum(scratch, r0, threads_per_row, cluster, p.D);
+  const int col = r0.col, D = p.D;
+  const bool live = col < D;  // VEC: else a thread past the row, whose values are zero
+  const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
+  const bool gate_full = gate && p.gate_full;
+  const int lo = int(r0.worker * p.chunk_rows < p.N ? r0.worker * p.chunk_rows : p.N);
+  const int hi = int(lo + p.chunk_rows < p.N ? lo + p.chunk_rows : p.N);
+  RowRing ring{};
+  RowPtr<TX> src_x(p.x, p.ld_x, lo, col), src_gx(p.gate, p.ld_gate, lo, col);
+  RowPtr<TR> src_r(p.residual, p.ld_residual, lo, col), src_gr(p.gate, p.ld_gate, lo, col);
+  int next = lo;  // the row that is copied next
+  auto fetch = [&](uint32_t at) FLCE_INLINE {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (live && r < per && next + r < hi) {
+        const uint32_t row_at = at + uint32_t(r * ring.row_bytes);
+        ring.copy(row_at, kX, src_x.row(r));
+        if (p.residual != nullptr) ring.copy(row_at, kR, src_r.row(r));
+        if (gate_full) {
+          if (p.gate_res_type)
+            ring.copy(row_at, kG, src_gr.row(r));
+          else
+            ring.copy(row_at, kG, src_gx.row(r));
+        }
+      }
+    }
+    src_x.advance(per);
+    src_r.advance(per);
+    if (GATE) {
+      src_gx.advance(per);
+      src_gr.advance(per);
+    }
+    next += per;
+    ring.commit();
+  };
+  if constexpr (VEC) {
+    ring.init(ring_smem + (FULL ? kParams * 32 * threads_per_row : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
+    for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
+  }
   if (cluster > 1) cluster_sync_all();
-  const int col = r.col, D = p.D;
-  const bool post = p.w1 != nullptr, pre = p.w2 != nullptr;
-  float w1[8], b1[8], w2[8], b2[8], a[8];
-  load_weight(p.w1, p.w1_dt, p.w_off, col, D, w1);
-  load8_any(p.b1, p.b1_dt, 0, col, D, b1);
-  load_weight(p.w2, p.w2_dt, p.w_off, col, D, w2);
-  load8_any(p.b2, p.b2_dt, 0, col, D, b2);
+  // c: what a row's value after the first norm is multiplied by, w1 scale act(gate), and c_b what
+  // is added, b1 scale act(gate)
+  float2 w2[4], c[4], c_b[4];
+  SharedParam s_w1{}, s_b1{}, s_w2{}, s_b2{};
+  load_weight<VEC>(p.w1, p.w1_dt, p.w_off, col, D, c);
+  load_weight<VEC>(p.w2, p.w2_dt, p.w_off, col, D, w2);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = 1.f;
+  for (int i = 0; i < 4; ++i) c[i] = post ? mul2(c[i], both(p.scale)) : both(p.scale);
+  if (FULL) {
+    load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, c_b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c_b[i] = mul2(c_b[i], both(p.scale));
+    float2 b2[4];
+    load_weight<VEC>(p.b2, p.b2_dt, 0.f, col, D, b2);
+    s_w2 = share_param(ring_smem, 0, r0, threads_per_row, w2);
+    s_b2 = share_param(ring_smem, 1, r0, threads_per_row, b2);
+    if (GATE) {
+      s_w1 = share_param(ring_smem, 2, r0, threads_per_row, c);
+      s_b1 = share_param(ring_smem, 3, r0, threads_per_row, c_b);
+    }
+    __syncthreads();
+  }
+  float2 w1[4];
+  if (GATE && !FULL) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w1[i] = c[i];
+  }
+  auto set_gate = [&](const float2(&a)[4]) FLCE_INLINE {
+    if (FULL) {
+      s_w1.get(c);
+      s_b1.get(c_b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = mul2(c[i], a[i]);
+        c_b[i] = mul2(c_b[i], a[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = mul2(w1[i], a[i]);
+    }
+  };
   const float inv_d = 1.f / float(D);
-  const int64_t lo = r.worker * p.chunk_rows;
-  const int64_t hi = lo + p.chunk_rows < p.N ? lo + p.chunk_rows : p.N;
-  int64_t gate_end = lo;  // first row whose gate is not in a[]
-  for (int64_t row = lo; row < hi; ++row) {
-    const Raw8<TX> rx = load8<TX, VEC>(static_cast<const TX*>(p.x) + row * p.ld_x, col, D);
-    Raw8<TR> rr = raw_zero<TR>();
-    if (p.residual != nullptr) rr = load8<TR, VEC>(static_cast<const TR*>(p.residual) + row * p.ld_residual, col, D);
-    if (p.gate != nullptr && row >= gate_end) {
-      const int64_t g = row / p.gate_group;
-      load_gate<TX, TR, VEC>(p, g, col, a);
-      gate_end = (g + 1) * p.gate_group;
-    }
-    float u[8], h[8];
-    unpack8(rx, u);
-    unpack8(rr, h);
-    float m1 = 0.f, r1 = 0.f, m2 = 0.f, r2 = 0.f;
-    if (post) {
-      row_stats(u, col, D, p.layer, p.eps, inv_d, rs, m1, r1);
+  int gate_end = lo;  // first row whose gate is not in c
+  RowPtr<TR> out_h(p.h, D, lo, col);
+  RowPtr<TX> out_y(p.y, D, lo, col);
+  // The first norm of a batch and the second norm of the batch before it share a sum: the
+  // latency of a batch is one sum, and what comes before and after it is independent work.
+  uint32_t batch = ring.first;
+  auto get_x = [&](uint32_t at, int first, int r, float2 (&v)[4]) FLCE_INLINE {
+    if constexpr (VEC)
+      ring.get<TX>(at, r, kX, v);
+    else
+      unpack8(r < per && first + r < hi ? load8<TX, VEC>(static_cast<const TX*>(p.x) + (first + r) * p.ld_x, col, D) : raw_zero<TX>(), v);
+  };
+  float m1[R], r1[R];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = (u[i] - m1) * r1 * w1[i] + b1[i];
-    }
+  for (int r = 0; r < R; ++r) m1[r] = 0.f, r1[r] = 1.f;
+  if (lo < hi) {
+    if constexpr (VEC) ring.wait(batches - 1);
+    if (post) row_stats<R, VEC, FULL>([&](int r, float2 (&v)[4]) { get_x(batch, lo, r, v); }, col, D, p.layer, p.eps, inv_d, rs, m1, r1);
+  }
+  for (int row = lo; row < hi; row += per) {
+    const bool second = per > 1 && row + 1 < hi;  // the last batch may have one row
+    float2 h[R][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] += p.scale * (a[i] * u[i]);
-    store8<TR, VEC>(static_cast<TR*>(p.h) + row * D, col, D, h);
+    for (int r = 0; r < R; ++r) {
+      if (r > 0 && !second) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[r][i] = both(0.f);
+        continue;
+      }
+      if (gate_full) {
+        float2 a[4];
+        if constexpr (VEC) {
+          if (p.gate_res_type)
+            ring.get<TR>(batch, r, kG, a);
+          else
+            ring.get<TX>(batch, r, kG, a);
+          activate8(a, p.act);
+        } else {
+          load_gate<TX, TR, VEC>(p, row + r, col, a);
+        }
+        set_gate(a);
+      } else if (gate && row + r >= gate_end) {
+        const int g = (row + r) / int(p.gate_group);
+        float2 a[4];
+        load_gate<TX, TR, VEC>(p, g, col, a);
+        set_gate(a);
+        gate_end = int((g + 1) * p.gate_group);
+      }
+      float2 u[4];
+      get_x(batch, row, r, u);
+      if constexpr (VEC) {
+        ring.get<TR>(batch, r, kR, h[r]);
+      } else {
+        unpack8(p.residual == nullptr ? raw_zero<TR>() : load8<TR, VEC>(static_cast<const TR*>(p.residual) + (row + r) * p.ld_residual, col, D), h[r]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (FULL) {
+          u[i] = mul2(add2(u[i], both(-m1[r])), both(r1[r]));
+          h[r][i] = add2(h[r][i], fma2(u[i], c[i], c_b[i]));
+        } else {
+          if (POST) u[i] = mul2(u[i], both(r1[r]));
+          h[r][i] = fma2(u[i], c[i], h[r][i]);
+        }
+      }
+      store8_at<TR, VEC>(out_h.row(r), col, D, h[r]);
+    }
+    out_h.advance(per);
+    float m2[R], r2[R], n1[R], k1[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) m2[r] = r2[r] = n1[r] = 0.f, k1[r] = 1.f;
+    if constexpr (VEC) {
+      fetch(batch);
+      batch = ring.after(batch);
+      ring.wait(batches - 1);
+    }
+    auto get_h = [&](int r, float2 (&v)[4]) FLCE_INLINE {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = h[r][i];
+    };
+    const int after = row + per;
+    if (post && pre) {
+      float mean[2 * R], rstd[2 * R];
+      row_stats<2 * R, VEC, FULL>(
+          [&](int r, float2 (&v)[4]) {
+            if (r < R)
+              get_h(r, v);
+            else
+              get_x(batch, after, r - R, v);
+          },
+          col, D, p.layer, p.eps, inv_d, rs, mean, rstd);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        m2[r] = mean[r];
+        r2[r] = rstd[r];
+        n1[r] = mean[R + r];
+        k1[r] = rstd[R + r];
+      }
+    } else if (pre) {
+      row_stats<R, VEC, FULL>(get_h, col, D, p.layer, p.eps, inv_d, rs, m2, r2);
+    } else if (post) {
+      row_stats<R, VEC, FULL>([&](int r, float2 (&v)[4]) { get_x(batch, after, r, v); }, col, D, p.layer, p.eps, inv_d, rs, n1, k1);
+    }
     if (pre) {
-      row_stats(h, col, D, p.layer, p.eps, inv_d, rs, m2, r2);
+      float2 b2[4];
+      if (FULL) {
+        s_w2.get(w2);
+        s_b2.get(b2);
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = (h[i] - m2) * r2 * w2[i] + b2[i];
-      store8<TX, VEC>(static_cast<TX*>(p.y) + row * D, col, D, h);
+      for (int r = 0; r < R; ++r) {
+        if (r > 0 && !second) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (FULL)
+            h[r][i] = fma2(mul2(add2(h[r][i], both(-m2[r])), both(r2[r])), w2[i], b2[i]);
+          else
+            h[r][i] = mul2(mul2(h[r][i], both(r2[r])), w2[i]);
+        }
+        store8_at<TX, VEC>(out_y.row(r), col, D, h[r]);
+      }
+      out_y.advance(per);
     }
     if (p.stats != nullptr && col == 0) {
-      p.stats[row] = m1;
-      p.stats[p.N + row] = r1;
-      p.stats[2 * p.N + row] = m2;
-      p.stats[3 * p.N + row] = r2;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r == 0 || second) reinterpret_cast<float4*>(p.stats)[row + r] = make_float4(m1[r], r1[r], m2[r], r2[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m1[r] = n1[r];
+      r1[r] = k1[r];
     }
   }
   if (cluster > 1) cluster_sync_all();  // no block leaves while another may still write to it
 }
 
+// With n = (v - m) r and g = upstream * w, a norm's gradient is r (g - mean(g) - n mean(g n)) =
+// r g - r mean(g) - (v - m) r^3 mean(g (v - m)): it is computed in the last form, from the row's
+// own values, so a norm costs two sums in which no normalised row is formed.
 template <typename TX, typename TR, bool VEC, int FEAT>
 __global__ void __launch_bounds__(kBnMaxThreads)
-    flce_block_norm_backward_kernel(const BlockNormParams p, int threads_per_row, int cluster) {
-  constexpr bool POST = (FEAT & BN_POST) != 0, GATE = (FEAT & BN_GATE) != 0, BIAS = (FEAT & BN_BIAS) != 0;
+    flce_block_norm_backward_kernel(const __grid_constant__ BlockNormParams p, int threads_per_row, int cluster, int batches, int per) {
+  constexpr int R = kBnRows;
+  constexpr bool POST = (FEAT & BN_POST) != 0, GATE = (FEAT & BN_GATE) != 0, FULL = (FEAT & BN_FULL) != 0;
   __shared__ __align__(16) float scratch[kRowSumWords];
-  extern __shared__ float fold[];  // [threads][8] when a block has several row groups
-  const RowThread r = row_thread(threads_per_row, cluster);
-  RowSum rs = row_sum(scratch, r, threads_per_row, cluster);
-  if (cluster > 1) cluster_sync_all();
-  const int col = r.col, D = p.D;
+  extern __shared__ __align__(16) char ring_smem[];
+  constexpr int kX = 0, kY = sizeof(TX) / 2, kH = 2 * kY, kDh = kH + sizeof(TR) / 2, kG = kDh + sizeof(TR) / 2;  // planes
+  constexpr int kParams = bn_shared_params(FEAT, true);
+  constexpr bool OWN = POST && GATE;  // the gate and the sum of its gradient are in shared memory
+  const RowThread r0 = row_thread(threads_per_row, cluster);
+  RowSum rs = row_sum(scratch, r0, threads_per_row, cluster, p.D);
+  const int col = r0.col, D = p.D;
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
-  float w1[8], w2[8], b1[8], a[8], dw1[8], db1[8], dw2[8], db2[8], dg[8];
-  load_weight(p.w1, p.w1_dt, p.w_off, col, D, w1);
-  load_weight(p.w2, p.w2_dt, p.w_off, col, D, w2);
-  load8_any(p.b1, p.b1_dt, 0, col, D, b1);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    a[i] = 1.f;
-    dw1[i] = db1[i] = dw2[i] = db2[i] = dg[i] = 0.f;
-  }
-  const float inv_d = 1.f / float(D), inv_d0 = p.layer ? inv_d : 0.f;
-  const int64_t workers = int64_t(int(gridDim.x) / cluster) * (int(blockDim.x) / threads_per_row);
-  for (int64_t chunk = r.worker; chunk < p.chunks; chunk += workers) {
-    const int64_t g = chunk / p.chunks_per_group, first = g * p.group_rows;
-    const int64_t lo = first + (chunk - g * p.chunks_per_group) * p.chunk_rows;
-    const int64_t end = first + p.group_rows;
-    const int64_t hi = lo + p.chunk_rows < end ? lo + p.chunk_rows : end;
-    if (gate && !p.gate_full) load_gate<TX, TR, VEC>(p, g, col, a);
-    for (int64_t row = lo; row < hi; ++row) {
-      const Raw8<TX> rx = load8<TX, VEC>(static_cast<const TX*>(p.x) + row * p.ld_x, col, D);
-      Raw8<TR> rh = raw_zero<TR>(), rdh = raw_zero<TR>();
-      Raw8<TX> rdy = raw_zero<TX>();
-      if (pre) rh = load8<TR, VEC>(static_cast<const TR*>(p.h_in) + row * D, col, D);
-      if (p.dh != nullptr) rdh = load8<TR, VEC>(static_cast<const TR*>(p.dh) + row * p.ld_dh, col, D);
-      if (pre && p.dy != nullptr) rdy = load8<TX, VEC>(static_cast<const TX*>(p.dy) + row * p.ld_dy, col, D);
-      if (gate && p.gate_full) load_gate<TX, TR, VEC>(p, row, col, a);
-      float x[8], d[8];  // d: the gradient of h, then of u
-      unpack8(rx, x);
-      unpack8(rdh, d);
-      if (pre) {
-        const float m2 = p.stats[2 * p.N + row], r2 = p.stats[3 * p.N + row];
-        float n[8], dy[8];
-        unpack8(rh, n);
-        unpack8(rdy, dy);
-        float s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          n[i] = (n[i] - m2) * r2;
-          dw2[i] += dy[i] * n[i];
-          if (BIAS) db2[i] += dy[i];
-          dy[i] *= w2[i];
-          s[0] += dy[i] * n[i];
-          s[1] += dy[i];
-        }
-        if (p.layer) {
-          rs.sum(s);
-        } else {
-          float one[1] = {s[0]};
-          rs.sum(one);
-          s[0] = one[0];
-        }
-        const float c0 = s[1] * inv_d0, c1 = s[0] * inv_d;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] += r2 * (dy[i] - c0 - n[i] * c1);
+  const bool gate_full = gate && p.gate_full;
+  const int workers = int(gridDim.x) / cluster * (int(blockDim.x) / threads_per_row);
+  const bool live_col = col < D;
+  // the worker's rows: chunk after chunk, once for the copies and once, behind them, for the work
+  struct Rows {
+    int chunk, group, row, hi;
+  };
+  auto open = [&](Rows& w) FLCE_INLINE {
+    if (w.chunk >= p.chunks) return;
+    w.group = w.chunk / int(p.chunks_per_group);
+    const int first = w.group * int(p.group_rows), end = first + int(p.group_rows);
+    w.row = first + (w.chunk - w.group * int(p.chunks_per_group)) * int(p.chunk_rows);
+    w.hi = end - w.row < int(p.chunk_rows) ? end : w.row + int(p.chunk_rows);
+  };
+  RowRing ring{};
+  Rows ahead{int(r0.worker), 0, 0, 0};
+  open(ahead);
+  RowPtr<TX> src_x(p.x, p.ld_x, ahead.row, col), src_dy(p.dy, p.ld_dy, ahead.row, col);
+  RowPtr<TR> src_h(p.h_in, D, ahead.row, col), src_dh(p.dh, p.ld_dh, ahead.row, col);
+  // a batch's statistics: copied by the first lanes of each warp for the warp alone
+  __shared__ __align__(16) float4 warp_stats[kBnMaxThreads / 32][kBnMaxBatches][R];
+  const float4* stats = reinterpret_cast<const float4*>(p.stats);
+  const uint32_t stat_at = smem_addr(&warp_stats[threadIdx.x / 32][0][0]);
+  int stat_slot = 0;
+  auto fetch = [&](uint32_t at) FLCE_INLINE {
+    if (ahead.chunk < p.chunks) {
+      if (rs.lane < R) {  // the rows' statistics, for this warp
+        const int row = ahead.row + (rs.lane < per && ahead.row + rs.lane < ahead.hi ? rs.lane : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(stat_at + uint32_t(stat_slot * R + rs.lane) * 16u),
+                     "l"(stats + row)
+                     : "memory");
       }
+      if (live_col) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i >= D) d[i] = 0.f;
-      if (p.dres != nullptr) store8<TR, VEC>(static_cast<TR*>(p.dres) + row * D, col, D, d);
-      float m1 = 0.f, r1 = 1.f;
-      if (post) {
-        m1 = p.stats[row];
-        r1 = p.stats[p.N + row];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (x[i] - m1) * r1;
-      }
-      if (gate) {
-        float e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          e[i] = d[i] * (post ? x[i] * w1[i] + b1[i] : x[i]);
-          d[i] *= p.scale * a[i];
-        }
-        if (p.gate_full) {
-          if (p.dgate != nullptr) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] *= p.scale * activate_d(a[i], p.act);
+        for (int r = 0; r < R; ++r) {
+          if (r > 0 && (r >= per || ahead.row + r >= ahead.hi)) continue;
+          const uint32_t row_at = at + uint32_t(r * ring.row_bytes);
+          ring.copy(row_at, kX, src_x.row(r));
+          if (pre) ring.copy(row_at, kH, src_h.row(r));
+          if (p.dh != nullptr) ring.copy(row_at, kDh, src_dh.row(r));
+          if (pre && p.dy != nullptr) ring.copy(row_at, kY, src_dy.row(r));
+          if (gate_full) {
             if (p.gate_res_type)
-              store8<TR, VEC>(static_cast<TR*>(p.dgate) + row * D, col, D, e);
+              ring.copy(row_at, kG, static_cast<const TR*>(p.gate) + (ahead.row + r) * p.ld_gate + col);
             else
-              store8<TX, VEC>(static_cast<TX*>(p.dgate) + row * D, col, D, e);
+              ring.copy(row_at, kG, static_cast<const TX*>(p.gate) + (ahead.row + r) * p.ld_gate + col);
+          }
+        }
+      }
+      ahead.row += per;
+      src_x.advance(per);
+      src_h.advance(per);
+      src_dh.advance(per);
+      src_dy.advance(per);
+      if (ahead.row >= ahead.hi) {
+        ahead.chunk += workers;
+        open(ahead);
+        src_x = RowPtr<TX>(p.x, p.ld_x, ahead.row, col);
+        src_dy = RowPtr<TX>(p.dy, p.ld_dy, ahead.row, col);
+        src_h = RowPtr<TR>(p.h_in, D, ahead.row, col);
+        src_dh = RowPtr<TR>(p.dh, p.ld_dh, ahead.row, col);
+      }
+    }
+    ring.commit();
+    stat_slot = stat_slot + 1 == batches ? 0 : stat_slot + 1;
+  };
+  if constexpr (VEC) {
+    ring.init(ring_smem + kParams * 32 * threads_per_row + (OWN && !gate_full ? 64 * int(blockDim.x) : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
+    for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
+  }
+  if (cluster > 1) cluster_sync_all();
+  float2 w1[4], w2[4], b1[4], a[4], dw1[4], db1[4], dw2[4], db2[4], dg[4];
+  SharedParam s_w1{}, s_w2{}, s_b1{};
+  load_weight<VEC>(p.w2, p.w2_dt, p.w_off, col, D, w2);
+  if (POST) load_weight<VEC>(p.w1, p.w1_dt, p.w_off, col, D, w1);
+  if (GATE && FULL) load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, b1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = both(1.f);
+    if (!post) w1[i] = both(1.f);
+    dw1[i] = db1[i] = dw2[i] = db2[i] = dg[i] = both(0.f);
+  }
+  if (FULL) {
+    s_w2 = share_param(ring_smem, 0, r0, threads_per_row, w2);
+    if (POST) s_w1 = share_param(ring_smem, 1, r0, threads_per_row, w1);
+    if (POST && GATE) s_b1 = share_param(ring_smem, 2, r0, threads_per_row, b1);
+    __syncthreads();
+  }
+  const int own_plane = int(blockDim.x);
+  float4* own = reinterpret_cast<float4*>(ring_smem + kParams * 32 * threads_per_row) + threadIdx.x;
+  const OwnParam own_a{own, own_plane}, own_dg{own + 2 * own_plane, own_plane};
+  if (OWN && gate && !gate_full) own_dg.set(dg);
+  const float inv_d = 1.f / float(D), inv_d0 = p.layer ? inv_d : 0.f;
+  const float live = live_col ? 1.f : 0.f;  // threads past the row: their values stay zero
+  // values of a row of the batch in slot `at`, whose first row is `first`
+  auto get_x = [&](uint32_t at, int first, int r, float m1, float2 (&v)[4]) FLCE_INLINE {
+    if constexpr (VEC) ring.get<TX>(at, r, kX, v);
+    else unpack8(load8<TX, VEC>(static_cast<const TX*>(p.x) + (first + r) * p.ld_x, col, D), v);
+    if (FULL && POST) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = add2(v[i], both(-m1));
+    }
+  };
+  auto get_h = [&](uint32_t at, int first, int r, float m2, float2 (&v)[4]) FLCE_INLINE {
+    if constexpr (VEC) ring.get<TR>(at, r, kH, v);
+    else unpack8(load8<TR, VEC>(static_cast<const TR*>(p.h_in) + int64_t(first + r) * D, col, D), v);
+    if (FULL) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = add2(v[i], both(-m2));
+    }
+  };
+  auto get_dy = [&](uint32_t at, int first, int r, float2 (&v)[4]) FLCE_INLINE {
+    if constexpr (VEC) ring.get<TX>(at, r, kY, v);
+    else unpack8(p.dy == nullptr ? raw_zero<TX>() : load8<TX, VEC>(static_cast<const TX*>(p.dy) + (first + r) * p.ld_dy, col, D), v);
+  };
+  auto get_dh = [&](uint32_t at, int first, int r, float2 (&v)[4]) FLCE_INLINE {
+    if constexpr (VEC) ring.get<TR>(at, r, kDh, v);
+    else unpack8(p.dh == nullptr ? raw_zero<TR>() : load8<TR, VEC>(static_cast<const TR*>(p.dh) + (first + r) * p.ld_dh, col, D), v);
+  };
+  auto get_stats = [&](int slot, int first, int r) FLCE_INLINE {
+    float4 s = VEC ? warp_stats[threadIdx.x / 32][slot][r] : stats[first + r];
+    s.y = post ? s.y * live : live;
+    s.w *= live;
+    return s;
+  };
+  auto step = [&](Rows& w) FLCE_INLINE {
+    w.row += per;
+    if (w.row >= w.hi) {
+      w.chunk += workers;
+      open(w);
+    }
+  };
+  // Sums of the second norm's gradient over the batch's rows: s1 of g (h - mean), s0 of g.
+  auto second_norm = [&](uint32_t at, int slot, const Rows& w, float (&s1)[R], float (&s0)[R]) FLCE_INLINE {
+    if (FULL) s_w2.get(w2);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s1[r] = s0[r] = 0.f;
+      if (r > 0 && (r >= per || w.row + r >= w.hi)) continue;
+      const float4 st = get_stats(slot, w.row, r);
+      float2 n[4], g[4];
+      get_h(at, w.row, r, st.z, n);
+      get_dy(at, w.row, r, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], w2[i]);
+      s1[r] = dot8(g, n);
+      if (FULL) s0[r] = sum8(g);
+    }
+  };
+  // A batch's sums of the first norm and the next batch's sums of the second share a sum over
+  // the row's threads, so a batch costs the latency of one.
+  auto total = [&](float (&t1)[R], float (&t0)[R], float (&s1)[R], float (&s0)[R]) FLCE_INLINE {
+    constexpr int kOf = POST ? 2 : 1;
+    float v[kOf * R * (FULL ? 2 : 1)];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      v[r] = s1[r];
+      if (POST) v[R + r] = t1[r];
+      if (FULL) v[kOf * R + r] = s0[r];
+      if (FULL && POST) v[kOf * R + R + r] = t0[r];
+    }
+    rs.sum(v);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s1[r] = v[r];
+      if (POST) t1[r] = v[R + r];
+      if (FULL) s0[r] = v[kOf * R + r];
+      if (FULL && POST) t0[r] = v[kOf * R + R + r];
+    }
+  };
+  Rows now{int(r0.worker), 0, 0, 0};
+  open(now);
+  uint32_t batch = ring.first;
+  int slot = 0, open_chunk = -1;
+  float s1[R], s0[R], t1[R], t0[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) s1[r] = s0[r] = t1[r] = t0[r] = 0.f;
+  if (now.chunk < p.chunks && pre) {
+    if constexpr (VEC) {
+      ring.wait(batches - 1);
+      __syncwarp();
+    }
+    second_norm(batch, slot, now, s1, s0);
+    total(t1, t0, s1, s0);
+  }
+  while (now.chunk < p.chunks) {
+    const int row = now.row;
+    const bool second = per > 1 && row + 1 < now.hi;  // a chunk's last batch may have one row
+    Rows next = now;
+    step(next);
+    if (!pre && VEC) {
+      ring.wait(batches - 1);
+      __syncwarp();
+    }
+    if (gate && !gate_full && now.chunk != open_chunk) {
+      load_gate<TX, TR, VEC>(p, now.group, col, a);
+      if (OWN) own_a.set(a);
+    }
+    open_chunk = now.chunk;
+    float2 d[R][4];  // the gradient of h, then what the first norm's gradient is taken of
+    if (FULL && POST) s_w1.get(w1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      t1[r] = t0[r] = 0.f;
+      if (r > 0 && !second) continue;
+      const float4 st = get_stats(slot, row, r);
+      get_dh(batch, row, r, d[r]);
+      if (pre) {
+        float2 n[4], g[4];
+        get_h(batch, row, r, st.z, n);
+        get_dy(batch, row, r, g);
+        if (FULL) s_w2.get(w2);
+        const float2 k1 = both(-(s1[r] * st.w * inv_d) * st.w * st.w), k0 = both(-st.w * (s0[r] * inv_d0)), k = both(st.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (FULL) db2[i] = add2(db2[i], g[i]);
+          d[r][i] = fma2(n[i], k1, d[r][i]);
+          if (FULL) d[r][i] = add2(d[r][i], k0);
+          g[i] = mul2(g[i], k);
+          d[r][i] = fma2(g[i], w2[i], d[r][i]);
+          dw2[i] = fma2(g[i], n[i], dw2[i]);
+        }
+        if (!VEC && FULL) cut8<VEC>(d[r], col, D);
+      }
+      if (p.dres != nullptr) store8_at<TR, VEC>(static_cast<TR*>(p.dres) + int64_t(row + r) * D + col, col, D, d[r]);
+      float2 x[4];
+      if (POST || GATE) get_x(batch, row, r, st.x, x);
+      if (gate) {
+        if (gate_full) {
+          if constexpr (VEC) {
+            if (p.gate_res_type)
+              ring.get<TR>(batch, r, kG, a);
+            else
+              ring.get<TX>(batch, r, kG, a);
+            activate8(a, p.act);
+          } else {
+            load_gate<TX, TR, VEC>(p, row + r, col, a);
+          }
+        } else if (OWN) {
+          own_a.get(a);
+        }
+        // d u, without the scale: u = (x - m) r w1 + b1, or x
+        float2 e[4];
+        if (FULL && POST) s_b1.get(b1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = x[i];
+          if (POST) {
+            e[i] = mul2(mul2(e[i], both(st.y)), w1[i]);
+            if (FULL && post) e[i] = add2(e[i], b1[i]);
+          }
+          e[i] = mul2(e[i], d[r][i]);
+        }
+        if (gate_full) {
+          if (p.dgate != nullptr) {
+            float2 da[4];
+            derive8(a, p.act, da);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = mul2(e[i], mul2(da[i], both(p.scale)));
+            if (p.gate_res_type)
+              store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(row + r) * D, col, D, e);
+            else
+              store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(row + r) * D, col, D, e);
+          }
+        } else {
+          if (OWN) own_dg.get(dg);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dg[i] = add2(dg[i], e[i]);
+          if (OWN) own_dg.set(dg);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[r][i] = mul2(d[r][i], a[i]);
+      }
+      if (post) {
+        const float2 k = both(st.y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dw1[i] = fma2(mul2(d[r][i], k), x[i], dw1[i]);
+          if (FULL) db1[i] = add2(db1[i], d[r][i]);
+          d[r][i] = mul2(d[r][i], w1[i]);
+        }
+        t1[r] = dot8(d[r], x);
+        if (FULL) t0[r] = sum8(d[r]);
+      }
+    }
+    const uint32_t batch_next = ring.after(batch);
+    const int slot_next = slot + 1 == batches ? 0 : slot + 1;
+    if (pre && next.chunk < p.chunks) {
+      if constexpr (VEC) {
+        ring.wait(batches - 2);
+        __syncwarp();
+      }
+      second_norm(batch_next, slot_next, next, s1, s0);
+    }
+    if (pre || post) total(t1, t0, s1, s0);
+    if (p.dx != nullptr) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r > 0 && !second) continue;
+        if (post) {
+          const float4 st = get_stats(slot, row, r);
+          float2 x[4];
+          get_x(batch, row, r, st.x, x);
+          const float s = st.y * p.scale;
+          const float2 k1 = both(-(t1[r] * st.y * inv_d) * st.y * s), k0 = both(-s * (t0[r] * inv_d0)), k = both(s);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (FULL)
+              d[r][i] = fma2(d[r][i], k, fma2(x[i], k1, k0));
+            else
+              d[r][i] = fma2(d[r][i], k, mul2(x[i], k1));
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dg[i] += e[i];
+          for (int i = 0; i < 4; ++i) d[r][i] = mul2(d[r][i], both(p.scale));
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] *= p.scale;
+        store8_at<TX, VEC>(static_cast<TX*>(p.dx) + int64_t(row + r) * D + col, col, D, d[r]);
       }
-      if (post) {
-        float s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dw1[i] += d[i] * x[i];
-          if (BIAS) db1[i] += d[i];
-          d[i] *= w1[i];
-          s[0] += d[i] * x[i];
-          s[1] += d[i];
-        }
-        if (p.layer) {
-          rs.sum(s);
-        } else {
-          float one[1] = {s[0]};
-          rs.sum(one);
-          s[0] = one[0];
-        }
-        const float c0 = s[1] * inv_d0, c1 = s[0] * inv_d;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = r1 * (d[i] - c0 - x[i] * c1);
-      }
-      if (p.dx != nullptr) store8<TX, VEC>(static_cast<TX*>(p.dx) + row * D, col, D, d);
     }
-    if (gate && !p.gate_full && p.dgate != nullptr) {
+    if constexpr (VEC) {
+      __syncwarp();  // the warp has read the batch's statistics
+      fetch(batch);
+    }
+    if (gate && !gate_full && p.dgate != nullptr && next.chunk != now.chunk) {
+      float2 da[4];
+      if (OWN) {
+        own_a.get(a);
+        own_dg.get(dg);
+      }
+      derive8(a, p.act, da);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dg[i] *= p.scale * activate_d(a[i], p.act);
+      for (int i = 0; i < 4; ++i) dg[i] = mul2(dg[i], mul2(da[i], both(p.scale)));
       if (p.part_gate != nullptr)
-        store8<float, VEC>(p.part_gate + chunk * D, col, D, dg);
+        store8<float, VEC>(p.part_gate + int64_t(now.chunk) * D, col, D, dg);
       else if (p.gate_res_type)
-        store8<TR, VEC>(static_cast<TR*>(p.dgate) + g * D, col, D, dg);
+        store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(now.group) * D, col, D, dg);
       else
-        store8<TX, VEC>(static_cast<TX*>(p.dgate) + g * D, col, D, dg);
+        store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(now.group) * D, col, D, dg);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dg[i] = 0.f;
+      for (int i = 0; i < 4; ++i) dg[i] = both(0.f);
+      if (OWN) own_dg.set(dg);
     }
+    batch = batch_next;
+    slot = slot_next;
+    now = next;
   }
   // one partial sum a block and parameter: the block's row groups first
   const int groups = int(blockDim.x) / threads_per_row;
   const int64_t block = int64_t(int(blockIdx.x) / cluster);
-  auto flush = [&](float* part, const float(&v)[8]) {
+  // every copy has been waited for but the empty ones past the last row: the room is free
+  float2* fold = reinterpret_cast<float2*>(ring_smem);  // [threads][4]
+  auto flush = [&](float* part, const float2(&v)[4], float scale) FLCE_INLINE {
     if (part == nullptr) return;
-    if (groups == 1) {
-      store8<float, VEC>(part + block * D, col, D, v);
-      return;
+    float2 s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = v[i];
+    if (groups > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fold[threadIdx.x * 4 + i] = v[i];
+      __syncthreads();
+      if (r0.group != 0) return;
+      for (int q = 1; q < groups; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = add2(s[i], fold[(q * threads_per_row + r0.t) * 4 + i]);
     }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) fold[threadIdx.x * 8 + i] = v[i];
-    __syncthreads();
-    if (r.group == 0) {
-      float s[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = 0.f;
-      for (int q = 0; q < groups; ++q)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] += fold[(q * threads_per_row + r.t) * 8 + i];
-      store8<float, VEC>(part + block * D, col, D, s);
-    }
+    for (int i = 0; i < 4; ++i) s[i] = mul2(s[i], both(scale));
+    store8<float, VEC>(part + block * D, col, D, s);
   };
-  if (POST) flush(p.part[0], dw1);
-  if (POST && BIAS) flush(p.part[1], db1);
-  flush(p.part[2], dw2);
-  if (BIAS) flush(p.part[3], db2);
+  if (POST) flush(p.part[0], dw1, p.scale);
+  if (POST && FULL) flush(p.part[1], db1, p.scale);
+  flush(p.part[2], dw2, 1.f);
+  if (FULL) flush(p.part[3], db2, 1.f);
   if (cluster > 1) cluster_sync_all();
 }
 
 template <typename K>
-cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& s, unsigned blocks, size_t smem,
-                      cudaStream_t stream) {
+cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& s, unsigned blocks, int planes, int params,
+                      int own, cudaStream_t stream) {
+  const int threads = s.threads_per_row * s.rows_per_block;
+  const int params_bytes = params * 32 * s.threads_per_row + own * 32 * threads, row_bytes = planes * 16 * threads;
+  // As many batches of rows as fit beside the parameters; batches of one row where there is no
+  // room for two of two. (Unaligned rows are not copied: planes is 0.)
+  int per = kBnRows, batches = 1;
+  if (planes) {
+    if ((kBnSmemBytes - params_bytes) / (row_bytes * per) < 2) per = 1;
+    batches = (kBnSmemBytes - params_bytes) / (row_bytes * per);
+    if (batches > kBnMaxBatches) batches = kBnMaxBatches;
+  }
+  size_t smem = size_t(params_bytes) + size_t(row_bytes) * per * batches;
+  if (smem < size_t(threads) * 32) smem = size_t(threads) * 32;  // row groups add up their sums in it
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmemBytes);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(blocks * unsigned(s.cluster));
-  c.blockDim = dim3(unsigned(s.threads_per_row * s.rows_per_block));
+  c.blockDim = dim3(unsigned(threads));
   c.dynamicSmemBytes = smem;
   c.stream = stream;
   cudaLaunchAttribute at[1];
@@ -389,34 +1080,38 @@ cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& 
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   c.attrs = at;
   c.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, p, s.threads_per_row, s.cluster);
+  e = cudaLaunchKernelEx(&c, kernel, p, s.threads_per_row, s.cluster, batches, per);
   if (e == cudaSuccess) count_launch();
   return e;
 }
 
+// Unaligned rows take the kernel that has everything.
+#define FLCE_BN_DISPATCH(KERNEL, BWD)                                                                                \
+  const int own = BWD && p.gate != nullptr && p.w1 != nullptr && !p.gate_full ? 2 : 0;                               \
+  if (!vec) return bn_launch(KERNEL<TX, TR, false, BN_ALL>, p, s, blocks, 0, bn_shared_params(7, BWD), 2, stream);   \
+  switch (feat) {                                                                                                    \
+    case 0: return bn_launch(KERNEL<TX, TR, true, 0>, p, s, blocks, planes, bn_shared_params(0, BWD), own, stream);  \
+    case 1: return bn_launch(KERNEL<TX, TR, true, 1>, p, s, blocks, planes, bn_shared_params(1, BWD), own, stream);  \
+    case 2: return bn_launch(KERNEL<TX, TR, true, 2>, p, s, blocks, planes, bn_shared_params(2, BWD), own, stream);  \
+    case 3: return bn_launch(KERNEL<TX, TR, true, 3>, p, s, blocks, planes, bn_shared_params(3, BWD), own, stream);  \
+    case 4: return bn_launch(KERNEL<TX, TR, true, 4>, p, s, blocks, planes, bn_shared_params(4, BWD), own, stream);  \
+    case 5: return bn_launch(KERNEL<TX, TR, true, 5>, p, s, blocks, planes, bn_shared_params(5, BWD), own, stream);  \
+    case 6: return bn_launch(KERNEL<TX, TR, true, 6>, p, s, blocks, planes, bn_shared_params(6, BWD), own, stream);  \
+    default: return bn_launch(KERNEL<TX, TR, true, 7>, p, s, blocks, planes, bn_shared_params(7, BWD), own, stream); \
+  }
+
 template <typename TX, typename TR>
-cudaError_t bn_forward_typed(const BlockNormParams& p, const BlockNormShape& s, bool vec, unsigned blocks,
+cudaError_t bn_forward_typed(const BlockNormParams& p, const BlockNormShape& s, bool vec, int feat, unsigned blocks,
                              cudaStream_t stream) {
-  return vec ? bn_launch(flce_block_norm_forward_kernel<TX, TR, true>, p, s, blocks, 0, stream)
-             : bn_launch(flce_block_norm_forward_kernel<TX, TR, false>, p, s, blocks, 0, stream);
+  const int planes = int(sizeof(TX) + sizeof(TR)) / 2 + (p.gate_full ? int(sizeof(TR)) / 2 : 0);
+  FLCE_BN_DISPATCH(flce_block_norm_forward_kernel, false)
 }
 
 template <typename TX, typename TR>
 cudaError_t bn_backward_typed(const BlockNormParams& p, const BlockNormShape& s, bool vec, int feat, unsigned blocks,
                               cudaStream_t stream) {
-  const size_t smem = s.rows_per_block > 1 ? size_t(s.threads_per_row) * s.rows_per_block * 8 * sizeof(float) : 0;
-  // unaligned rows take the kernel with every accumulator
-  if (!vec) return bn_launch(flce_block_norm_backward_kernel<TX, TR, false, BN_ALL>, p, s, blocks, smem, stream);
-  switch (feat) {
-    case 0: return bn_launch(flce_block_norm_backward_kernel<TX, TR, true, 0>, p, s, blocks, smem, stream);
-    case 1: return bn_launch(flce_block_norm_backward_kernel<TX, TR, true, 1>, p, s, blocks, smem, stream);
-    case 2: return bn_launch(flce_block_norm_backward_kernel<TX, TR, true, 2>, p, s, blocks, smem, stream);
-    case 3: return bn_launch(flce_block_norm_backward_kernel<TX, TR, true, 3>, p, s, blocks, smem, stream);
-    case 4: return bn_launch(flce_block_norm_backward_kernel<TX, TR, true, 4>, p, s, blocks, smem, stream);
-    case 5: return bn_launch(flce_block_norm_backward_kernel<TX, TR, true, 5>, p, s, blocks, smem, stream);
-    case 6: return bn_launch(flce_block_norm_backward_kernel<TX, TR, true, 6>, p, s, blocks, smem, stream);
-    default: return bn_launch(flce_block_norm_backward_kernel<TX, TR, true, 7>, p, s, blocks, smem, stream);
-  }
+  const int planes = int(sizeof(TX) + sizeof(TR)) + (p.gate_full ? int(sizeof(TR)) / 2 : 0);
+  FLCE_BN_DISPATCH(flce_block_norm_backward_kernel, true)
 }
 
 }  // namespace

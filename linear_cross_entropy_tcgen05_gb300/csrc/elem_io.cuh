@@ -109,6 +109,52 @@ template <typename T> __device__ __forceinline__ Raw8<T> pack8(const float (&f)[
   return r;
 }
 
+// Two fp32 values in a register pair, worked on by one instruction (f32x2).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <typename T> __device__ __forceinline__ void unpack8(const Raw8<T>& r, float2 (&f)[4]) {
+  if constexpr (sizeof(T) == 2) {
+    f[0] = unpack2(r.v[0].x, T());
+    f[1] = unpack2(r.v[0].y, T());
+    f[2] = unpack2(r.v[0].z, T());
+    f[3] = unpack2(r.v[0].w, T());
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[2 * i] = make_float2(__uint_as_float(r.v[i].x), __uint_as_float(r.v[i].y));
+      f[2 * i + 1] = make_float2(__uint_as_float(r.v[i].z), __uint_as_float(r.v[i].w));
+    }
+  }
+}
+template <typename T> __device__ __forceinline__ Raw8<T> pack8(const float2 (&f)[4]) {
+  const float g[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+  return pack8<T>(g);
+}
+
 // Elements [col, col + 8) of a row of D elements; columns past the row read as zero and are
 // not written. VEC: rows are aligned to eight elements and D is a multiple of eight.
 template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> load8(const T* row, int col, int D) {
@@ -132,20 +178,21 @@ template <typename T, bool VEC> __device__ __forceinline__ void store8(T* row, i
   }
 }
 
-// The same with the type known at run time only (parameters, read once per block or chunk).
-__device__ __forceinline__ void load8_any(const void* base, int dt, int64_t off, int col, int D, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[i] = 0.f;
-    if (base != nullptr && col + i < D) {
-      const int64_t k = off + col + i;
-      f[i] = dt == ELEM_F32    ? static_cast<const float*>(base)[k]
-             : dt == ELEM_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(base)[k])
-                               : __half2float(static_cast<const __half*>(base)[k]);
-    }
+template <typename T, bool VEC> __device__ __forceinline__ void store8(T* row, int col, int D, const float2 (&f)[4]) {
+  const float g[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+  store8<T, VEC>(row, col, D, g);
+}
+
+// The same where `at` is the address of column col.
+template <typename T, bool VEC> __device__ __forceinline__ void store8_at(T* at, int col, int D, const float2 (&f)[4]) {
+  if constexpr (VEC) {
+    if (col < D) raw_store(at, pack8<T>(f));
+  } else {
+    store8<T, VEC>(at - col, col, D, f);
   }
 }
 
+// One element of a type known at run time only.
 __device__ __forceinline__ void store_any(void* base, int dt, int64_t k, float v) {
   if (dt == ELEM_F32)
     static_cast<float*>(base)[k] = v;

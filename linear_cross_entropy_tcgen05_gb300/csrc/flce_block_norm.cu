@@ -25,14 +25,12 @@ BlockNormShape bn_shape(int64_t D) {
   while (threads > int64_t(kBnMaxThreads) * s.cluster) s.cluster *= 2;
   s.threads_per_row = int(cdiv(cdiv(threads, s.cluster), 32) * 32);
   s.rows_per_block = s.cluster > 1 ? 1 : kBnMaxThreads / s.threads_per_row;
-  if (s.rows_per_block > 8) s.rows_per_block = 8;
   return s;
 }
 
 // Blocks (or clusters) that stay on the device together.
 int64_t bn_resident(const BlockNormShape& s) {
-  const int per_sm = kBnMaxThreads / (s.threads_per_row * s.rows_per_block);
-  return int64_t(kSms) * (per_sm < 1 ? 1 : per_sm) / s.cluster;
+  return kSms / s.cluster;  // one an SM: the rows on their way in fill its shared memory
 }
 
 struct BwdPlan {
@@ -155,6 +153,7 @@ BlockNormParams bn_params(const flce_block_norm_desc* d) {
   p.w2_dt = d->weight_dtype;
   p.b2_dt = d->bias_dtype;
   p.gate_res_type = d->gate_dtype == d->residual_dtype;
+  p.gate_full = d->gate != nullptr && d->gate_rows == d->N;
   p.act = d->gate_activation;
   p.layer = d->norm == FLCE_NORM_LAYER;
   p.eps = d->eps;
@@ -163,9 +162,16 @@ BlockNormParams bn_params(const flce_block_norm_desc* d) {
   return p;
 }
 
+int bn_features(const flce_block_norm_desc* d) {
+  return (d->post_weight ? BN_POST : 0) | (d->gate ? BN_GATE : 0) |
+         (d->norm == FLCE_NORM_LAYER || d->post_bias || d->bias ? BN_FULL : 0);
+}
+
 bool desc_vec(const flce_block_norm_desc* d) {
   return d->D % 8 == 0 && rows_vec(d->x, d->ld_x, d->x_dtype) && rows_vec(d->residual, d->ld_residual, d->residual_dtype) &&
-         rows_vec(d->gate, d->ld_gate, d->gate_dtype);
+         rows_vec(d->gate, d->ld_gate, d->gate_dtype) && rows_vec(d->post_weight, 8, d->post_weight_dtype) &&
+         rows_vec(d->post_bias, 8, d->post_bias_dtype) && rows_vec(d->weight, 8, d->weight_dtype) &&
+         rows_vec(d->bias, 8, d->bias_dtype);
 }
 
 // Column sums of the partial sums: 32 columns a block, 16 threads down the rows of each, then
@@ -228,7 +234,7 @@ flce_status flce_block_norm_forward(const flce_block_norm_desc* d, void* h, void
   if (!h) return bad("h", "is null");
   if ((y != nullptr) != (d->weight != nullptr)) return bad("y", "is given exactly when weight is");
   if (!api_aligned(h, uintptr_t(elem_bytes(d->residual_dtype))) || !api_aligned(y, uintptr_t(elem_bytes(d->x_dtype))) ||
-      !api_aligned(stats, 4))
+      !api_aligned(stats, 16))
     return FLCE_ERR_ALIGNMENT;
   int sms = 0, dev = -1;
   if ((st = api_device(&sms, &dev)) != FLCE_OK || (st = check_desc_memory(dev, d)) != FLCE_OK ||
@@ -247,7 +253,7 @@ flce_status flce_block_norm_forward(const flce_block_norm_desc* d, void* h, void
   blocks = cdiv(cdiv(d->N, p.chunk_rows), s.rows_per_block);
   const bool f32 = d->residual_dtype == FLCE_DTYPE_F32;
   const auto fn = d->x_dtype == FLCE_DTYPE_BF16 ? bn_forward_bf16 : d->x_dtype == FLCE_DTYPE_F16 ? bn_forward_f16 : bn_forward_f32;
-  return api_cuda("block norm forward", fn(p, s, f32, vec, unsigned(blocks), reinterpret_cast<cudaStream_t>(stream)));
+  return api_cuda("block norm forward", fn(p, s, f32, vec, bn_features(d), unsigned(blocks), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* h, const float* stats, const void* dh,
@@ -265,7 +271,7 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* 
     return bad("grads", "a gradient of an input that is not there");
   const int er = elem_bytes(d->residual_dtype), ex = elem_bytes(d->x_dtype);
   if (!api_aligned(h, er) || !api_aligned(dh, er) || !api_aligned(g->dresidual, er) || !api_aligned(dy, ex) ||
-      !api_aligned(g->dx, ex) || !api_aligned(stats, 4) || !api_aligned(g->dgate, elem_bytes(d->gate_dtype)) ||
+      !api_aligned(g->dx, ex) || !api_aligned(stats, 16) || !api_aligned(g->dgate, elem_bytes(d->gate_dtype)) ||
       !api_aligned(g->dpost_weight, elem_bytes(d->post_weight_dtype)) ||
       !api_aligned(g->dpost_bias, elem_bytes(d->post_bias_dtype)) ||
       !api_aligned(g->dweight, elem_bytes(d->weight_dtype)) || !api_aligned(g->dbias, elem_bytes(d->bias_dtype)) ||
@@ -298,7 +304,6 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* 
   p.chunks_per_group = plan.chunks_per_group;
   p.chunk_rows = plan.chunk_rows;
   p.group_rows = plan.group_rows;
-  p.gate_full = d->gate_rows == d->N;
   p.part_gate = g->dgate && plan.gate_parts ? reinterpret_cast<float*>(ws + plan.part_gate) : nullptr;
   BnSums sums{};
   sums.D = int(d->D);
@@ -313,10 +318,9 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* 
   const bool vec = desc_vec(d) && rows_vec(h, d->D, d->residual_dtype) && rows_vec(dh, ld_dh, d->residual_dtype) &&
                    rows_vec(dy, ld_dy, d->x_dtype) && rows_vec(g->dx, d->D, d->x_dtype) &&
                    rows_vec(g->dresidual, d->D, d->residual_dtype) && rows_vec(g->dgate, d->D, d->gate_dtype);
-  const int feat = (d->post_weight ? BN_POST : 0) | (d->gate ? BN_GATE : 0) | (g->dpost_bias || g->dbias ? BN_BIAS : 0);
   const bool f32 = d->residual_dtype == FLCE_DTYPE_F32;
   const auto fn = d->x_dtype == FLCE_DTYPE_BF16 ? bn_backward_bf16 : d->x_dtype == FLCE_DTYPE_F16 ? bn_backward_f16 : bn_backward_f32;
-  if ((st = api_cuda("block norm backward", fn(p, plan.shape, f32, vec, feat, unsigned(plan.blocks), stream))) != FLCE_OK) return st;
+  if ((st = api_cuda("block norm backward", fn(p, plan.shape, f32, vec, bn_features(d), unsigned(plan.blocks), stream))) != FLCE_OK) return st;
   return api_cuda("block norm sums", bn_column_sums(sums, stream));
 }
 

@@ -163,7 +163,7 @@ def _describe(x, residual, weight, bias, post_weight, post_bias, gate, norm, eps
 def _forward(d, x, h_dtype, want_y: bool, want_stats: bool):
     h = torch.empty(x.shape, dtype=h_dtype, device=x.device)
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_y else None
-    stats = torch.empty((4, d.N), dtype=torch.float32, device=x.device) if want_stats else None
+    stats = torch.empty((d.N, 4), dtype=torch.float32, device=x.device) if want_stats else None
     if d.N > 0:
         if x.device.index == torch.cuda.current_device():
             flce_block_norm_forward(d, h, y, stats)

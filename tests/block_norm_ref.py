@@ -73,7 +73,7 @@ def backward(x, h, gate, post_weight, post_bias, weight, bias, stats, dh, dy, no
     """Gradients from the kernel's own h and statistics: {name: (value, bound)}."""
     N, D = x.shape
     d = lambda t: None if t is None else t.double()  # noqa: E731
-    x, h, w1, b1, w2, st = d(x), d(h), d(post_weight), d(post_bias), d(weight), d(stats)
+    x, h, w1, b1, w2, st = d(x), d(h), d(post_weight), d(post_bias), d(weight), d(stats).T
     zero = torch.zeros_like(x)
     g = zero if dh is None else d(dh)
     mg = g.abs()

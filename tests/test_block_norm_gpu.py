@@ -246,7 +246,7 @@ def test_on_another_stream_and_in_a_graph(gpu_lib):
                                gate=t["gate"].data_ptr(), post_weight=t["post_weight"].data_ptr(), weight=t["weight"].data_ptr(),
                                ld_x=D, ld_residual=D, ld_gate=D, gate_activation=1, eps=1e-5, scale=0.75, weight_offset=0.125)
     h, y, dx, dw = (torch.empty_like(t["x"]) for _ in range(4))
-    dw, stats = torch.empty_like(t["weight"]), torch.empty(4, N, device=DEV)
+    dw, stats = torch.empty_like(t["weight"]), torch.empty(N, 4, device=DEV)
     ws = torch.empty(flce.flce_block_norm_workspace_size(N, D, 1), dtype=torch.uint8, device=DEV)
     grads = flce.FlceBlockNormGrads(dx=dx.data_ptr(), dweight=dw.data_ptr())
 
