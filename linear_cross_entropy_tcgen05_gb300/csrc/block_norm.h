@@ -13,7 +13,7 @@ namespace flce {
 constexpr int kBnMaxThreads = 512;
 constexpr int kBnMaxCluster = 8;
 constexpr int kBnSmemBytes = 212 << 10;  // shared memory for parameters and rows on their way in
-constexpr int64_t kBnMaxD = 32768;
+constexpr int64_t kBnMaxD = 16384;
 
 struct BlockNormShape {
   int cluster;          // blocks that share a row
@@ -53,6 +53,40 @@ __host__ __device__ constexpr int bn_shared_params(int feat, bool backward) {
   if (!(feat & BN_FULL)) return 0;
   if (!backward) return feat & BN_GATE ? 4 : 2;
   return feat & BN_POST ? (feat & BN_GATE ? 3 : 2) : 1;
+}
+// Values that each thread of a backward kernel keeps there for itself: a gate, the sum of its
+// gradient and a bias's (with all of them in registers the kernel spills: 386 us against 210 at
+// N = 16384, D = 2304).
+__host__ __device__ constexpr int bn_own_params(int feat, bool backward) {
+  return backward && (feat & BN_POST) && (feat & BN_GATE) ? (feat & BN_FULL ? 3 : 2) : 0;
+}
+
+// Rows that a row group works on together at most: they share the latency of their sums. (Four in
+// the forward pass measured slower: their copies come in bursts that leave the memory idle
+// between them, N = 65536, D = 4096 bf16: 537 us against 431.)
+constexpr int kBnRows = 2;
+constexpr int kBnMaxBatches = 6;
+
+// 16-byte planes a thread of one row: x and the residual, or x, dy, h and dh, and a full gate.
+constexpr int bn_planes(int x_bytes, int residual_bytes, bool gate_full, bool backward) {
+  return (x_bytes + residual_bytes) / 2 * (backward ? 2 : 1) + (gate_full ? residual_bytes / 2 : 0);
+}
+
+// Batches of rows on their way in: as many as fit beside the parameters, of one row where there
+// is no room for two batches of two. At least two are needed: one in work, one landed. (Unaligned
+// rows are not copied: planes is 0.)
+struct BnRing {
+  int per, batches, params_bytes;
+};
+constexpr BnRing bn_ring(const BlockNormShape& s, int planes, int feat, bool backward) {
+  const int threads = s.threads_per_row * s.rows_per_block;
+  BnRing r{kBnRows, 1, bn_shared_params(feat, backward) * 32 * s.threads_per_row + bn_own_params(feat, backward) * 32 * threads};
+  if (planes == 0) return r;
+  const int room = kBnSmemBytes - r.params_bytes, row = planes * 16 * threads;
+  if (room / (row * r.per) < 2) r.per = 1;
+  r.batches = room / (row * r.per);
+  if (r.batches > kBnMaxBatches) r.batches = kBnMaxBatches;
+  return r;
 }
 
 cudaError_t bn_forward_bf16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);

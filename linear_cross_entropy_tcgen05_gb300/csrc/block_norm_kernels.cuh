@@ -23,12 +23,6 @@
 namespace flce {
 namespace {
 
-// Rows that a row group works on together at most: they share the latency of their sums. Where
-// shared memory has no room for two batches of two rows, a batch is one row.
-// (Four in the forward pass measured slower: their copies come in bursts that leave the
-// memory idle between them, N = 65536, D = 4096 bf16: 537 us against 431.)
-constexpr int kBnRows = 2;
-
 // Rows are copied to shared memory (cp.async) some batches of kBnRows rows ahead. A thread
 // copies and reads only its own eight columns, so a batch is ready for it when its own copies
 // are: no barrier. A batch has, for each of its rows and tensors, planes of 16 bytes a thread.
@@ -79,17 +73,15 @@ struct RowRing {
     }
   }
 };
-constexpr int kBnMaxBatches = 6;
 
-// A tensor's rows, as the address of a thread's columns in the next row to be copied or written.
-template <typename T> struct RowPtr {
-  T* at;
-  int64_t step;
-  __device__ __forceinline__ RowPtr(const void* base, int64_t ld, int64_t row, int col)
-      : at(static_cast<T*>(const_cast<void*>(base)) + row * ld + col), step(ld) {}
-  __device__ __forceinline__ T* row(int r) const { return at + r * step; }
-  __device__ __forceinline__ void advance(int rows) { at += rows * step; }
-};
+// Address of a thread's columns in a row (computed where it is used: pointers that are kept
+// from row to row cost the registers that the sums need).
+template <typename T> __device__ __forceinline__ const T* row_at(const void* base, int64_t row, int64_t ld, int col) {
+  return static_cast<const T*>(base) + row * ld + col;
+}
+template <typename T> __device__ __forceinline__ T* row_at(void* base, int64_t row, int64_t ld, int col) {
+  return static_cast<T*>(base) + row * ld + col;
+}
 
 // Sums over the threads of a row, of NV values at once (those of several rows: a sum is all
 // latency, about 500 cycles of shuffles, a barrier and reads, so rows share it). Within a warp
@@ -447,29 +439,21 @@ __global__ void __launch_bounds__(kBnMaxThreads)
   const int lo = int(r0.worker * p.chunk_rows < p.N ? r0.worker * p.chunk_rows : p.N);
   const int hi = int(lo + p.chunk_rows < p.N ? lo + p.chunk_rows : p.N);
   RowRing ring{};
-  RowPtr<TX> src_x(p.x, p.ld_x, lo, col), src_gx(p.gate, p.ld_gate, lo, col);
-  RowPtr<TR> src_r(p.residual, p.ld_residual, lo, col), src_gr(p.gate, p.ld_gate, lo, col);
   int next = lo;  // the row that is copied next
   auto fetch = [&](uint32_t at) FLCE_INLINE {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (live && r < per && next + r < hi) {
-        const uint32_t row_at = at + uint32_t(r * ring.row_bytes);
-        ring.copy(row_at, kX, src_x.row(r));
-        if (p.residual != nullptr) ring.copy(row_at, kR, src_r.row(r));
+        const uint32_t to = at + uint32_t(r * ring.row_bytes);
+        ring.copy(to, kX, row_at<TX>(p.x, next + r, p.ld_x, col));
+        if (p.residual != nullptr) ring.copy(to, kR, row_at<TR>(p.residual, next + r, p.ld_residual, col));
         if (gate_full) {
           if (p.gate_res_type)
-            ring.copy(row_at, kG, src_gr.row(r));
+            ring.copy(to, kG, row_at<TR>(p.gate, next + r, p.ld_gate, col));
           else
-            ring.copy(row_at, kG, src_gx.row(r));
+            ring.copy(to, kG, row_at<TX>(p.gate, next + r, p.ld_gate, col));
         }
       }
-    }
-    src_x.advance(per);
-    src_r.advance(per);
-    if (GATE) {
-      src_gx.advance(per);
-      src_gr.advance(per);
     }
     next += per;
     ring.commit();
@@ -522,8 +506,6 @@ __global__ void __launch_bounds__(kBnMaxThreads)
   };
   const float inv_d = 1.f / float(D);
   int gate_end = lo;  // first row whose gate is not in c
-  RowPtr<TR> out_h(p.h, D, lo, col);
-  RowPtr<TX> out_y(p.y, D, lo, col);
   // The first norm of a batch and the second norm of the batch before it share a sum: the
   // latency of a batch is one sum, and what comes before and after it is independent work.
   uint32_t batch = ring.first;
@@ -586,9 +568,8 @@ __global__ void __launch_bounds__(kBnMaxThreads)
           h[r][i] = fma2(u[i], c[i], h[r][i]);
         }
       }
-      store8_at<TR, VEC>(out_h.row(r), col, D, h[r]);
+      store8_at<TR, VEC>(row_at<TR>(p.h, row + r, D, col), col, D, h[r]);
     }
-    out_h.advance(per);
     float m2[R], r2[R], n1[R], k1[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) m2[r] = r2[r] = n1[r] = 0.f, k1[r] = 1.f;
@@ -640,9 +621,8 @@ __global__ void __launch_bounds__(kBnMaxThreads)
           else
             h[r][i] = mul2(mul2(h[r][i], both(r2[r])), w2[i]);
         }
-        store8_at<TX, VEC>(out_y.row(r), col, D, h[r]);
+        store8_at<TX, VEC>(row_at<TX>(p.y, row + r, D, col), col, D, h[r]);
       }
-      out_y.advance(per);
     }
     if (p.stats != nullptr && col == 0) {
 #pragma unroll
@@ -670,7 +650,8 @@ __global__ void __launch_bounds__(kBnMaxThreads)
   extern __shared__ __align__(16) char ring_smem[];
   constexpr int kX = 0, kY = sizeof(TX) / 2, kH = 2 * kY, kDh = kH + sizeof(TR) / 2, kG = kDh + sizeof(TR) / 2;  // planes
   constexpr int kParams = bn_shared_params(FEAT, true);
-  constexpr bool OWN = POST && GATE;  // the gate and the sum of its gradient are in shared memory
+  constexpr bool OWN = POST && GATE;  // the gate and the sum of its gradient are in shared memory,
+  constexpr bool OWN_B = OWN && FULL; // and one bias's sum
   const RowThread r0 = row_thread(threads_per_row, cluster);
   RowSum rs = row_sum(scratch, r0, threads_per_row, cluster, p.D);
   const int col = r0.col, D = p.D;
@@ -680,20 +661,18 @@ __global__ void __launch_bounds__(kBnMaxThreads)
   const bool live_col = col < D;
   // the worker's rows: chunk after chunk, once for the copies and once, behind them, for the work
   struct Rows {
-    int chunk, group, row, hi;
+    int chunk, row, hi;
   };
   auto open = [&](Rows& w) FLCE_INLINE {
     if (w.chunk >= p.chunks) return;
-    w.group = w.chunk / int(p.chunks_per_group);
-    const int first = w.group * int(p.group_rows), end = first + int(p.group_rows);
-    w.row = first + (w.chunk - w.group * int(p.chunks_per_group)) * int(p.chunk_rows);
+    const int group = w.chunk / int(p.chunks_per_group);
+    const int first = group * int(p.group_rows), end = first + int(p.group_rows);
+    w.row = first + (w.chunk - group * int(p.chunks_per_group)) * int(p.chunk_rows);
     w.hi = end - w.row < int(p.chunk_rows) ? end : w.row + int(p.chunk_rows);
   };
   RowRing ring{};
-  Rows ahead{int(r0.worker), 0, 0, 0};
+  Rows ahead{int(r0.worker), 0, 0};
   open(ahead);
-  RowPtr<TX> src_x(p.x, p.ld_x, ahead.row, col), src_dy(p.dy, p.ld_dy, ahead.row, col);
-  RowPtr<TR> src_h(p.h_in, D, ahead.row, col), src_dh(p.dh, p.ld_dh, ahead.row, col);
   // a batch's statistics: copied by the first lanes of each warp for the warp alone
   __shared__ __align__(16) float4 warp_stats[kBnMaxThreads / 32][kBnMaxBatches][R];
   const float4* stats = reinterpret_cast<const float4*>(p.stats);
@@ -711,38 +690,31 @@ __global__ void __launch_bounds__(kBnMaxThreads)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           if (r > 0 && (r >= per || ahead.row + r >= ahead.hi)) continue;
-          const uint32_t row_at = at + uint32_t(r * ring.row_bytes);
-          ring.copy(row_at, kX, src_x.row(r));
-          if (pre) ring.copy(row_at, kH, src_h.row(r));
-          if (p.dh != nullptr) ring.copy(row_at, kDh, src_dh.row(r));
-          if (pre && p.dy != nullptr) ring.copy(row_at, kY, src_dy.row(r));
+          const uint32_t to = at + uint32_t(r * ring.row_bytes);
+          const int row = ahead.row + r;
+          ring.copy(to, kX, row_at<TX>(p.x, row, p.ld_x, col));
+          if (pre) ring.copy(to, kH, row_at<TR>(p.h_in, row, D, col));
+          if (p.dh != nullptr) ring.copy(to, kDh, row_at<TR>(p.dh, row, p.ld_dh, col));
+          if (pre && p.dy != nullptr) ring.copy(to, kY, row_at<TX>(p.dy, row, p.ld_dy, col));
           if (gate_full) {
             if (p.gate_res_type)
-              ring.copy(row_at, kG, static_cast<const TR*>(p.gate) + (ahead.row + r) * p.ld_gate + col);
+              ring.copy(to, kG, row_at<TR>(p.gate, row, p.ld_gate, col));
             else
-              ring.copy(row_at, kG, static_cast<const TX*>(p.gate) + (ahead.row + r) * p.ld_gate + col);
+              ring.copy(to, kG, row_at<TX>(p.gate, row, p.ld_gate, col));
           }
         }
       }
       ahead.row += per;
-      src_x.advance(per);
-      src_h.advance(per);
-      src_dh.advance(per);
-      src_dy.advance(per);
       if (ahead.row >= ahead.hi) {
         ahead.chunk += workers;
         open(ahead);
-        src_x = RowPtr<TX>(p.x, p.ld_x, ahead.row, col);
-        src_dy = RowPtr<TX>(p.dy, p.ld_dy, ahead.row, col);
-        src_h = RowPtr<TR>(p.h_in, D, ahead.row, col);
-        src_dh = RowPtr<TR>(p.dh, p.ld_dh, ahead.row, col);
       }
     }
     ring.commit();
     stat_slot = stat_slot + 1 == batches ? 0 : stat_slot + 1;
   };
   if constexpr (VEC) {
-    ring.init(ring_smem + kParams * 32 * threads_per_row + (OWN && !gate_full ? 64 * int(blockDim.x) : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
+    ring.init(ring_smem + kParams * 32 * threads_per_row + (OWN ? (OWN_B ? 96 : 64) * int(blockDim.x) : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
     for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
   }
   if (cluster > 1) cluster_sync_all();
@@ -765,7 +737,8 @@ __global__ void __launch_bounds__(kBnMaxThreads)
   }
   const int own_plane = int(blockDim.x);
   float4* own = reinterpret_cast<float4*>(ring_smem + kParams * 32 * threads_per_row) + threadIdx.x;
-  const OwnParam own_a{own, own_plane}, own_dg{own + 2 * own_plane, own_plane};
+  const OwnParam own_a{own, own_plane}, own_dg{own + 2 * own_plane, own_plane}, own_db1{own + 4 * own_plane, own_plane};
+  if (OWN_B) own_db1.set(db1);
   if (OWN && gate && !gate_full) own_dg.set(dg);
   const float inv_d = 1.f / float(D), inv_d0 = p.layer ? inv_d : 0.f;
   const float live = live_col ? 1.f : 0.f;  // threads past the row: their values stay zero
@@ -845,7 +818,7 @@ __global__ void __launch_bounds__(kBnMaxThreads)
       if (FULL && POST) t0[r] = v[kOf * R + R + r];
     }
   };
-  Rows now{int(r0.worker), 0, 0, 0};
+  Rows now{int(r0.worker), 0, 0};
   open(now);
   uint32_t batch = ring.first;
   int slot = 0, open_chunk = -1;
@@ -870,7 +843,7 @@ __global__ void __launch_bounds__(kBnMaxThreads)
       __syncwarp();
     }
     if (gate && !gate_full && now.chunk != open_chunk) {
-      load_gate<TX, TR, VEC>(p, now.group, col, a);
+      load_gate<TX, TR, VEC>(p, now.chunk / int(p.chunks_per_group), col, a);
       if (OWN) own_a.set(a);
     }
     open_chunk = now.chunk;
@@ -950,11 +923,19 @@ __global__ void __launch_bounds__(kBnMaxThreads)
       }
       if (post) {
         const float2 k = both(st.y);
+        float2 e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           dw1[i] = fma2(mul2(d[r][i], k), x[i], dw1[i]);
-          if (FULL) db1[i] = add2(db1[i], d[r][i]);
+          if (FULL && !OWN_B) db1[i] = add2(db1[i], d[r][i]);
+          e[i] = d[r][i];
           d[r][i] = mul2(d[r][i], w1[i]);
+        }
+        if (OWN_B) {
+          own_db1.get(db1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) db1[i] = add2(db1[i], e[i]);
+          own_db1.set(db1);
         }
         t1[r] = dot8(d[r], x);
         if (FULL) t0[r] = sum8(d[r]);
@@ -1010,9 +991,9 @@ __global__ void __launch_bounds__(kBnMaxThreads)
       if (p.part_gate != nullptr)
         store8<float, VEC>(p.part_gate + int64_t(now.chunk) * D, col, D, dg);
       else if (p.gate_res_type)
-        store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(now.group) * D, col, D, dg);
+        store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, col, D, dg);
       else
-        store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(now.group) * D, col, D, dg);
+        store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, col, D, dg);
 #pragma unroll
       for (int i = 0; i < 4; ++i) dg[i] = both(0.f);
       if (OWN) own_dg.set(dg);
@@ -1045,6 +1026,8 @@ __global__ void __launch_bounds__(kBnMaxThreads)
     for (int i = 0; i < 4; ++i) s[i] = mul2(s[i], both(scale));
     store8<float, VEC>(part + block * D, col, D, s);
   };
+  if (OWN_B) own_db1.get(db1);
+  if (OWN_B) __syncthreads();  // the sums' room is used again
   if (POST) flush(p.part[0], dw1, p.scale);
   if (POST && FULL) flush(p.part[1], db1, p.scale);
   flush(p.part[2], dw2, 1.f);
@@ -1053,19 +1036,11 @@ __global__ void __launch_bounds__(kBnMaxThreads)
 }
 
 template <typename K>
-cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& s, unsigned blocks, int planes, int params,
-                      int own, cudaStream_t stream) {
+cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& s, unsigned blocks, int planes, int feat,
+                      bool backward, cudaStream_t stream) {
   const int threads = s.threads_per_row * s.rows_per_block;
-  const int params_bytes = params * 32 * s.threads_per_row + own * 32 * threads, row_bytes = planes * 16 * threads;
-  // As many batches of rows as fit beside the parameters; batches of one row where there is no
-  // room for two of two. (Unaligned rows are not copied: planes is 0.)
-  int per = kBnRows, batches = 1;
-  if (planes) {
-    if ((kBnSmemBytes - params_bytes) / (row_bytes * per) < 2) per = 1;
-    batches = (kBnSmemBytes - params_bytes) / (row_bytes * per);
-    if (batches > kBnMaxBatches) batches = kBnMaxBatches;
-  }
-  size_t smem = size_t(params_bytes) + size_t(row_bytes) * per * batches;
+  const BnRing r = bn_ring(s, planes, feat, backward);
+  size_t smem = size_t(r.params_bytes) + size_t(planes) * 16 * threads * r.per * r.batches;
   if (smem < size_t(threads) * 32) smem = size_t(threads) * 32;  // row groups add up their sums in it
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmemBytes);
   if (e != cudaSuccess) return e;
@@ -1080,37 +1055,36 @@ cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& 
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   c.attrs = at;
   c.numAttrs = 1;
-  e = cudaLaunchKernelEx(&c, kernel, p, s.threads_per_row, s.cluster, batches, per);
+  e = cudaLaunchKernelEx(&c, kernel, p, s.threads_per_row, s.cluster, r.batches, r.per);
   if (e == cudaSuccess) count_launch();
   return e;
 }
 
 // Unaligned rows take the kernel that has everything.
-#define FLCE_BN_DISPATCH(KERNEL, BWD)                                                                                \
-  const int own = BWD && p.gate != nullptr && p.w1 != nullptr && !p.gate_full ? 2 : 0;                               \
-  if (!vec) return bn_launch(KERNEL<TX, TR, false, BN_ALL>, p, s, blocks, 0, bn_shared_params(7, BWD), 2, stream);   \
-  switch (feat) {                                                                                                    \
-    case 0: return bn_launch(KERNEL<TX, TR, true, 0>, p, s, blocks, planes, bn_shared_params(0, BWD), own, stream);  \
-    case 1: return bn_launch(KERNEL<TX, TR, true, 1>, p, s, blocks, planes, bn_shared_params(1, BWD), own, stream);  \
-    case 2: return bn_launch(KERNEL<TX, TR, true, 2>, p, s, blocks, planes, bn_shared_params(2, BWD), own, stream);  \
-    case 3: return bn_launch(KERNEL<TX, TR, true, 3>, p, s, blocks, planes, bn_shared_params(3, BWD), own, stream);  \
-    case 4: return bn_launch(KERNEL<TX, TR, true, 4>, p, s, blocks, planes, bn_shared_params(4, BWD), own, stream);  \
-    case 5: return bn_launch(KERNEL<TX, TR, true, 5>, p, s, blocks, planes, bn_shared_params(5, BWD), own, stream);  \
-    case 6: return bn_launch(KERNEL<TX, TR, true, 6>, p, s, blocks, planes, bn_shared_params(6, BWD), own, stream);  \
-    default: return bn_launch(KERNEL<TX, TR, true, 7>, p, s, blocks, planes, bn_shared_params(7, BWD), own, stream); \
+#define FLCE_BN_DISPATCH(KERNEL, BWD)                                                              \
+  if (!vec) return bn_launch(KERNEL<TX, TR, false, BN_ALL>, p, s, blocks, 0, BN_ALL, BWD, stream); \
+  switch (feat) {                                                                                  \
+    case 0: return bn_launch(KERNEL<TX, TR, true, 0>, p, s, blocks, planes, 0, BWD, stream);       \
+    case 1: return bn_launch(KERNEL<TX, TR, true, 1>, p, s, blocks, planes, 1, BWD, stream);       \
+    case 2: return bn_launch(KERNEL<TX, TR, true, 2>, p, s, blocks, planes, 2, BWD, stream);       \
+    case 3: return bn_launch(KERNEL<TX, TR, true, 3>, p, s, blocks, planes, 3, BWD, stream);       \
+    case 4: return bn_launch(KERNEL<TX, TR, true, 4>, p, s, blocks, planes, 4, BWD, stream);       \
+    case 5: return bn_launch(KERNEL<TX, TR, true, 5>, p, s, blocks, planes, 5, BWD, stream);       \
+    case 6: return bn_launch(KERNEL<TX, TR, true, 6>, p, s, blocks, planes, 6, BWD, stream);       \
+    default: return bn_launch(KERNEL<TX, TR, true, 7>, p, s, blocks, planes, 7, BWD, stream);      \
   }
 
 template <typename TX, typename TR>
 cudaError_t bn_forward_typed(const BlockNormParams& p, const BlockNormShape& s, bool vec, int feat, unsigned blocks,
                              cudaStream_t stream) {
-  const int planes = int(sizeof(TX) + sizeof(TR)) / 2 + (p.gate_full ? int(sizeof(TR)) / 2 : 0);
+  const int planes = bn_planes(int(sizeof(TX)), int(sizeof(TR)), p.gate_full, false);
   FLCE_BN_DISPATCH(flce_block_norm_forward_kernel, false)
 }
 
 template <typename TX, typename TR>
 cudaError_t bn_backward_typed(const BlockNormParams& p, const BlockNormShape& s, bool vec, int feat, unsigned blocks,
                               cudaStream_t stream) {
-  const int planes = int(sizeof(TX) + sizeof(TR)) + (p.gate_full ? int(sizeof(TR)) / 2 : 0);
+  const int planes = bn_planes(int(sizeof(TX)), int(sizeof(TR)), p.gate_full, true);
   FLCE_BN_DISPATCH(flce_block_norm_backward_kernel, true)
 }
 

@@ -18,19 +18,28 @@ constexpr int kSms = 152;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-BlockNormShape bn_shape(int64_t D) {
+BlockNormShape bn_shape(int64_t D, int max_threads) {
   BlockNormShape s{};
   const int64_t threads = cdiv(D, 8);
   s.cluster = 1;
-  while (threads > int64_t(kBnMaxThreads) * s.cluster) s.cluster *= 2;
+  while (threads > int64_t(max_threads) * s.cluster) s.cluster *= 2;
   s.threads_per_row = int(cdiv(cdiv(threads, s.cluster), 32) * 32);
-  s.rows_per_block = s.cluster > 1 ? 1 : kBnMaxThreads / s.threads_per_row;
+  s.rows_per_block = s.cluster > 1 ? 1 : max_threads / s.threads_per_row;
   return s;
 }
 
 // Blocks (or clusters) that stay on the device together.
 int64_t bn_resident(const BlockNormShape& s) {
   return kSms / s.cluster;  // one an SM: the rows on their way in fill its shared memory
+}
+
+// Threads of a block for these tensors: half as many where the rows of the widest would leave no
+// room for two batches of them (fp32
+// rows of 4096 columns with a gate for each), so that clusters share them.
+int bn_threads(const flce_block_norm_desc* d, bool vec, int feat, bool backward) {
+  if (!vec) return kBnMaxThreads;
+  const int planes = bn_planes(elem_bytes(d->x_dtype), elem_bytes(d->residual_dtype), d->gate && d->gate_rows == d->N, backward);
+  return bn_ring(bn_shape(d->D, kBnMaxThreads), planes, feat, backward).batches >= 2 ? kBnMaxThreads : kBnMaxThreads / 2;
 }
 
 struct BwdPlan {
@@ -44,9 +53,9 @@ struct BwdPlan {
 // blocks) in turn. Among splits that keep the partial sums of the gate's gradient small the
 // one with the shortest longest worker is taken. A worker keeps its sums over at least four
 // rows, so that the partial sums stay small beside the rows.
-BwdPlan bwd_plan(int64_t N, int64_t D, int64_t gate_rows) {
+BwdPlan bwd_plan(int64_t N, int64_t D, int64_t gate_rows, int max_threads) {
   BwdPlan p{};
-  p.shape = bn_shape(D);
+  p.shape = bn_shape(D, max_threads);
   const int64_t groups = gate_rows == 0 || gate_rows == N ? 1 : gate_rows;  // a full gate needs no sums
   p.group_rows = N / groups;
   int64_t blocks = bn_resident(p.shape);
@@ -224,7 +233,8 @@ extern "C" {
 size_t flce_block_norm_workspace_size(int64_t N, int64_t D, int64_t gate_rows) {
   if (N < 1 || D < 1 || N >= (int64_t(1) << 30) || D > kBnMaxD || gate_rows < 0 || gate_rows > N) return 0;
   if (gate_rows > 0 && N % gate_rows != 0) return 0;
-  return bwd_plan(N, D, gate_rows).total;
+  const size_t a = bwd_plan(N, D, gate_rows, kBnMaxThreads).total, b = bwd_plan(N, D, gate_rows, kBnMaxThreads / 2).total;
+  return a > b ? a : b;
 }
 
 flce_status flce_block_norm_forward(const flce_block_norm_desc* d, void* h, void* y, float* stats,
@@ -245,15 +255,16 @@ flce_status flce_block_norm_forward(const flce_block_norm_desc* d, void* h, void
   p.h = h;
   p.y = y;
   p.stats = stats;
-  const BlockNormShape s = bn_shape(d->D);
   const bool vec = desc_vec(d) && rows_vec(h, d->D, d->residual_dtype) && rows_vec(y, d->D, d->x_dtype);
+  const int feat = bn_features(d);
+  const BlockNormShape s = bn_shape(d->D, bn_threads(d, vec, feat, false));
   const int64_t need = cdiv(d->N, s.rows_per_block), resident = bn_resident(s);
   int64_t blocks = need < resident ? need : resident;
   p.chunk_rows = cdiv(d->N, blocks * s.rows_per_block);
   blocks = cdiv(cdiv(d->N, p.chunk_rows), s.rows_per_block);
   const bool f32 = d->residual_dtype == FLCE_DTYPE_F32;
   const auto fn = d->x_dtype == FLCE_DTYPE_BF16 ? bn_forward_bf16 : d->x_dtype == FLCE_DTYPE_F16 ? bn_forward_f16 : bn_forward_f32;
-  return api_cuda("block norm forward", fn(p, s, f32, vec, bn_features(d), unsigned(blocks), reinterpret_cast<cudaStream_t>(stream)));
+  return api_cuda("block norm forward", fn(p, s, f32, vec, feat, unsigned(blocks), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* h, const float* stats, const void* dh,
@@ -278,8 +289,7 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* 
       !api_aligned(workspace, 256))
     return FLCE_ERR_ALIGNMENT;
   if (!workspace) return bad("workspace", "is null");
-  const BwdPlan plan = bwd_plan(d->N, d->D, d->gate_rows);
-  if (ws_bytes < plan.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < flce_block_norm_workspace_size(d->N, d->D, d->gate_rows)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0, dev = -1;
   if ((st = api_device(&sms, &dev)) != FLCE_OK || (st = check_desc_memory(dev, d)) != FLCE_OK) return st;
   const struct { const char* name; const void* p; } ptrs[] = {
@@ -289,6 +299,11 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* 
   for (const auto& q : ptrs)
     if ((st = api_check_memory(dev, q.name, q.p)) != FLCE_OK) return st;
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const bool vec = desc_vec(d) && rows_vec(h, d->D, d->residual_dtype) && rows_vec(dh, ld_dh, d->residual_dtype) &&
+                   rows_vec(dy, ld_dy, d->x_dtype) && rows_vec(g->dx, d->D, d->x_dtype) &&
+                   rows_vec(g->dresidual, d->D, d->residual_dtype) && rows_vec(g->dgate, d->D, d->gate_dtype);
+  const int feat = bn_features(d);
+  const BwdPlan plan = bwd_plan(d->N, d->D, d->gate_rows, bn_threads(d, vec, feat, true));
   char* ws = static_cast<char*>(workspace);
   BlockNormParams p = bn_params(d);
   p.stats = const_cast<float*>(stats);
@@ -315,12 +330,9 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* 
     sums.a[sums.n++] = BnSum{p.part[i], params[i].out, 1, plan.blocks, params[i].dt};
   }
   if (p.part_gate) sums.a[sums.n++] = BnSum{p.part_gate, g->dgate, d->gate_rows, plan.chunks_per_group, d->gate_dtype};
-  const bool vec = desc_vec(d) && rows_vec(h, d->D, d->residual_dtype) && rows_vec(dh, ld_dh, d->residual_dtype) &&
-                   rows_vec(dy, ld_dy, d->x_dtype) && rows_vec(g->dx, d->D, d->x_dtype) &&
-                   rows_vec(g->dresidual, d->D, d->residual_dtype) && rows_vec(g->dgate, d->D, d->gate_dtype);
   const bool f32 = d->residual_dtype == FLCE_DTYPE_F32;
   const auto fn = d->x_dtype == FLCE_DTYPE_BF16 ? bn_backward_bf16 : d->x_dtype == FLCE_DTYPE_F16 ? bn_backward_f16 : bn_backward_f32;
-  if ((st = api_cuda("block norm backward", fn(p, plan.shape, f32, vec, bn_features(d), unsigned(plan.blocks), stream))) != FLCE_OK) return st;
+  if ((st = api_cuda("block norm backward", fn(p, plan.shape, f32, vec, feat, unsigned(plan.blocks), stream))) != FLCE_OK) return st;
   return api_cuda("block norm sums", bn_column_sums(sums, stream));
 }
 

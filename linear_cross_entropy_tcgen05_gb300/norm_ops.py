@@ -233,7 +233,7 @@ def block_norm(x, residual=None, weight=None, *, bias=None, post_weight=None, po
     (x's or the residual's type) has one row for all rows ([D]), one for each equal run of rows
     ([G, D]; for x [B, T, D] also [B, 1, D]) or x's shape, and goes through
     ``gate_activation`` ("none", "sigmoid", "tanh"). ``norm`` is "rms" or "layer"; weights are
-    used as ``weight + weight_offset``. D is at most 32768.
+    used as ``weight + weight_offset``. D is at most 16384.
 
     Differentiable in every tensor; a gradient has its input's type. With a 16-bit residual
     stream the backward pass reads the rounded h.

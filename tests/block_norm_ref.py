@@ -2,7 +2,7 @@
 
 Every bound is ``K * 2^-24`` times a magnitude that is the formula evaluated on absolute
 values (what cancellation can blow up a 32-bit rounding to), plus half a step of the output's
-type. K counts the roundings on the way to a value: a tree sum of up to 32768 terms (15), the
+type. K counts the roundings on the way to a value: a tree sum of up to 16384 terms (14), the
 reciprocal square root and its argument (8), the products and sums of the formula (at most 16
 for each of two norms), so 64 covers a forward value and 128 a gradient, in which the
 statistics enter twice. A sum over N rows adds at most N roundings of its terms."""

@@ -29,7 +29,7 @@ def _bwd(h=0x40000, stats=0x60000, dh=0x70000, ld_dh=64, dy=0x80000, ld_dy=64, w
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(N=0), 1), (dict(D=0), 1), (dict(D=32769, ld_x=32769, ld_residual=32769), 9), (dict(N=1 << 30), 9),
+    (dict(N=0), 1), (dict(D=0), 1), (dict(D=16385, ld_x=16385, ld_residual=16385), 9), (dict(N=1 << 30), 9),
     (dict(x=None), 1), (dict(h=None), 1), (dict(y=None), 1), (dict(weight=None), 1), (dict(ld_x=63), 1),
     (dict(ld_residual=1), 1), (dict(x_dtype=3), 1), (dict(residual_dtype=1), 1), (dict(norm=2), 1),
     (dict(gate_activation=3), 1), (dict(gate_rows=1), 1), (dict(gate=0x11000, ld_gate=64), 1),
@@ -58,8 +58,8 @@ def test_good_arguments_reach_the_device_check():
 
 def test_workspace_size():
     size = flce.flce_block_norm_workspace_size
-    assert size(0, 64) == size(4, 0) == size(4, 32769) == size(4, 64, 3) == size(4, 64, 5) == size(4, 64, -1) == 0
-    for N, D in [(1, 1), (1, 4096), (65536, 4096), (100000, 64), (77, 32768)]:
+    assert size(0, 64) == size(4, 0) == size(4, 16385) == size(4, 64, 3) == size(4, 64, 5) == size(4, 64, -1) == 0
+    for N, D in [(1, 1), (1, 4096), (65536, 4096), (100000, 64), (77, 16384)]:
         # four parameter sums for each of at most 152 * 16 blocks
         assert 4 * D * 4 <= size(N, D) <= 4 * 152 * 16 * (D * 4 + 256)
         # a gate for every row needs no sums; groups need at most a few for each worker

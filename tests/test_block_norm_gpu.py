@@ -32,8 +32,12 @@ CASES = [
     (33, 5121, "f16", "f32", "rms", True, 3, "sigmoid", False),
     (350, 8192, "bf16", "bf16", "rms", True, -1, "none", False),
     (11, 16384, "bf16", "f32", "layer", True, 11, "sigmoid", True),
-    (3, 32768, "f32", "f32", "layer", True, 1, "tanh", True),
-    (2, 32767, "bf16", "bf16", "rms", False, 0, "none", False),
+    (3, 16384, "f32", "f32", "layer", True, 1, "tanh", True),
+    (30, 4096, "f32", "f32", "layer", True, -1, "tanh", True),
+    (30, 3456, "f32", "f32", "layer", True, 2, "sigmoid", True),
+    (19, 4096, "bf16", "f32", "rms", True, 19, "sigmoid", False),
+    (1500, 2560, "f16", "f16", "layer", True, 6, "sigmoid", True),
+    (2, 16383, "bf16", "bf16", "rms", False, 0, "none", False),
     (40, 512, "bf16", None, "rms", False, 0, "none", False),
     (41, 640, "f16", None, "layer", True, 1, "sigmoid", True),
     (700, 96, "bf16", "bf16", "rms", True, 350, "sigmoid", False),
