@@ -244,6 +244,19 @@ def _stream(stream) -> int | None:
     return int(stream)
 
 
+def _call_on(dev: torch.device, where: str, fn, *args) -> None:
+    """fn(*args, the current stream of dev) with dev current, as the library needs it; raises on
+    an error. What the small calls spend on the host counts, so the device is switched only
+    where it has to be and the stream's handle is asked for without a Stream object."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st != 0:
+        raise FLCEError(st, where)
+
+
 def _check(status: int, where: str) -> None:
     if status != 0:
         raise FLCEError(status, where)

@@ -3,7 +3,9 @@
 ``flce_beam_select`` and ``flce_beam_reorder`` marshal to the C ABI (include/flce.h)."""
 from __future__ import annotations
 
+import array
 import ctypes
+import math
 
 import torch
 
@@ -25,11 +27,11 @@ def declare(lib) -> None:
     lib.flce_beam_select_workspace_size.argtypes, lib.flce_beam_select_workspace_size.restype = [i64] * 4, sz
     lib.flce_beam_select.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, vp, i32, i64, vp, vp, vp, vp, sz, vp]
     lib.flce_beam_select.restype = ctypes.c_int
-    lib.flce_beam_reorder.argtypes = [ctypes.POINTER(FlceBeamState), i64, vp, i64, i64, i64, vp]
+    lib.flce_beam_reorder.argtypes = [vp, i64, vp, i64, i64, i64, vp]
     lib.flce_beam_reorder.restype = ctypes.c_int
 
 
-from . import _check, _nbytes, _ptr, _stream, load_library  # noqa: E402  (defined before this module is imported)
+from . import _call_on, _check, _nbytes, _ptr, _stream, load_library  # noqa: E402  (defined before this module is imported)
 from .norm_ops import DTYPES  # noqa: E402
 
 
@@ -38,14 +40,19 @@ def flce_beam_select_workspace_size(B: int, K: int, V: int, M: int) -> int:
     return int(load_library().flce_beam_select_workspace_size(B, K, V, M))
 
 
+def _select_args(logits, scores, finished, pad_token, M, out_scores, out_parents, out_tokens, workspace, ws_bytes):
+    B, K, V = logits.shape
+    sb, sk, _ = logits.stride()
+    return (logits.data_ptr(), DTYPES[logits.dtype], B, K, V, max(sb, V) if B == 1 else sb, max(sk, V) if K == 1 else sk,
+            scores.data_ptr(), None if finished is None else finished.data_ptr(), int(pad_token), int(M), _ptr(out_scores),
+            _ptr(out_parents), _ptr(out_tokens), _ptr(workspace), ws_bytes)
+
+
 def flce_beam_select(logits, scores, finished, pad_token: int, M: int, out_scores, out_parents, out_tokens, workspace,
                      stream=None, raise_on_error: bool = True) -> int:
     """Call flce_beam_select on logits [B, K, V] with unit stride along V; returns the status."""
-    B, K, V = logits.shape
-    st = load_library().flce_beam_select(
-        _ptr(logits), DTYPES[logits.dtype], B, K, V, max(logits.stride(0), V) if B == 1 else logits.stride(0),
-        max(logits.stride(1), V) if K == 1 else logits.stride(1), _ptr(scores), _ptr(finished), int(pad_token), int(M),
-        _ptr(out_scores), _ptr(out_parents), _ptr(out_tokens), _ptr(workspace), _nbytes(workspace), _stream(stream))
+    st = load_library().flce_beam_select(*_select_args(logits, scores, finished, pad_token, M, out_scores, out_parents,
+                                                       out_tokens, workspace, _nbytes(workspace)), _stream(stream))
     if raise_on_error:
         _check(st, "flce_beam_select")
     return st
@@ -55,14 +62,13 @@ def flce_beam_reorder(states, parents, B: int, K: int, ld_parents: int | None = 
                       raise_on_error: bool = True) -> int:
     """Call flce_beam_reorder on a list of FlceBeamState; returns the status."""
     table = (FlceBeamState * len(states))(*states)
-    st = load_library().flce_beam_reorder(table, len(states), _ptr(parents), K if ld_parents is None else ld_parents, B, K,
+    st = load_library().flce_beam_reorder(ctypes.addressof(table), len(states), _ptr(parents), K if ld_parents is None else ld_parents, B, K,
                                           _stream(stream))
     if raise_on_error:
         _check(st, "flce_beam_reorder")
     return st
 
 
-@torch.no_grad()
 def beam_select(logits, scores, num: int | None = None, finished=None, pad_token: int = 0):
     """The ``num`` best continuations (K unless given) of each request: ``(scores, parents, tokens)``,
     float32 and int32 [B, num], best first.
@@ -97,20 +103,27 @@ def beam_select(logits, scores, num: int | None = None, finished=None, pad_token
     num = K if num is None else int(num)
     if K < 1 or V < 1 or not 1 <= num <= K * V:
         raise ValueError(f"num must be between 1 and the {K * V} candidates, got {num}")
-    with torch.cuda.device(dev):
-        out = torch.empty((B, num), dtype=torch.float32, device=dev)
-        parents, tokens = (torch.empty((B, num), dtype=torch.int32, device=dev) for _ in range(2))
-        if B > 0:
-            ws = torch.empty(flce_beam_select_workspace_size(B, K, V, num), dtype=torch.uint8, device=dev)
-            flce_beam_select(logits, scores.contiguous(), finished, pad_token, num, out, parents, tokens, ws)
+    out = torch.empty((B, num), dtype=torch.float32, device=dev)
+    parents, tokens = torch.empty((2, B, num), dtype=torch.int32, device=dev).unbind(0)
+    if B > 0:
+        lib = load_library()
+        need = lib.flce_beam_select_workspace_size(B, K, V, num)
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _call_on(dev, "flce_beam_select", lib.flce_beam_select,
+                 *_select_args(logits, scores if scores.is_contiguous() else scores.contiguous(), finished, pad_token, num,
+                               out, parents, tokens, ws, need))
     return out, parents, tokens
 
 
-def _state(src, dst, dim: int, K: int):
-    """The descriptor of a state: the dimensions but the beams' joined into one inner run of
-    bytes and at most four outer ones."""
-    size = src.element_size()
-    dims = [(n, a * size, b * size) for i, (n, a, b) in enumerate(zip(src.shape, src.stride(), dst.stride()))
+def _state(src, dst, dim: int):
+    """A state's flce_beam_state as its 17 words: the dimensions but the beams' joined into one
+    inner run of bytes and at most four outer ones."""
+    size, shape = src.element_size(), src.shape
+    if src.is_contiguous() and dst.is_contiguous():
+        inner = math.prod(shape[dim + 1:]) * size
+        step = inner * shape[dim]
+        return (src.data_ptr(), dst.data_ptr(), inner, inner, inner, math.prod(shape[:dim]), 1, 1, 1, step, 0, 0, 0, step, 0, 0, 0)
+    dims = [(n, a * size, b * size) for i, (n, a, b) in enumerate(zip(shape, src.stride(), dst.stride()))
             if i != dim and n != 1]
     dims.sort(key=lambda t: (t[1], t[2]))  # innermost first
     inner, outer = size, []
@@ -124,12 +137,10 @@ def _state(src, dst, dim: int, K: int):
     if len(outer) > 4:
         raise ValueError("a state has too many separate strides")
     outer += [(1, 0, 0)] * (4 - len(outer))
-    col = lambda i: (ctypes.c_int64 * 4)(*[t[i] for t in outer])  # noqa: E731
-    return FlceBeamState(src.data_ptr(), dst.data_ptr(), src.stride(dim) * size, dst.stride(dim) * size, inner, col(0),
-                         col(1), col(2))
+    return (src.data_ptr(), dst.data_ptr(), src.stride(dim) * size, dst.stride(dim) * size, inner,
+            *[t[i] for i in range(3) for t in outer])
 
 
-@torch.no_grad()
 def beam_reorder(states, parents, dims=0, out=None):
     """Moves the beams of every tensor in ``states``: along its dimension ``dims`` (a number, or one for
     each state), of size B * K, beam j of request b becomes what beam ``parents[b, j]`` of that
@@ -162,11 +173,12 @@ def beam_reorder(states, parents, dims=0, out=None):
             raise ValueError(f"a state of shape {tuple(s.shape)} has no {B * K} beams along dimension {dim}")
         if d.shape != s.shape or d.dtype != s.dtype or s.device != dev or d.device != dev:
             raise ValueError("out must have the states' shapes and types, and all be on the parents' device")
-        if any(n > 1 and st == 0 for n, st in zip(d.shape, d.stride())):
+        if not d.is_contiguous() and any(n > 1 and st == 0 for n, st in zip(d.shape, d.stride())):
             raise ValueError("an expanded tensor cannot be reordered into")
         if s.numel():
-            table.append(_state(s, d, dim % s.dim(), K))
+            table += _state(s, d, dim % s.dim())
     if table:
-        with torch.cuda.device(dev):
-            flce_beam_reorder(table, parents, B, K, parents.stride(0) if B > 1 else K)
+        words = array.array("q", table)
+        _call_on(dev, "flce_beam_reorder", load_library().flce_beam_reorder, words.buffer_info()[0], len(words) // 17,
+                 parents.data_ptr(), parents.stride(0) if B > 1 else K, B, K)
     return dst

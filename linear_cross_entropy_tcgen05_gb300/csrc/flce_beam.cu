@@ -392,7 +392,9 @@ template <typename T> cudaError_t launch_rows(const SelectParams& p, int nv, cud
 // ---------------------------------------------------------------------------------
 // Reordering
 // ---------------------------------------------------------------------------------
-constexpr int kStates = 64;      // tensors of one launch
+// Tensors of one launch. Their descriptors are kernel parameters, which are copied with the
+// launch: most calls have few.
+constexpr int kFewStates = 6, kManyStates = 64;
 constexpr int kOuter = 4;
 
 struct StateDesc {
@@ -407,8 +409,8 @@ struct StateDesc {
   int in_place;
 };
 
-struct ReorderParams {
-  StateDesc s[kStates];
+template <int CAP> struct ReorderParams {
+  StateDesc s[CAP];
   int count, B, K;
   const int32_t* parents;
   int64_t ld_parents;
@@ -437,8 +439,8 @@ __device__ __forceinline__ void reorder_column(const StateDesc& s, int K, int b,
     if (j < K && !(s.in_place && parent[j] == j)) *reinterpret_cast<W*>(dst + j * s.beam_dst) = v[j];
 }
 
-template <int KMAX>
-__global__ void __launch_bounds__(kBeamThreads) flce_beam_reorder_kernel(const __grid_constant__ ReorderParams p) {
+template <int KMAX, int CAP>
+__global__ void __launch_bounds__(kBeamThreads) flce_beam_reorder_kernel(const __grid_constant__ ReorderParams<CAP> p) {
   __shared__ int parent[kMaxBeams];
   int lo = 0, hi = p.count - 1;
   const int64_t tile = blockIdx.x;
@@ -470,6 +472,64 @@ __global__ void __launch_bounds__(kBeamThreads) flce_beam_reorder_kernel(const _
 flce_status bad(const char* what, const char* why) {
   api_note_error(what, why);
   return FLCE_ERR_INVALID_ARG;
+}
+
+template <int CAP>
+flce_status reorder_states(const flce_beam_state* states, int64_t count, const int32_t* parents, int64_t ld_parents,
+                           int64_t B, int64_t K, cudaStream_t stream) {
+  for (int64_t i = 0; i < count;) {
+    ReorderParams<CAP> p;
+    p.count = 0;
+    p.B = int(B);
+    p.K = int(K);
+    p.parents = parents;
+    p.ld_parents = ld_parents;
+    int64_t tiles = 0;
+    for (; i < count && p.count < CAP; ++i) {
+      const flce_beam_state& s = states[i];
+      StateDesc d{};
+      d.src = static_cast<const char*>(s.src);
+      d.dst = static_cast<char*>(s.dst);
+      d.beam_src = s.beam_stride_src;
+      d.beam_dst = s.beam_stride_dst;
+      d.in_place = s.src == s.dst;
+      uint64_t bits = uint64_t(reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst)) |
+                      uint64_t(s.beam_stride_src) | uint64_t(s.beam_stride_dst) | uint64_t(s.inner_bytes);
+      int64_t outer = 1;
+      for (int k = 0; k < kOuter; ++k) {
+        d.size[k] = s.outer_size[k];
+        d.stride_src[k] = s.outer_stride_src[k];
+        d.stride_dst[k] = s.outer_stride_dst[k];
+        if (s.outer_size[k] > 1) bits |= uint64_t(s.outer_stride_src[k]) | uint64_t(s.outer_stride_dst[k]);
+        outer *= s.outer_size[k];
+      }
+      d.width = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+      d.cols = s.inner_bytes / d.width;
+      if (outer == 0 || d.cols == 0) continue;
+      d.tiles = (outer * d.cols + kBeamThreads - 1) / kBeamThreads;
+      if (tiles + B * d.tiles > 0x7fffffff) {
+        if (p.count == 0) return FLCE_ERR_TOO_LARGE;
+        break;
+      }
+      d.first = tiles;
+      tiles += B * d.tiles;
+      p.s[p.count++] = d;
+    }
+    if (p.count == 0) continue;
+    const unsigned grid = unsigned(tiles);
+    if (K <= 4)
+      flce_beam_reorder_kernel<4, CAP><<<grid, kBeamThreads, 0, stream>>>(p);
+    else if (K <= 8)
+      flce_beam_reorder_kernel<8, CAP><<<grid, kBeamThreads, 0, stream>>>(p);
+    else if (K <= 16)
+      flce_beam_reorder_kernel<16, CAP><<<grid, kBeamThreads, 0, stream>>>(p);
+    else
+      flce_beam_reorder_kernel<32, CAP><<<grid, kBeamThreads, 0, stream>>>(p);
+    count_launch();
+    const flce_status st = api_cuda("beam reorder", cudaGetLastError());
+    if (st != FLCE_OK) return st;
+  }
+  return FLCE_OK;
 }
 
 struct SelectLayout {
@@ -582,59 +642,9 @@ flce_status flce_beam_reorder(const flce_beam_state* states, int64_t count, cons
     if ((st = api_check_memory(dev, "state", states[i].src)) != FLCE_OK) return st;
     if (states[i].dst != states[i].src && (st = api_check_memory(dev, "reordered state", states[i].dst)) != FLCE_OK) return st;
   }
-  for (int64_t i = 0; i < count;) {
-    ReorderParams p;
-    p.count = 0;
-    p.B = int(B);
-    p.K = int(K);
-    p.parents = parents;
-    p.ld_parents = ld_parents;
-    int64_t tiles = 0;
-    for (; i < count && p.count < kStates; ++i) {
-      const flce_beam_state& s = states[i];
-      StateDesc d{};
-      d.src = static_cast<const char*>(s.src);
-      d.dst = static_cast<char*>(s.dst);
-      d.beam_src = s.beam_stride_src;
-      d.beam_dst = s.beam_stride_dst;
-      d.in_place = s.src == s.dst;
-      uint64_t bits = uint64_t(reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst)) |
-                      uint64_t(s.beam_stride_src) | uint64_t(s.beam_stride_dst) | uint64_t(s.inner_bytes);
-      int64_t outer = 1;
-      for (int k = 0; k < kOuter; ++k) {
-        d.size[k] = s.outer_size[k];
-        d.stride_src[k] = s.outer_stride_src[k];
-        d.stride_dst[k] = s.outer_stride_dst[k];
-        if (s.outer_size[k] > 1) bits |= uint64_t(s.outer_stride_src[k]) | uint64_t(s.outer_stride_dst[k]);
-        outer *= s.outer_size[k];
-      }
-      d.width = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
-      d.cols = s.inner_bytes / d.width;
-      if (outer == 0 || d.cols == 0) continue;
-      d.tiles = (outer * d.cols + kBeamThreads - 1) / kBeamThreads;
-      if (tiles + B * d.tiles > 0x7fffffff) {
-        if (p.count == 0) return FLCE_ERR_TOO_LARGE;
-        break;
-      }
-      d.first = tiles;
-      tiles += B * d.tiles;
-      p.s[p.count++] = d;
-    }
-    if (p.count == 0) continue;
-    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    const unsigned grid = unsigned(tiles);
-    if (K <= 4)
-      flce_beam_reorder_kernel<4><<<grid, kBeamThreads, 0, stream>>>(p);
-    else if (K <= 8)
-      flce_beam_reorder_kernel<8><<<grid, kBeamThreads, 0, stream>>>(p);
-    else if (K <= 16)
-      flce_beam_reorder_kernel<16><<<grid, kBeamThreads, 0, stream>>>(p);
-    else
-      flce_beam_reorder_kernel<32><<<grid, kBeamThreads, 0, stream>>>(p);
-    count_launch();
-    if ((st = api_cuda("beam reorder", cudaGetLastError())) != FLCE_OK) return st;
-  }
-  return FLCE_OK;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  return count <= kFewStates ? reorder_states<kFewStates>(states, count, parents, ld_parents, B, K, stream)
+                             : reorder_states<kManyStates>(states, count, parents, ld_parents, B, K, stream);
 }
 
 }  // extern "C"

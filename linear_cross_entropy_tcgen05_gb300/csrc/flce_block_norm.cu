@@ -62,9 +62,11 @@ BwdPlan bwd_plan(int64_t N, int64_t D, int64_t gate_rows, int max_threads) {
   const int64_t need = cdiv(cdiv(N, 4), p.shape.rows_per_block);
   p.blocks = blocks < need ? blocks : need;
   const int64_t workers = p.blocks * p.shape.rows_per_block;
+  // a worker takes one to four chunks: the split whose longest worker is shortest
   int64_t best = -1;
-  const int64_t most = p.group_rows < 4 * cdiv(workers, groups) ? p.group_rows : 4 * cdiv(workers, groups);
-  for (int64_t k = 1; k <= most; ++k) {
+  for (int64_t rounds = 1; rounds <= 4; ++rounds) {
+    int64_t k = rounds * workers / groups;
+    k = k < 1 ? rounds : k < p.group_rows ? k : p.group_rows;
     const int64_t rows = cdiv(p.group_rows, k), per = cdiv(p.group_rows, rows);
     const int64_t cost = cdiv(groups * per, workers) * rows;
     if (best < 0 || cost < best) {
@@ -72,6 +74,7 @@ BwdPlan bwd_plan(int64_t N, int64_t D, int64_t gate_rows, int max_threads) {
       p.chunks_per_group = per;
       p.chunk_rows = rows;
     }
+    if (groups == 1) break;  // one chunk a worker is even already
   }
   p.chunks = groups * p.chunks_per_group;
   p.gate_parts = gate_rows > 0 && gate_rows != N && p.chunks_per_group > 1;

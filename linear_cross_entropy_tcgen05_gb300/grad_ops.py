@@ -3,6 +3,7 @@ tensors, ``clip_grad_norm_`` parameters; ``flce_clip_grad_norm`` marshals to the
 (include/flce.h), which has the formulas."""
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 
@@ -19,7 +20,7 @@ def declare(lib) -> None:
     lib.flce_clip_grad_norm.restype = ctypes.c_int
 
 
-from . import _check, _nbytes, _ptr, _stream, load_library  # noqa: E402  (defined before this module is imported)
+from . import _call_on, _check, _nbytes, _ptr, _stream, load_library  # noqa: E402  (defined before this module is imported)
 from .norm_ops import DTYPES  # noqa: E402
 
 
@@ -32,14 +33,17 @@ def flce_clip_grad_norm(tensors, total_norm, workspace, max_norm: float, norm_ty
                         grad_scale: float = 1.0, stream=None, raise_on_error: bool = True) -> int:
     """Call flce_clip_grad_norm; ``tensors`` is a list of (gradient address, output address or 0,
     elements, dtype, output dtype) with dtypes as in flce_dtype. Returns the status."""
-    # an entry of flce_grad_tensor is two addresses, a size and two 32-bit types: four 64-bit words
-    words = [w for g, o, n, dt, odt in tensors for w in (g, o, n, dt | odt << 32)]
-    table = (ctypes.c_int64 * len(words))(*words)
-    st = load_library().flce_clip_grad_norm(table, len(tensors), max_norm, norm_type, eps, grad_scale, _ptr(total_norm),
-                                            _ptr(workspace), _nbytes(workspace), _stream(stream))
+    table = _table([w for g, o, n, dt, odt in tensors for w in (g, o, n, dt | odt << 32)])
+    st = load_library().flce_clip_grad_norm(table.buffer_info()[0], len(tensors), max_norm, norm_type, eps, grad_scale,
+                                            _ptr(total_norm), _ptr(workspace), _nbytes(workspace), _stream(stream))
     if raise_on_error:
         _check(st, "flce_clip_grad_norm")
     return st
+
+
+def _table(words) -> array.array:
+    """An array of flce_grad_tensor: two addresses, a size and two 32-bit types, four 64-bit words."""
+    return array.array("q", words)
 
 
 def _dense(t) -> bool:
@@ -59,7 +63,7 @@ def _run(grads, max_norm, norm_type, eps, grad_scale, out):
     dev = first.device
     if dev.type != "cuda":
         raise ValueError("gradients must be CUDA tensors")
-    entries = []
+    words = []
     for i, g in enumerate(grads):
         dt = DTYPES.get(g.dtype)
         if dt is None:
@@ -69,26 +73,28 @@ def _run(grads, max_norm, norm_type, eps, grad_scale, out):
         if not g.is_contiguous() and not _dense(g):
             raise ValueError("a gradient must fill one run of memory (no gaps, nothing expanded)")
         p = g.data_ptr()
-        if out is grads:
-            entries.append((p, p, g.numel(), dt, dt))
-        elif out is None:
-            entries.append((p, 0, g.numel(), dt, dt))
+        if out is None:
+            words += (p, 0, g.numel(), dt)
+        elif out is grads:
+            words += (p, p, g.numel(), dt | dt << 32)
         else:
             o = out[i]
-            if o.dtype not in DTYPES:
+            odt = DTYPES.get(o.dtype)
+            if odt is None:
                 raise TypeError(f"out must be bfloat16, float16 or float32, got {o.dtype}")
             if o.device != dev or o.shape != g.shape or (o.stride() != g.stride() and not
                                                          (g.is_contiguous() and o.is_contiguous())):
                 raise ValueError("out must have the gradients' shapes, strides and device")
-            entries.append((p, o.data_ptr(), g.numel(), dt, DTYPES[o.dtype]))
-    with torch.cuda.device(dev):
-        total = torch.empty((), dtype=torch.float32, device=dev)
-        ws = torch.empty(flce_clip_grad_norm_workspace_size(len(entries)), dtype=torch.uint8, device=dev)
-        flce_clip_grad_norm(entries, total, ws, max_norm, norm_type, eps, grad_scale)
+            words += (p, o.data_ptr(), g.numel(), dt | odt << 32)
+    lib, table = load_library(), _table(words)
+    total = torch.empty((), dtype=torch.float32, device=dev)
+    need = lib.flce_clip_grad_norm_workspace_size(len(grads))
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call_on(dev, "flce_clip_grad_norm", lib.flce_clip_grad_norm, table.buffer_info()[0], len(grads), max_norm, norm_type,
+             eps, grad_scale, total.data_ptr(), ws.data_ptr(), need)
     return total
 
 
-@torch.no_grad()
 def clip_grad_norm(grads, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, grad_scale: float = 1.0, out=None):
     """Scales all ``grads`` (a list of tensors) by ``grad_scale * min(1, max_norm / (total + eps))``
     and returns ``total``, the norm of all of them together after ``grad_scale``, as a 0-dim
@@ -109,7 +115,6 @@ def clip_grad_norm(grads, max_norm: float, norm_type: float = 2.0, eps: float = 
     return _run(grads, max_norm, norm_type, eps, grad_scale, grads if out is None else out)
 
 
-@torch.no_grad()
 def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, grad_scale: float = 1.0):
     """``clip_grad_norm`` in place on the ``.grad`` of ``parameters`` (a tensor or an iterable);
     those without one are passed over."""
@@ -118,7 +123,6 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0, eps: fl
     return clip_grad_norm([p.grad for p in parameters if p.grad is not None], max_norm, norm_type, eps, grad_scale)
 
 
-@torch.no_grad()
 def grad_norm(grads, norm_type: float = 2.0, grad_scale: float = 1.0):
     """The norm of all ``grads`` together, which stay as they are."""
     grads = list(grads)

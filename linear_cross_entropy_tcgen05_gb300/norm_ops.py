@@ -45,7 +45,7 @@ def declare(lib) -> None:
     lib.flce_block_norm_backward.restype = i
 
 
-from . import _check, _nbytes, _ptr, _stream, load_library  # noqa: E402  (defined before this module is imported)
+from . import _call_on, _check, _nbytes, _ptr, _stream, load_library  # noqa: E402  (defined before this module is imported)
 
 
 def flce_block_norm_workspace_size(N: int, D: int, gate_rows: int = 0) -> int:
@@ -165,11 +165,8 @@ def _forward(d, x, h_dtype, want_y: bool, want_stats: bool):
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_y else None
     stats = torch.empty((d.N, 4), dtype=torch.float32, device=x.device) if want_stats else None
     if d.N > 0:
-        if x.device.index == torch.cuda.current_device():
-            flce_block_norm_forward(d, h, y, stats)
-        else:  # the library works on the current device and the current stream: make them x's
-            with torch.cuda.device(x.device):
-                flce_block_norm_forward(d, h, y, stats)
+        _call_on(x.device, "flce_block_norm_forward", load_library().flce_block_norm_forward, ctypes.byref(d), h.data_ptr(),
+                 None if y is None else y.data_ptr(), None if stats is None else stats.data_ptr())
     return h, y, stats
 
 
@@ -191,34 +188,44 @@ class BlockNormFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dy):
-        x, weight, bias, post_weight, post_bias, gate, h, stats = ctx.saved_tensors
-        want = ctx.needs_input_grad
         if dh is None and dy is None:
             return (None,) * 12
-        with torch.cuda.device(x.device):
-            D = x.shape[-1]
-            d = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
-            out = {"dx": torch.empty_like(x, memory_format=torch.contiguous_format) if want[0] else None,
-                   "dresidual": torch.empty_like(h) if want[1] else None}
-            for i, (name, t) in enumerate((("dweight", weight), ("dbias", bias), ("dpost_weight", post_weight),
-                                           ("dpost_bias", post_bias), ("dgate", gate))):
-                out[name] = torch.empty(t.shape, dtype=t.dtype, device=t.device) if want[2 + i] else None
-            if d.N == 0:
-                for t in out.values():
-                    if t is not None:
-                        t.zero_()
-            else:
-                # gradients may come with any strides (expanded ones, say): rows are made of those
-                dh, dy = (t if t is None else t.reshape(-1, D) for t in (dh, dy))
-                dh, dy = (t if t is None or (t.stride(1) == 1 and _row_stride(t) >= D) else t.contiguous()
-                          for t in (dh, dy))
-                dh = dh if dh is None or dh.dtype == h.dtype else dh.to(h.dtype)
-                dy = dy if dy is None or dy.dtype == x.dtype else dy.to(x.dtype)
-                ws = torch.empty(flce_block_norm_workspace_size(d.N, D, d.gate_rows), dtype=torch.uint8, device=x.device)
-                grads = FlceBlockNormGrads(**{k: _ptr(v) for k, v in out.items()})
-                flce_block_norm_backward(d, h, stats, dh, dy, grads, ws)
-        return (out["dx"], out["dresidual"], out["dweight"], out["dbias"], out["dpost_weight"], out["dpost_bias"],
-                out["dgate"], None, None, None, None, None)
+        x, weight, bias, post_weight, post_bias, gate, h, stats = ctx.saved_tensors
+        want, dev, D = ctx.needs_input_grad, x.device, x.shape[-1]
+        d = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
+        grads, out = FlceBlockNormGrads(), [None] * 12
+        for i, name, t in ((0, "dx", x), (1, "dresidual", h), (2, "dweight", weight), (3, "dbias", bias),
+                           (4, "dpost_weight", post_weight), (5, "dpost_bias", post_bias), (6, "dgate", gate)):
+            if want[i]:
+                out[i] = torch.empty(t.shape, dtype=t.dtype, device=dev)
+                setattr(grads, name, out[i].data_ptr())
+        if d.N == 0:
+            for t in out:
+                if t is not None:
+                    t.zero_()
+            return tuple(out)
+        dh, ld_dh, _dh = _upstream(dh, D, h.dtype)
+        dy, ld_dy, _dy = _upstream(dy, D, x.dtype)
+        lib = load_library()
+        need = lib.flce_block_norm_workspace_size(d.N, D, d.gate_rows)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _call_on(dev, "flce_block_norm_backward", lib.flce_block_norm_backward, ctypes.byref(d), h.data_ptr(),
+                 stats.data_ptr(), dh, ld_dh, dy, ld_dy, ctypes.byref(grads), ws.data_ptr(), need)
+        return tuple(out)
+
+
+def _upstream(t, D: int, dtype):
+    """Address, row stride and tensor of an upstream gradient as rows of D columns; one that is
+    expanded, or of another type, is copied."""
+    if t is None:
+        return None, 0, None
+    if t.dtype != dtype:
+        t = t.to(dtype)
+    if t.dim() != 2:
+        t = t.reshape(-1, D)
+    if (t.stride(1) != 1 and D > 1) or _row_stride(t) < D:
+        t = t.contiguous()
+    return t.data_ptr(), _row_stride(t), t
 
 
 def block_norm(x, residual=None, weight=None, *, bias=None, post_weight=None, post_bias=None, gate=None,
@@ -239,7 +246,7 @@ def block_norm(x, residual=None, weight=None, *, bias=None, post_weight=None, po
     stream the backward pass reads the rounded h.
     """
     args = (x, residual, weight, bias, post_weight, post_bias, gate)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args):
+    if torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in args]):
         return BlockNormFunction.apply(*args, norm, eps, scale, gate_activation, weight_offset)
     d = _describe(*args, norm, eps, scale, gate_activation, weight_offset)
     h, y, _ = _forward(d, x, x.dtype if residual is None else residual.dtype, weight is not None, False)

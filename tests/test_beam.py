@@ -29,7 +29,7 @@ def _reorder(src=0x10000, dst=0x20000, inner=64, sizes=(1, 1, 1, 1), ss=64, sd=6
     a = ctypes.c_int64 * 4
     st = flce.FlceBeamState(src, dst, ss, sd, inner, a(*sizes), a(*os), a(*od))
     t = (flce.FlceBeamState * 1)(st) if table else None
-    return flce.load_library().flce_beam_reorder(t, count, parents, ld, B, K, None)
+    return flce.load_library().flce_beam_reorder(t and ctypes.addressof(t), count, parents, ld, B, K, None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -54,20 +54,27 @@ def test_workspace_size():
 
 
 def test_state_descriptors():
-    from linear_cross_entropy_tcgen05_gb300.beam_ops import _state
+    from linear_cross_entropy_tcgen05_gb300.beam_ops import _state as words
+
+    def _state(src, dst, dim):
+        w = words(src, dst, dim)
+        assert len(w) * 8 == ctypes.sizeof(flce.FlceBeamState)
+        return flce.FlceBeamState.from_buffer_copy((ctypes.c_int64 * 17)(*w))
+
     a = torch.zeros(3, 8, 5, 16, 4)  # layers, beams, heads, positions, columns
-    s = _state(a, a, 1, 4)
+    s = _state(a, a, 1)
     assert s.inner_bytes == 5 * 16 * 4 * 4 and list(s.outer_size) == [3, 1, 1, 1] and s.beam_stride_src == 5 * 16 * 4 * 4
-    s = _state(a[:, :, :, :7], a[:, :, :, :7], 1, 4)  # the first positions alone
+    assert s.outer_stride_src[0] == s.outer_stride_dst[0] == 8 * 5 * 16 * 4 * 4
+    s = _state(a[:, :, :, :7], a[:, :, :, :7], 1)  # the first positions alone
     assert s.inner_bytes == 7 * 4 * 4 and list(s.outer_size) == [5, 3, 1, 1]
     assert list(s.outer_stride_src)[:2] == [16 * 4 * 4, 8 * 5 * 16 * 4 * 4]
-    s = _state(a.permute(4, 3, 2, 1, 0), a.permute(4, 3, 2, 1, 0), 3, 4)
+    s = _state(a.permute(4, 3, 2, 1, 0), a.permute(4, 3, 2, 1, 0), 3)
     assert s.inner_bytes == 5 * 16 * 4 * 4 and list(s.outer_size) == [3, 1, 1, 1]
     b = torch.zeros(3, 8, 5, 16, 4).permute(0, 1, 3, 2, 4).contiguous().permute(0, 1, 3, 2, 4)  # another layout for out
-    s = _state(a, b, 1, 4)
+    s = _state(a, b, 1)
     assert s.inner_bytes == 4 * 4 and sorted(s.outer_size) == [1, 3, 5, 16]
     f = torch.zeros(8, dtype=torch.bool)
-    s = _state(f, f, 0, 4)
+    s = _state(f, f, 0)
     assert s.inner_bytes == 1 and list(s.outer_size) == [1, 1, 1, 1] and s.beam_stride_src == 1
 
 
