@@ -54,11 +54,12 @@ __host__ __device__ constexpr int bn_shared_params(int feat, bool backward) {
   if (!backward) return feat & BN_GATE ? 4 : 2;
   return feat & BN_POST ? (feat & BN_GATE ? 3 : 2) : 1;
 }
-// Values that each thread of a backward kernel keeps there for itself: a gate, the sum of its
-// gradient and a bias's (with all of them in registers the kernel spills: 386 us against 210 at
-// N = 16384, D = 2304).
+// Values that each thread of a backward kernel keeps there for itself: a gate and the sum of its
+// gradient, and sums of the biases' (with all of them in registers the kernel spills, to local
+// memory for which there is no L1 left: 386 us against 210 at N = 16384, D = 2304).
 __host__ __device__ constexpr int bn_own_params(int feat, bool backward) {
-  return backward && (feat & BN_POST) && (feat & BN_GATE) ? (feat & BN_FULL ? 3 : 2) : 0;
+  if (!backward || !(feat & BN_POST)) return 0;
+  return feat & BN_GATE ? (feat & BN_FULL ? 4 : 2) : (feat & BN_FULL ? 1 : 0);
 }
 
 // Rows that a row group works on together at most: they share the latency of their sums. (Four in

@@ -161,63 +161,104 @@ struct RowSum {
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * (32 / NV));
     }
-    if (cluster > 1)
-      exchange(v);
-    else
-      turn ^= 1;
+    if (cluster > 1) exchange(v);
+    turn ^= 1;
   }
 
   // Of the warps' column sums s and squared distances q from their own means (value i in lanes
   // i * (32 / NR) ...): the rows' means and the squared distances from those. A warp has 256
-  // columns, but for one that has the row's last `part` ones.
+  // columns, but for one that has the row's last `part` ones. With c the first warp's mean, the
+  // distances are sum q_w + n_w (m_w - c)^2, less n (mean - c)^2: one pass over the warps, and
+  // c is near enough to the mean that the difference loses nothing to speak of.
   template <int NR> __device__ __forceinline__ void merge(float s, float q, float inv_d, float (&mean)[NR], float (&dist)[NR]) {
     static_assert(2 * NR <= kMaxValues, "values of a sum");
-    float* b = buf + turn * kWords;
     if (nw > 1) {
-      if (lane % (32 / NR) == 0) reinterpret_cast<float2*>(b)[warp * NR + lane / (32 / NR)] = make_float2(s, q);
+      float* b = buf + turn * kWords;
+      if (lane % (32 / NR) == 0) {
+        const int i = lane / (32 / NR);
+        float* at = b + warp * 2 * NR + (i / 2) * 4 + i % 2;
+        at[0] = s;
+        at[2] = q;
+      }
       named_barrier_sync(uint32_t(bar), uint32_t(threads));
+      float2 total[NR / 2], far[NR / 2], c[NR / 2];
+      const float first_inv = full > 0 ? 1.f / 256.f : part_inv;
 #pragma unroll
-      for (int i = 0; i < NR; ++i) mean[i] = dist[i] = 0.f;
-#pragma unroll 4
-      for (int w = 0; w < nw; ++w)
-#pragma unroll
-        for (int i = 0; i < NR; i += 2) {
-          const float4 o = reinterpret_cast<const float4*>(b + w * 2 * NR)[i / 2];
-          mean[i] += o.x;
-          mean[i + 1] += o.z;
-        }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NR; ++i) mean[i] = __shfl_sync(0xffffffffu, s, i * (32 / NR));
-    }
-    if (cluster > 1) exchange(mean);
-#pragma unroll
-    for (int i = 0; i < NR; ++i) mean[i] *= inv_d;
-    if (nw > 1) {
+      for (int i = 0; i < NR / 2; ++i) {
+        const float4 o = reinterpret_cast<const float4*>(b)[i];
+        total[i] = far[i] = both(0.f);
+        c[i] = mul2(make_float2(o.x, o.y), both(-first_inv));
+      }
       auto add = [&](int w, float n, float inv_n) {
 #pragma unroll
-        for (int i = 0; i < NR; i += 2) {
-          const float4 o = reinterpret_cast<const float4*>(b + w * 2 * NR)[i / 2];
-          const float a = fmaf(o.x, inv_n, -mean[i]), c = fmaf(o.z, inv_n, -mean[i + 1]);
-          dist[i] += fmaf(n * a, a, o.y);
-          dist[i + 1] += fmaf(n * c, c, o.w);
+        for (int i = 0; i < NR / 2; ++i) {
+          const float4 o = reinterpret_cast<const float4*>(b + w * 2 * NR)[i];
+          const float2 m = fma2(make_float2(o.x, o.y), both(inv_n), c[i]);
+          total[i] = add2(total[i], make_float2(o.x, o.y));
+          far[i] = add2(far[i], fma2(mul2(m, both(n)), m, make_float2(o.z, o.w)));
         }
       };
-#pragma unroll 4
+#pragma unroll 3
       for (int w = 0; w < full; ++w) add(w, 256.f, 1.f / 256.f);
       if (part > 0) add(full, float(part), part_inv);
+      const float n = 256.f * float(full) + float(part), inv_n = cluster > 1 ? (n > 0.f ? 1.f / n : 0.f) : inv_d;
+#pragma unroll
+      for (int i = 0; i < NR / 2; ++i) {
+        const float2 m = fma2(total[i], both(inv_n), c[i]);  // this block's mean, less c
+        far[i] = fma2(mul2(m, both(-n)), m, far[i]);
+        mean[2 * i] = total[i].x;
+        mean[2 * i + 1] = total[i].y;
+        dist[2 * i] = far[i].x;
+        dist[2 * i + 1] = far[i].y;
+      }
     } else {
       // one warp: its mean is the row's
 #pragma unroll
-      for (int i = 0; i < NR; ++i) dist[i] = __shfl_sync(0xffffffffu, q, i * (32 / NR));
+      for (int i = 0; i < NR; ++i) {
+        mean[i] = __shfl_sync(0xffffffffu, s, i * (32 / NR));
+        dist[i] = __shfl_sync(0xffffffffu, q, i * (32 / NR));
+      }
     }
-    if (cluster > 1)
-      exchange(dist);
-    else
-      turn ^= 1;
+    if (cluster > 1) {
+      float v[2 * NR];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        v[i] = mean[i];
+        v[NR + i] = dist[i];
+      }
+      const float* c = publish(v);
+      float all[NR];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) all[i] = dist[i] = 0.f;
+      for (int r = 0; r < cluster; ++r)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) all[i] += c[kMaxValues * r + i];
+      for (int r = 0; r < cluster; ++r) {
+        const float n = block_columns(r), inv_n = n > 0.f ? 1.f / n : 0.f;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const float d = c[kMaxValues * r + i] * inv_n - all[i] * inv_d;
+          dist[i] += c[kMaxValues * r + NR + i] + n * d * d;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NR; ++i) mean[i] = all[i];
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      mean[i] *= inv_d;
+      dist[i] = fmaxf(dist[i], 0.f);
+    }
+    turn ^= 1;
   }
-  // Sums over the blocks of the cluster; takes the next scratch buffer.
-  template <int NV> __device__ __forceinline__ void exchange(float (&v)[NV]) {
+  // Columns of the row that block r of the cluster has.
+  int D;
+  __device__ __forceinline__ float block_columns(int r) const {
+    const int most = 8 * threads, left = D - r * most;
+    return float(left < 0 ? 0 : left < most ? left : most);
+  }
+  // Shows this block's values to the blocks of the cluster, and returns all blocks' values.
+  template <int NV> __device__ __forceinline__ const float* publish(const float (&v)[NV]) {
     float* c = clus + turn * (kMaxValues * kBnMaxCluster);
     const int tid = warp * 32 + lane;
     if (tid < cluster) {
@@ -226,12 +267,16 @@ struct RowSum {
       for (int i = 0; i < NV; ++i) st_shared_cluster_u32(at + 4 * i, __float_as_uint(v[i]));
     }
     cluster_sync_all();
+    return c;
+  }
+  // Sums over the blocks of the cluster.
+  template <int NV> __device__ __forceinline__ void exchange(float (&v)[NV]) {
+    const float* c = publish(v);
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = 0.f;
     for (int r = 0; r < cluster; ++r)
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] += c[kMaxValues * r + i];
-    turn ^= 1;
   }
   int full, part;  // warps of this block with 256 columns, and the columns of the one after them
   float part_inv;
@@ -298,39 +343,20 @@ __device__ __forceinline__ void load_weight(const void* w, int dt, float off, in
     f[i] = make_float2(col + 2 * i < D ? f[i].x + off : 0.f, col + 2 * i + 1 < D ? f[i].y + off : 0.f);
 }
 
-// A parameter in shared memory, for the kernels with more of them than registers: two planes of
-// 16 bytes a thread of a row.
-struct SharedParam {
-  const float4* at;
-  int plane;
-  __device__ __forceinline__ void get(float2 (&f)[4]) const {
-    const float4 a = at[0], b = at[plane];
-    f[0] = make_float2(a.x, a.y);
-    f[1] = make_float2(a.z, a.w);
-    f[2] = make_float2(b.x, b.y);
-    f[3] = make_float2(b.z, b.w);
-  }
-};
-__device__ __forceinline__ SharedParam share_param(char* smem, int index, const RowThread& r, int threads_per_row,
-                                                   const float2 (&f)[4]) {
-  float4* at = reinterpret_cast<float4*>(smem) + 2 * index * threads_per_row + r.t;
-  if (r.group == 0) {
-    at[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-    at[threads_per_row] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
-  }
-  return SharedParam{at, threads_per_row};
+// Eight values in shared memory, in two planes: a parameter's for a thread of a row, in the
+// kernels with more of them than registers, or a thread's own (a gate, a sum). Offsets are 32-bit
+// and made where they are used: a spilled register costs more than they do.
+__device__ __forceinline__ void shared_get(const char* smem, int at, int plane, float2 (&f)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(smem + at), b = *reinterpret_cast<const float4*>(smem + at + plane);
+  f[0] = make_float2(a.x, a.y);
+  f[1] = make_float2(a.z, a.w);
+  f[2] = make_float2(b.x, b.y);
+  f[3] = make_float2(b.z, b.w);
 }
-
-// Eight values of a thread's own in shared memory (a gate, the sum of its gradient).
-struct OwnParam {
-  float4* at;
-  int plane;
-  __device__ __forceinline__ void get(float2 (&f)[4]) const { SharedParam{at, plane}.get(f); }
-  __device__ __forceinline__ void set(const float2 (&f)[4]) const {
-    at[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-    at[plane] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
-  }
-};
+__device__ __forceinline__ void shared_set(char* smem, int at, int plane, const float2 (&f)[4]) {
+  *reinterpret_cast<float4*>(smem + at) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  *reinterpret_cast<float4*>(smem + at + plane) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+}
 
 __device__ __forceinline__ float sum8(const float2 (&v)[4]) {
   const float2 s = add2(add2(v[0], v[1]), add2(v[2], v[3]));
@@ -358,6 +384,7 @@ constexpr int kRowSumWords = 2 * RowSum::kMaxValues * kBnMaxCluster + kBnMaxThre
 
 __device__ __forceinline__ RowSum row_sum(float* scratch, const RowThread& r, int threads_per_row, int cluster, int D) {
   RowSum rs;
+  rs.D = D;
   const int cols = D - (r.col - 8 * r.t), most = 8 * threads_per_row;  // columns from this block's first on
   rs.full = (cols < 0 ? 0 : cols < most ? cols : most) / 256;
   rs.part = cols < 0 || cols >= most ? 0 : cols % 256;
@@ -377,9 +404,9 @@ __device__ __forceinline__ RowSum row_sum(float* scratch, const RowThread& r, in
 }
 
 // Means (0 for the RMS norm) and 1 / sqrt(mean of the squared distances from it + eps) of R
-// rows; get(r, v) gives a row's eight values. A layer norm's warps first take the mean m_w and
-// the squared distances q_w from it over their own n_w columns; then q = sum q_w + n_w (m_w -
-// m)^2, so one sum over the row's warps is enough and a large common offset costs no precision.
+// rows; get(r, v) gives a row's eight values. A layer norm's warps first take the mean and the
+// squared distances from it over their own columns, so one sum over the row's warps is enough
+// and a large common offset costs no precision.
 template <int R, bool VEC, bool LAYER, typename F>
 __device__ __forceinline__ void row_stats(F&& get, int col, int D, bool layer, float eps, float inv_d, RowSum& rs,
                                           float (&mean)[R], float (&rstd)[R]) {
@@ -422,7 +449,7 @@ __device__ __forceinline__ void row_stats(F&& get, int col, int D, bool layer, f
 // What a kernel's code has: the norm after the block, a gate, and (FULL) the means of layer norms
 // and biases. A kernel takes what has less at run time.
 template <typename TX, typename TR, bool VEC, int FEAT>
-__global__ void __launch_bounds__(kBnMaxThreads)
+__global__ void __launch_bounds__(kBnMaxThreads, 1)
     flce_block_norm_forward_kernel(const __grid_constant__ BlockNormParams p, int threads_per_row, int cluster, int batches, int per) {
   constexpr int R = kBnRows;
   constexpr bool POST = (FEAT & BN_POST) != 0, GATE = (FEAT & BN_GATE) != 0, FULL = (FEAT & BN_FULL) != 0;
@@ -466,7 +493,12 @@ __global__ void __launch_bounds__(kBnMaxThreads)
   // c: what a row's value after the first norm is multiplied by, w1 scale act(gate), and c_b what
   // is added, b1 scale act(gate)
   float2 w2[4], c[4], c_b[4];
-  SharedParam s_w1{}, s_b1{}, s_w2{}, s_b2{};
+  const int t16 = 16 * r0.t, plane = 16 * threads_per_row;  // a parameter's values for this thread
+  auto param = [&](int index, float2 (&f)[4]) FLCE_INLINE { shared_get(ring_smem, t16 + 2 * index * plane, plane, f); };
+  auto set_param = [&](int index, const float2 (&f)[4]) FLCE_INLINE {
+    if (r0.group == 0) shared_set(ring_smem, t16 + 2 * index * plane, plane, f);
+  };
+  constexpr int kW2 = 0, kB2 = 1, kW1 = 2, kB1 = 3;
   load_weight<VEC>(p.w1, p.w1_dt, p.w_off, col, D, c);
   load_weight<VEC>(p.w2, p.w2_dt, p.w_off, col, D, w2);
 #pragma unroll
@@ -477,11 +509,11 @@ __global__ void __launch_bounds__(kBnMaxThreads)
     for (int i = 0; i < 4; ++i) c_b[i] = mul2(c_b[i], both(p.scale));
     float2 b2[4];
     load_weight<VEC>(p.b2, p.b2_dt, 0.f, col, D, b2);
-    s_w2 = share_param(ring_smem, 0, r0, threads_per_row, w2);
-    s_b2 = share_param(ring_smem, 1, r0, threads_per_row, b2);
+    set_param(kW2, w2);
+    set_param(kB2, b2);
     if (GATE) {
-      s_w1 = share_param(ring_smem, 2, r0, threads_per_row, c);
-      s_b1 = share_param(ring_smem, 3, r0, threads_per_row, c_b);
+      set_param(kW1, c);
+      set_param(kB1, c_b);
     }
     __syncthreads();
   }
@@ -492,8 +524,8 @@ __global__ void __launch_bounds__(kBnMaxThreads)
   }
   auto set_gate = [&](const float2(&a)[4]) FLCE_INLINE {
     if (FULL) {
-      s_w1.get(c);
-      s_b1.get(c_b);
+      param(kW1, c);
+      param(kB1, c_b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         c[i] = mul2(c[i], a[i]);
@@ -608,8 +640,8 @@ __global__ void __launch_bounds__(kBnMaxThreads)
     if (pre) {
       float2 b2[4];
       if (FULL) {
-        s_w2.get(w2);
-        s_b2.get(b2);
+        param(kW2, w2);
+        param(kB2, b2);
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -642,7 +674,7 @@ __global__ void __launch_bounds__(kBnMaxThreads)
 // r g - r mean(g) - (v - m) r^3 mean(g (v - m)): it is computed in the last form, from the row's
 // own values, so a norm costs two sums in which no normalised row is formed.
 template <typename TX, typename TR, bool VEC, int FEAT>
-__global__ void __launch_bounds__(kBnMaxThreads)
+__global__ void __launch_bounds__(kBnMaxThreads, 1)
     flce_block_norm_backward_kernel(const __grid_constant__ BlockNormParams p, int threads_per_row, int cluster, int batches, int per) {
   constexpr int R = kBnRows;
   constexpr bool POST = (FEAT & BN_POST) != 0, GATE = (FEAT & BN_GATE) != 0, FULL = (FEAT & BN_FULL) != 0;
@@ -650,8 +682,8 @@ __global__ void __launch_bounds__(kBnMaxThreads)
   extern __shared__ __align__(16) char ring_smem[];
   constexpr int kX = 0, kY = sizeof(TX) / 2, kH = 2 * kY, kDh = kH + sizeof(TR) / 2, kG = kDh + sizeof(TR) / 2;  // planes
   constexpr int kParams = bn_shared_params(FEAT, true);
-  constexpr bool OWN = POST && GATE;  // the gate and the sum of its gradient are in shared memory,
-  constexpr bool OWN_B = OWN && FULL; // and one bias's sum
+  // in shared memory: the gate and the sum of its gradient, and the biases' sums
+  constexpr bool OWN = POST && GATE, OWN_B1 = POST && FULL, OWN_B2 = POST && GATE && FULL;
   const RowThread r0 = row_thread(threads_per_row, cluster);
   RowSum rs = row_sum(scratch, r0, threads_per_row, cluster, p.D);
   const int col = r0.col, D = p.D;
@@ -714,12 +746,24 @@ __global__ void __launch_bounds__(kBnMaxThreads)
     stat_slot = stat_slot + 1 == batches ? 0 : stat_slot + 1;
   };
   if constexpr (VEC) {
-    ring.init(ring_smem + kParams * 32 * threads_per_row + (OWN ? (OWN_B ? 96 : 64) * int(blockDim.x) : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
+    ring.init(ring_smem + kParams * 32 * threads_per_row + bn_own_params(FEAT, true) * 32 * int(blockDim.x), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
     for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
   }
   if (cluster > 1) cluster_sync_all();
   float2 w1[4], w2[4], b1[4], a[4], dw1[4], db1[4], dw2[4], db2[4], dg[4];
-  SharedParam s_w1{}, s_w2{}, s_b1{};
+  const int t16 = 16 * r0.t, plane = 16 * threads_per_row;  // a parameter's values for this thread
+  auto param = [&](int index, float2 (&f)[4]) FLCE_INLINE { shared_get(ring_smem, t16 + 2 * index * plane, plane, f); };
+  auto set_param = [&](int index, const float2 (&f)[4]) FLCE_INLINE {
+    if (r0.group == 0) shared_set(ring_smem, t16 + 2 * index * plane, plane, f);
+  };
+  constexpr int kW2 = 0, kW1 = 1, kB1 = 2;
+  // the thread's own values follow the parameters
+  const int own_plane = 16 * int(blockDim.x), own_at = 2 * kParams * plane + 16 * int(threadIdx.x);
+  auto own = [&](int index, float2 (&f)[4]) FLCE_INLINE { shared_get(ring_smem, own_at + 2 * index * own_plane, own_plane, f); };
+  auto set_own = [&](int index, const float2 (&f)[4]) FLCE_INLINE {
+    shared_set(ring_smem, own_at + 2 * index * own_plane, own_plane, f);
+  };
+  constexpr int kA = 0, kDg = 1, kDb1 = GATE ? 2 : 0, kDb2 = 3;
   load_weight<VEC>(p.w2, p.w2_dt, p.w_off, col, D, w2);
   if (POST) load_weight<VEC>(p.w1, p.w1_dt, p.w_off, col, D, w1);
   if (GATE && FULL) load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, b1);
@@ -730,16 +774,14 @@ __global__ void __launch_bounds__(kBnMaxThreads)
     dw1[i] = db1[i] = dw2[i] = db2[i] = dg[i] = both(0.f);
   }
   if (FULL) {
-    s_w2 = share_param(ring_smem, 0, r0, threads_per_row, w2);
-    if (POST) s_w1 = share_param(ring_smem, 1, r0, threads_per_row, w1);
-    if (POST && GATE) s_b1 = share_param(ring_smem, 2, r0, threads_per_row, b1);
+    set_param(kW2, w2);
+    if (POST) set_param(kW1, w1);
+    if (POST && GATE) set_param(kB1, b1);
     __syncthreads();
   }
-  const int own_plane = int(blockDim.x);
-  float4* own = reinterpret_cast<float4*>(ring_smem + kParams * 32 * threads_per_row) + threadIdx.x;
-  const OwnParam own_a{own, own_plane}, own_dg{own + 2 * own_plane, own_plane}, own_db1{own + 4 * own_plane, own_plane};
-  if (OWN_B) own_db1.set(db1);
-  if (OWN && gate && !gate_full) own_dg.set(dg);
+  if (OWN_B1) set_own(kDb1, db1);
+  if (OWN_B2) set_own(kDb2, db2);
+  if (OWN && gate && !gate_full) set_own(kDg, dg);
   const float inv_d = 1.f / float(D), inv_d0 = p.layer ? inv_d : 0.f;
   const float live = live_col ? 1.f : 0.f;  // threads past the row: their values stay zero
   // values of a row of the batch in slot `at`, whose first row is `first`
@@ -782,7 +824,7 @@ __global__ void __launch_bounds__(kBnMaxThreads)
   };
   // Sums of the second norm's gradient over the batch's rows: s1 of g (h - mean), s0 of g.
   auto second_norm = [&](uint32_t at, int slot, const Rows& w, float (&s1)[R], float (&s0)[R]) FLCE_INLINE {
-    if (FULL) s_w2.get(w2);
+    if (FULL) param(kW2, w2);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       s1[r] = s0[r] = 0.f;
@@ -821,7 +863,14 @@ __global__ void __launch_bounds__(kBnMaxThreads)
   Rows now{int(r0.worker), 0, 0};
   open(now);
   uint32_t batch = ring.first;
-  int slot = 0, open_chunk = -1;
+  int slot = 0;
+  auto enter = [&](int chunk) FLCE_INLINE {  // a chunk has one gate row
+    if (gate && !gate_full && chunk < p.chunks) {
+      load_gate<TX, TR, VEC>(p, chunk / int(p.chunks_per_group), col, a);
+      if (OWN) set_own(kA, a);
+    }
+  };
+  enter(now.chunk);
   float s1[R], s0[R], t1[R], t0[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) s1[r] = s0[r] = t1[r] = t0[r] = 0.f;
@@ -842,13 +891,8 @@ __global__ void __launch_bounds__(kBnMaxThreads)
       ring.wait(batches - 1);
       __syncwarp();
     }
-    if (gate && !gate_full && now.chunk != open_chunk) {
-      load_gate<TX, TR, VEC>(p, now.chunk / int(p.chunks_per_group), col, a);
-      if (OWN) own_a.set(a);
-    }
-    open_chunk = now.chunk;
     float2 d[R][4];  // the gradient of h, then what the first norm's gradient is taken of
-    if (FULL && POST) s_w1.get(w1);
+    if (FULL && POST) param(kW1, w1);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       t1[r] = t0[r] = 0.f;
@@ -859,11 +903,17 @@ __global__ void __launch_bounds__(kBnMaxThreads)
         float2 n[4], g[4];
         get_h(batch, row, r, st.z, n);
         get_dy(batch, row, r, g);
-        if (FULL) s_w2.get(w2);
+        if (FULL) param(kW2, w2);
+        if (OWN_B2) {
+          own(kDb2, db2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) db2[i] = add2(db2[i], g[i]);
+          set_own(kDb2, db2);
+        }
         const float2 k1 = both(-(s1[r] * st.w * inv_d) * st.w * st.w), k0 = both(-st.w * (s0[r] * inv_d0)), k = both(st.w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (FULL) db2[i] = add2(db2[i], g[i]);
+          if (FULL && !OWN_B2) db2[i] = add2(db2[i], g[i]);
           d[r][i] = fma2(n[i], k1, d[r][i]);
           if (FULL) d[r][i] = add2(d[r][i], k0);
           g[i] = mul2(g[i], k);
@@ -887,11 +937,11 @@ __global__ void __launch_bounds__(kBnMaxThreads)
             load_gate<TX, TR, VEC>(p, row + r, col, a);
           }
         } else if (OWN) {
-          own_a.get(a);
+          own(kA, a);
         }
         // d u, without the scale: u = (x - m) r w1 + b1, or x
         float2 e[4];
-        if (FULL && POST) s_b1.get(b1);
+        if (FULL && POST) param(kB1, b1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           e[i] = x[i];
@@ -913,10 +963,10 @@ __global__ void __launch_bounds__(kBnMaxThreads)
               store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(row + r) * D, col, D, e);
           }
         } else {
-          if (OWN) own_dg.get(dg);
+          if (OWN) own(kDg, dg);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dg[i] = add2(dg[i], e[i]);
-          if (OWN) own_dg.set(dg);
+          if (OWN) set_own(kDg, dg);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[r][i] = mul2(d[r][i], a[i]);
@@ -927,15 +977,15 @@ __global__ void __launch_bounds__(kBnMaxThreads)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           dw1[i] = fma2(mul2(d[r][i], k), x[i], dw1[i]);
-          if (FULL && !OWN_B) db1[i] = add2(db1[i], d[r][i]);
+          if (FULL && !OWN_B1) db1[i] = add2(db1[i], d[r][i]);
           e[i] = d[r][i];
           d[r][i] = mul2(d[r][i], w1[i]);
         }
-        if (OWN_B) {
-          own_db1.get(db1);
+        if (OWN_B1) {
+          own(kDb1, db1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) db1[i] = add2(db1[i], e[i]);
-          own_db1.set(db1);
+          set_own(kDb1, db1);
         }
         t1[r] = dot8(d[r], x);
         if (FULL) t0[r] = sum8(d[r]);
@@ -982,8 +1032,8 @@ __global__ void __launch_bounds__(kBnMaxThreads)
     if (gate && !gate_full && p.dgate != nullptr && next.chunk != now.chunk) {
       float2 da[4];
       if (OWN) {
-        own_a.get(a);
-        own_dg.get(dg);
+        own(kA, a);
+        own(kDg, dg);
       }
       derive8(a, p.act, da);
 #pragma unroll
@@ -996,8 +1046,9 @@ __global__ void __launch_bounds__(kBnMaxThreads)
         store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, col, D, dg);
 #pragma unroll
       for (int i = 0; i < 4; ++i) dg[i] = both(0.f);
-      if (OWN) own_dg.set(dg);
+      if (OWN) set_own(kDg, dg);
     }
+    if (next.chunk != now.chunk) enter(next.chunk);
     batch = batch_next;
     slot = slot_next;
     now = next;
@@ -1026,8 +1077,9 @@ __global__ void __launch_bounds__(kBnMaxThreads)
     for (int i = 0; i < 4; ++i) s[i] = mul2(s[i], both(scale));
     store8<float, VEC>(part + block * D, col, D, s);
   };
-  if (OWN_B) own_db1.get(db1);
-  if (OWN_B) __syncthreads();  // the sums' room is used again
+  if (OWN_B1) own(kDb1, db1);
+  if (OWN_B2) own(kDb2, db2);
+  if (OWN_B1) __syncthreads();  // the sums' room is used again
   if (POST) flush(p.part[0], dw1, p.scale);
   if (POST && FULL) flush(p.part[1], db1, p.scale);
   flush(p.part[2], dw2, 1.f);

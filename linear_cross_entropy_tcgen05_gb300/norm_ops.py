@@ -160,6 +160,15 @@ def _describe(x, residual, weight, bias, post_weight, post_bias, gate, norm, eps
     return d
 
 
+def _describes(d, x, weight, bias, post_weight, post_bias, gate) -> bool:
+    """Whether d still holds for these tensors: the ones of the forward, where they were."""
+    for t, p in ((x, d.x), (weight, d.weight), (bias, d.bias), (post_weight, d.post_weight), (post_bias, d.post_bias),
+                 (gate, d.gate)):
+        if t is not None and t.data_ptr() != p:
+            return False
+    return x.stride(-2) == d.ld_x if x.dim() > 1 and x.shape[-2] > 1 else False
+
+
 def _forward(d, x, h_dtype, want_y: bool, want_stats: bool):
     h = torch.empty(x.shape, dtype=h_dtype, device=x.device)
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_y else None
@@ -181,7 +190,7 @@ class BlockNormFunction(torch.autograd.Function):
         h, y, stats = _forward(d, x, x.dtype if residual is None else residual.dtype, weight is not None, True)
         # the residual's values are not needed again, only its type (h has it)
         ctx.save_for_backward(x, weight, bias, post_weight, post_bias, gate, h, stats)
-        ctx.opts = opts
+        ctx.opts, ctx.desc = opts, d
         ctx.set_materialize_grads(False)
         return h, y
 
@@ -192,7 +201,9 @@ class BlockNormFunction(torch.autograd.Function):
             return (None,) * 12
         x, weight, bias, post_weight, post_bias, gate, h, stats = ctx.saved_tensors
         want, dev, D = ctx.needs_input_grad, x.device, x.shape[-1]
-        d = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
+        d = ctx.desc
+        if not _describes(d, x, weight, bias, post_weight, post_bias, gate):  # a saved-tensor hook gave other tensors
+            d = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
         grads, out = FlceBlockNormGrads(), [None] * 12
         for i, name, t in ((0, "dx", x), (1, "dresidual", h), (2, "dweight", weight), (3, "dbias", bias),
                            (4, "dpost_weight", post_weight), (5, "dpost_bias", post_bias), (6, "dgate", gate)):
