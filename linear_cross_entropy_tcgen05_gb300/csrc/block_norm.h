@@ -41,7 +41,9 @@ struct BlockNormParams {
   void *dx, *dres, *dgate;
   int64_t chunks, chunks_per_group, group_rows;  // chunks never cross a gate group
   int gate_full;                                 // a gate row for each row: dgate is written row by row
-  float* part[4];    // dw1, db1, dw2, db2 partial sums [blocks][D], or null
+  // Partial sums of dw1, db1, dw2, db2 [blocks][D], or null; with gate groups the first two have a
+  // row for each worker.
+  float* part[4];
   float* part_gate;  // [chunks][D], or null (dgate written directly when a group is one chunk)
 };
 
@@ -52,14 +54,14 @@ enum BnFeature : int { BN_POST = 1, BN_GATE = 2, BN_FULL = 4, BN_ALL = 7 };
 __host__ __device__ constexpr int bn_shared_params(int feat, bool backward) {
   if (!(feat & BN_FULL)) return 0;
   if (!backward) return feat & BN_GATE ? 4 : 2;
-  return feat & BN_POST ? (feat & BN_GATE ? 3 : 2) : 1;
+  return feat & BN_POST ? 2 : 1;
 }
-// Values that each thread of a backward kernel keeps there for itself: a gate and the sum of its
-// gradient, and sums of the biases' (with all of them in registers the kernel spills, to local
-// memory for which there is no L1 left: 386 us against 210 at N = 16384, D = 2304).
+// Values that each thread of a backward kernel keeps there for itself: a bias's sum, or both and a
+// gate (with all of them in registers the kernel spills, to local memory for which there is
+// no L1 left: 386 us against 210 at N = 16384, D = 2304).
 __host__ __device__ constexpr int bn_own_params(int feat, bool backward) {
-  if (!backward || !(feat & BN_POST)) return 0;
-  return feat & BN_GATE ? (feat & BN_FULL ? 4 : 2) : (feat & BN_FULL ? 1 : 0);
+  if (!backward || !(feat & BN_POST) || !(feat & BN_FULL)) return 0;
+  return feat & BN_GATE ? 3 : 1;
 }
 
 // Rows that a row group works on together at most: they share the latency of their sums. (Four in

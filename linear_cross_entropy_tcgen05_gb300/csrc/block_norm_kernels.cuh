@@ -682,8 +682,8 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   extern __shared__ __align__(16) char ring_smem[];
   constexpr int kX = 0, kY = sizeof(TX) / 2, kH = 2 * kY, kDh = kH + sizeof(TR) / 2, kG = kDh + sizeof(TR) / 2;  // planes
   constexpr int kParams = bn_shared_params(FEAT, true);
-  // in shared memory: the gate and the sum of its gradient, and the biases' sums
-  constexpr bool OWN = POST && GATE, OWN_B1 = POST && FULL, OWN_B2 = POST && GATE && FULL;
+  // in shared memory: a bias's sum, and with a gate that and both biases' sums
+  constexpr bool OWN_B = POST && FULL, OWN_A = POST && GATE && FULL;
   const RowThread r0 = row_thread(threads_per_row, cluster);
   RowSum rs = row_sum(scratch, r0, threads_per_row, cluster, p.D);
   const int col = r0.col, D = p.D;
@@ -750,38 +750,35 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
   }
   if (cluster > 1) cluster_sync_all();
-  float2 w1[4], w2[4], b1[4], a[4], dw1[4], db1[4], dw2[4], db2[4], dg[4];
+  float2 w1[4], w2[4], a[4], dw1[4], db1[4], dw2[4], db2[4];
   const int t16 = 16 * r0.t, plane = 16 * threads_per_row;  // a parameter's values for this thread
   auto param = [&](int index, float2 (&f)[4]) FLCE_INLINE { shared_get(ring_smem, t16 + 2 * index * plane, plane, f); };
   auto set_param = [&](int index, const float2 (&f)[4]) FLCE_INLINE {
     if (r0.group == 0) shared_set(ring_smem, t16 + 2 * index * plane, plane, f);
   };
-  constexpr int kW2 = 0, kW1 = 1, kB1 = 2;
+  constexpr int kW2 = 0, kW1 = 1;
   // the thread's own values follow the parameters
   const int own_plane = 16 * int(blockDim.x), own_at = 2 * kParams * plane + 16 * int(threadIdx.x);
   auto own = [&](int index, float2 (&f)[4]) FLCE_INLINE { shared_get(ring_smem, own_at + 2 * index * own_plane, own_plane, f); };
   auto set_own = [&](int index, const float2 (&f)[4]) FLCE_INLINE {
     shared_set(ring_smem, own_at + 2 * index * own_plane, own_plane, f);
   };
-  constexpr int kA = 0, kDg = 1, kDb1 = GATE ? 2 : 0, kDb2 = 3;
+  constexpr int kDb1 = 0, kA = 1, kDb2 = 2;
   load_weight<VEC>(p.w2, p.w2_dt, p.w_off, col, D, w2);
   if (POST) load_weight<VEC>(p.w1, p.w1_dt, p.w_off, col, D, w1);
-  if (GATE && FULL) load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, b1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     a[i] = both(1.f);
     if (!post) w1[i] = both(1.f);
-    dw1[i] = db1[i] = dw2[i] = db2[i] = dg[i] = both(0.f);
+    dw1[i] = db1[i] = dw2[i] = db2[i] = both(0.f);
   }
   if (FULL) {
     set_param(kW2, w2);
     if (POST) set_param(kW1, w1);
-    if (POST && GATE) set_param(kB1, b1);
     __syncthreads();
   }
-  if (OWN_B1) set_own(kDb1, db1);
-  if (OWN_B2) set_own(kDb2, db2);
-  if (OWN && gate && !gate_full) set_own(kDg, dg);
+  if (OWN_A) set_own(kDb2, db2);
+  if (OWN_B) set_own(kDb1, db1);
   const float inv_d = 1.f / float(D), inv_d0 = p.layer ? inv_d : 0.f;
   const float live = live_col ? 1.f : 0.f;  // threads past the row: their values stay zero
   // values of a row of the batch in slot `at`, whose first row is `first`
@@ -867,7 +864,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   auto enter = [&](int chunk) FLCE_INLINE {  // a chunk has one gate row
     if (gate && !gate_full && chunk < p.chunks) {
       load_gate<TX, TR, VEC>(p, chunk / int(p.chunks_per_group), col, a);
-      if (OWN) set_own(kA, a);
+      if (OWN_A) set_own(kA, a);
     }
   };
   enter(now.chunk);
@@ -904,16 +901,15 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
         get_h(batch, row, r, st.z, n);
         get_dy(batch, row, r, g);
         if (FULL) param(kW2, w2);
-        if (OWN_B2) {
-          own(kDb2, db2);
+        if (FULL) {
+          if (OWN_A) own(kDb2, db2);
 #pragma unroll
           for (int i = 0; i < 4; ++i) db2[i] = add2(db2[i], g[i]);
-          set_own(kDb2, db2);
+          if (OWN_A) set_own(kDb2, db2);
         }
         const float2 k1 = both(-(s1[r] * st.w * inv_d) * st.w * st.w), k0 = both(-st.w * (s0[r] * inv_d0)), k = both(st.w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (FULL && !OWN_B2) db2[i] = add2(db2[i], g[i]);
           d[r][i] = fma2(n[i], k1, d[r][i]);
           if (FULL) d[r][i] = add2(d[r][i], k0);
           g[i] = mul2(g[i], k);
@@ -925,68 +921,54 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
       if (p.dres != nullptr) store8_at<TR, VEC>(static_cast<TR*>(p.dres) + int64_t(row + r) * D + col, col, D, d[r]);
       float2 x[4];
       if (POST || GATE) get_x(batch, row, r, st.x, x);
-      if (gate) {
-        if (gate_full) {
-          if constexpr (VEC) {
-            if (p.gate_res_type)
-              ring.get<TR>(batch, r, kG, a);
-            else
-              ring.get<TX>(batch, r, kG, a);
-            activate8(a, p.act);
-          } else {
-            load_gate<TX, TR, VEC>(p, row + r, col, a);
-          }
-        } else if (OWN) {
-          own(kA, a);
-        }
-        // d u, without the scale: u = (x - m) r w1 + b1, or x
-        float2 e[4];
-        if (FULL && POST) param(kB1, b1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          e[i] = x[i];
-          if (POST) {
-            e[i] = mul2(mul2(e[i], both(st.y)), w1[i]);
-            if (FULL && post) e[i] = add2(e[i], b1[i]);
-          }
-          e[i] = mul2(e[i], d[r][i]);
-        }
-        if (gate_full) {
-          if (p.dgate != nullptr) {
-            float2 da[4];
-            derive8(a, p.act, da);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = mul2(e[i], mul2(da[i], both(p.scale)));
-            if (p.gate_res_type)
-              store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(row + r) * D, col, D, e);
-            else
-              store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(row + r) * D, col, D, e);
-          }
+      if (gate_full) {
+        if constexpr (VEC) {
+          if (p.gate_res_type)
+            ring.get<TR>(batch, r, kG, a);
+          else
+            ring.get<TX>(batch, r, kG, a);
+          activate8(a, p.act);
         } else {
-          if (OWN) own(kDg, dg);
+          load_gate<TX, TR, VEC>(p, row + r, col, a);
+        }
+        if (p.dgate != nullptr) {  // d u scale act', u = (x - m) r w1 + b1, or x
+          float2 e[4], da[4];
+          derive8(a, p.act, da);
+          if (FULL && post) load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, e);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dg[i] = add2(dg[i], e[i]);
-          if (OWN) set_own(kDg, dg);
+          for (int i = 0; i < 4; ++i) {
+            float2 u = x[i];
+            if (POST) u = mul2(mul2(u, both(st.y)), w1[i]);
+            if (FULL && post) u = add2(u, e[i]);
+            e[i] = mul2(mul2(u, d[r][i]), mul2(da[i], both(p.scale)));
+          }
+          if (p.gate_res_type)
+            store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(row + r) * D, col, D, e);
+          else
+            store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(row + r) * D, col, D, e);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[r][i] = mul2(d[r][i], a[i]);
       }
-      if (post) {
+      if (POST || GATE) {
         const float2 k = both(st.y);
-        float2 e[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dw1[i] = fma2(mul2(d[r][i], k), x[i], dw1[i]);
-          if (FULL && !OWN_B1) db1[i] = add2(db1[i], d[r][i]);
-          e[i] = d[r][i];
-          d[r][i] = mul2(d[r][i], w1[i]);
-        }
-        if (OWN_B1) {
-          own(kDb1, db1);
+        for (int i = 0; i < 4; ++i) dw1[i] = fma2(mul2(d[r][i], k), x[i], dw1[i]);
+        if (OWN_B) own(kDb1, db1);
+        if (FULL) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) db1[i] = add2(db1[i], e[i]);
-          set_own(kDb1, db1);
+          for (int i = 0; i < 4; ++i) db1[i] = add2(db1[i], d[r][i]);
         }
+        if (OWN_B) set_own(kDb1, db1);
+      }
+      if (gate && !gate_full) {
+        if (OWN_A) own(kA, a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[r][i] = mul2(d[r][i], a[i]);
+      }
+      if (post) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[r][i] = mul2(d[r][i], w1[i]);
         t1[r] = dot8(d[r], x);
         if (FULL) t0[r] = sum8(d[r]);
       }
@@ -1029,24 +1011,49 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
       __syncwarp();  // the warp has read the batch's statistics
       fetch(batch);
     }
-    if (gate && !gate_full && p.dgate != nullptr && next.chunk != now.chunk) {
-      float2 da[4];
-      if (OWN) {
-        own(kA, a);
-        own(kDg, dg);
-      }
+    // The end of a gate group's chunk. With P = sum of d n and Q = sum of d over its rows (d before
+    // the gate, n = (x - m) r), the gate's gradient is (w1 P + b1 Q) scale act', and the chunk's
+    // part of w1's and b1's is scale a P and scale a Q.
+    if (gate && !gate_full && next.chunk != now.chunk) {
+      float2 e[4], q[4], da[4];
+      if (OWN_A) own(kA, a);
+      if (OWN_B) own(kDb1, db1);
+      if (FULL && POST) param(kW1, w1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = both(0.f);
+      if (FULL && POST) load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, q);
       derive8(a, p.act, da);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dg[i] = mul2(dg[i], mul2(da[i], both(p.scale)));
-      if (p.part_gate != nullptr)
-        store8<float, VEC>(p.part_gate + int64_t(now.chunk) * D, col, D, dg);
-      else if (p.gate_res_type)
-        store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, col, D, dg);
-      else
-        store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, col, D, dg);
+      for (int i = 0; i < 4; ++i) {
+        e[i] = mul2(dw1[i], w1[i]);
+        if (FULL && POST) e[i] = fma2(db1[i], q[i], e[i]);
+        e[i] = mul2(e[i], mul2(da[i], both(p.scale)));
+      }
+      if (p.dgate == nullptr) {
+      } else if (p.part_gate != nullptr) {
+        store8<float, VEC>(p.part_gate + int64_t(now.chunk) * D, col, D, e);
+      } else if (p.gate_res_type) {
+        store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, col, D, e);
+      } else {
+        store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, col, D, e);
+      }
+      // the worker's sums of w1 and b1 over its chunks are in the workspace
+      auto add_part = [&](float* part, const float2 (&v)[4]) FLCE_INLINE {
+        if (part == nullptr) return;
+        float* at = part + r0.worker * D;
+        float2 sum[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dg[i] = both(0.f);
-      if (OWN) set_own(kDg, dg);
+        for (int i = 0; i < 4; ++i) sum[i] = both(0.f);
+        if (now.chunk != int(r0.worker)) unpack8(load8<float, VEC>(at, col, D), sum);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = fma2(v[i], mul2(a[i], both(p.scale)), sum[i]);
+        store8<float, VEC>(at, col, D, sum);
+      };
+      if (POST) add_part(p.part[0], dw1);
+      if (POST && FULL) add_part(p.part[1], db1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dw1[i] = db1[i] = both(0.f);
+      if (OWN_B) set_own(kDb1, db1);
     }
     if (next.chunk != now.chunk) enter(next.chunk);
     batch = batch_next;
@@ -1077,11 +1084,18 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     for (int i = 0; i < 4; ++i) s[i] = mul2(s[i], both(scale));
     store8<float, VEC>(part + block * D, col, D, s);
   };
-  if (OWN_B1) own(kDb1, db1);
-  if (OWN_B2) own(kDb2, db2);
-  if (OWN_B1) __syncthreads();  // the sums' room is used again
-  if (POST) flush(p.part[0], dw1, p.scale);
-  if (POST && FULL) flush(p.part[1], db1, p.scale);
+  if (OWN_A) own(kDb2, db2);
+  if (OWN_B) {
+    own(kDb1, db1);
+    __syncthreads();  // the sums' room is used again
+  }
+  if (!gate || gate_full) {
+    if (POST) flush(p.part[0], dw1, p.scale);
+    if (POST && FULL) flush(p.part[1], db1, p.scale);
+  } else if (r0.worker >= p.chunks) {  // a worker without a chunk: its sums are zero
+    if (POST && p.part[0] != nullptr) store8<float, VEC>(p.part[0] + r0.worker * D, col, D, dw1);
+    if (POST && FULL && p.part[1] != nullptr) store8<float, VEC>(p.part[1] + r0.worker * D, col, D, dw1);
+  }
   flush(p.part[2], dw2, 1.f);
   if (FULL) flush(p.part[3], db2, 1.f);
   if (cluster > 1) cluster_sync_all();

@@ -45,6 +45,7 @@ int bn_threads(const flce_block_norm_desc* d, bool vec, int feat, bool backward)
 struct BwdPlan {
   BlockNormShape shape;
   int64_t blocks, chunks, chunks_per_group, chunk_rows, group_rows;
+  int64_t first_rows;  // partial sums of the first norm's parameters
   bool gate_parts;
   size_t part[4], part_gate, total;
 };
@@ -79,9 +80,10 @@ BwdPlan bwd_plan(int64_t N, int64_t D, int64_t gate_rows, int max_threads) {
   p.chunks = groups * p.chunks_per_group;
   p.gate_parts = gate_rows > 0 && gate_rows != N && p.chunks_per_group > 1;
   size_t o = 0;
-  for (size_t& at : p.part) {
-    at = o;
-    o += api_align256(size_t(p.blocks) * size_t(D) * sizeof(float));
+  p.first_rows = gate_rows > 0 && gate_rows != N ? workers : p.blocks;
+  for (int i = 0; i < 4; ++i) {
+    p.part[i] = o;
+    o += api_align256(size_t(i < 2 ? p.first_rows : p.blocks) * size_t(D) * sizeof(float));
   }
   p.part_gate = o;
   if (p.gate_parts) o += api_align256(size_t(p.chunks) * size_t(D) * sizeof(float));
@@ -330,7 +332,7 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* 
   for (int i = 0; i < 4; ++i) {
     if (!params[i].out) continue;
     p.part[i] = reinterpret_cast<float*>(ws + plan.part[i]);
-    sums.a[sums.n++] = BnSum{p.part[i], params[i].out, 1, plan.blocks, params[i].dt};
+    sums.a[sums.n++] = BnSum{p.part[i], params[i].out, 1, i < 2 ? plan.first_rows : plan.blocks, params[i].dt};
   }
   if (p.part_gate) sums.a[sums.n++] = BnSum{p.part_gate, g->dgate, d->gate_rows, plan.chunks_per_group, d->gate_dtype};
   const bool f32 = d->residual_dtype == FLCE_DTYPE_F32;
