@@ -47,9 +47,10 @@ struct BlockNormParams {
   float* part_gate;  // [chunks][D], or null (dgate written directly when a group is one chunk)
 };
 
-// What the code of a kernel has: the norm after the block, a gate, and (FULL) the means
+// What the code of a kernel has: the norm after the block, a gate (for groups of rows, or GATE_ROWS:
+// for each row), and (FULL) the means
 // of layer norms and biases. A kernel takes what has less at run time.
-enum BnFeature : int { BN_POST = 1, BN_GATE = 2, BN_FULL = 4, BN_ALL = 7 };
+enum BnFeature : int { BN_POST = 1, BN_GATE = 2, BN_FULL = 4, BN_GATE_ROWS = 8 };
 // Parameters that a kernel keeps in shared memory (the others have room for theirs in registers).
 __host__ __device__ constexpr int bn_shared_params(int feat, bool backward) {
   if (!(feat & BN_FULL)) return 0;

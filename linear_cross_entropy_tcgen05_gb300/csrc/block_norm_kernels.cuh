@@ -446,8 +446,8 @@ __device__ __forceinline__ void row_stats(F&& get, int col, int D, bool layer, f
   for (int r = 0; r < R; ++r) rstd[r] = rsqrtf(rstd[r] * inv_d + eps);
 }
 
-// What a kernel's code has: the norm after the block, a gate, and (FULL) the means of layer norms
-// and biases. A kernel takes what has less at run time.
+// What a kernel's code has: the norm after the block, a gate (for groups of rows or for each), and
+// (FULL) the means of layer norms and biases. A kernel takes what has less at run time.
 template <typename TX, typename TR, bool VEC, int FEAT>
 __global__ void __launch_bounds__(kBnMaxThreads, 1)
     flce_block_norm_forward_kernel(const __grid_constant__ BlockNormParams p, int threads_per_row, int cluster, int batches, int per) {
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   const int col = r0.col, D = p.D;
   const bool live = col < D;  // VEC: else a thread past the row, whose values are zero
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
-  const bool gate_full = gate && p.gate_full;
+  constexpr bool gate_full = GATE && (FEAT & BN_GATE_ROWS) != 0;  // a gate for each row, else for groups of rows
   const int lo = int(r0.worker * p.chunk_rows < p.N ? r0.worker * p.chunk_rows : p.N);
   const int hi = int(lo + p.chunk_rows < p.N ? lo + p.chunk_rows : p.N);
   RowRing ring{};
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   RowSum rs = row_sum(scratch, r0, threads_per_row, cluster, p.D);
   const int col = r0.col, D = p.D;
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
-  const bool gate_full = gate && p.gate_full;
+  constexpr bool gate_full = GATE && (FEAT & BN_GATE_ROWS) != 0;  // a gate for each row, else for groups of rows
   const int workers = int(gridDim.x) / cluster * (int(blockDim.x) / threads_per_row);
   const bool live_col = col < D;
   // the worker's rows: chunk after chunk, once for the copies and once, behind them, for the work
@@ -1126,18 +1126,23 @@ cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& 
   return e;
 }
 
-// Unaligned rows take the kernel that has everything.
-#define FLCE_BN_DISPATCH(KERNEL, BWD)                                                              \
-  if (!vec) return bn_launch(KERNEL<TX, TR, false, BN_ALL>, p, s, blocks, 0, BN_ALL, BWD, stream); \
-  switch (feat) {                                                                                  \
-    case 0: return bn_launch(KERNEL<TX, TR, true, 0>, p, s, blocks, planes, 0, BWD, stream);       \
-    case 1: return bn_launch(KERNEL<TX, TR, true, 1>, p, s, blocks, planes, 1, BWD, stream);       \
-    case 2: return bn_launch(KERNEL<TX, TR, true, 2>, p, s, blocks, planes, 2, BWD, stream);       \
-    case 3: return bn_launch(KERNEL<TX, TR, true, 3>, p, s, blocks, planes, 3, BWD, stream);       \
-    case 4: return bn_launch(KERNEL<TX, TR, true, 4>, p, s, blocks, planes, 4, BWD, stream);       \
-    case 5: return bn_launch(KERNEL<TX, TR, true, 5>, p, s, blocks, planes, 5, BWD, stream);       \
-    case 6: return bn_launch(KERNEL<TX, TR, true, 6>, p, s, blocks, planes, 6, BWD, stream);       \
-    default: return bn_launch(KERNEL<TX, TR, true, 7>, p, s, blocks, planes, 7, BWD, stream);      \
+// Unaligned rows take the kernels that have everything.
+#define FLCE_BN_DISPATCH(KERNEL, BWD)                                                                     \
+  if (!vec && p.gate_full) return bn_launch(KERNEL<TX, TR, false, 15>, p, s, blocks, 0, 15, BWD, stream); \
+  if (!vec) return bn_launch(KERNEL<TX, TR, false, 7>, p, s, blocks, 0, 7, BWD, stream);                  \
+  switch (feat) {                                                                                         \
+    case 0: return bn_launch(KERNEL<TX, TR, true, 0>, p, s, blocks, planes, 0, BWD, stream);              \
+    case 1: return bn_launch(KERNEL<TX, TR, true, 1>, p, s, blocks, planes, 1, BWD, stream);              \
+    case 2: return bn_launch(KERNEL<TX, TR, true, 2>, p, s, blocks, planes, 2, BWD, stream);              \
+    case 3: return bn_launch(KERNEL<TX, TR, true, 3>, p, s, blocks, planes, 3, BWD, stream);              \
+    case 4: return bn_launch(KERNEL<TX, TR, true, 4>, p, s, blocks, planes, 4, BWD, stream);              \
+    case 5: return bn_launch(KERNEL<TX, TR, true, 5>, p, s, blocks, planes, 5, BWD, stream);              \
+    case 6: return bn_launch(KERNEL<TX, TR, true, 6>, p, s, blocks, planes, 6, BWD, stream);              \
+    case 7: return bn_launch(KERNEL<TX, TR, true, 7>, p, s, blocks, planes, 7, BWD, stream);              \
+    case 10: return bn_launch(KERNEL<TX, TR, true, 10>, p, s, blocks, planes, 10, BWD, stream);           \
+    case 11: return bn_launch(KERNEL<TX, TR, true, 11>, p, s, blocks, planes, 11, BWD, stream);           \
+    case 14: return bn_launch(KERNEL<TX, TR, true, 14>, p, s, blocks, planes, 14, BWD, stream);           \
+    default: return bn_launch(KERNEL<TX, TR, true, 15>, p, s, blocks, planes, 15, BWD, stream);           \
   }
 
 template <typename TX, typename TR>

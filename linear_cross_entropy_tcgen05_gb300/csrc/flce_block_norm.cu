@@ -177,7 +177,7 @@ BlockNormParams bn_params(const flce_block_norm_desc* d) {
 }
 
 int bn_features(const flce_block_norm_desc* d) {
-  return (d->post_weight ? BN_POST : 0) | (d->gate ? BN_GATE : 0) |
+  return (d->post_weight ? BN_POST : 0) | (d->gate ? BN_GATE : 0) | (d->gate && d->gate_rows == d->N ? BN_GATE_ROWS : 0) |
          (d->norm == FLCE_NORM_LAYER || d->post_bias || d->bias ? BN_FULL : 0);
 }
 
