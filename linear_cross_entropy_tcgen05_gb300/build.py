@@ -19,8 +19,11 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libflce.so")
 
-SOURCES = ["flce_gemm.cu", "flce_small.cu", "flce_api.cu", "flce_noalloc.cu", "flce_block_norm.cu", "block_norm_bf16.cu",
-           "block_norm_f16.cu", "block_norm_f32.cu", "flce_grad_clip.cu", "flce_beam.cu"]
+SOURCES = ["flce_gemm.cu", "flce_small.cu", "flce_api.cu", "flce_noalloc.cu", "flce_block_norm.cu", "flce_grad_clip.cu",
+           "flce_beam.cu"]
+# the block norm's kernels, one file for each pair of activation and residual types and direction
+SOURCES += [f"block_norm_{d}_{t}.cu" for d in ("backward", "forward")
+            for t in ("bf16_bf16", "bf16_f32", "f16_f16", "f16_f32", "f32_f32")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]
@@ -50,7 +53,7 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     if verbose:
         extra += ["-Xptxas", "-v"]
     os.makedirs(OUT_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]

@@ -54,7 +54,7 @@ enum BnFeature : int { BN_POST = 1, BN_GATE = 2, BN_FULL = 4, BN_GATE_ROWS = 8 }
 // Parameters that a kernel keeps in shared memory (the others have room for theirs in registers).
 __host__ __device__ constexpr int bn_shared_params(int feat, bool backward) {
   if (!(feat & BN_FULL)) return 0;
-  if (!backward) return feat & BN_GATE ? 4 : 2;
+  if (!backward) return 4;
   return feat & BN_POST ? 2 : 1;
 }
 // Values that each thread of a backward kernel keeps there for itself: a bias's sum, or both and a
@@ -93,12 +93,27 @@ constexpr BnRing bn_ring(const BlockNormShape& s, int planes, int feat, bool bac
   return r;
 }
 
-cudaError_t bn_forward_bf16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
-cudaError_t bn_forward_f16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
-cudaError_t bn_forward_f32(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
-cudaError_t bn_backward_bf16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
-cudaError_t bn_backward_f16(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
-cudaError_t bn_backward_f32(const BlockNormParams&, const BlockNormShape&, bool res_f32, bool vec, int feat, unsigned blocks, cudaStream_t);
+// The features of the kernel that a call with these takes: unaligned rows, and rows shared by
+// clusters unless they have RMS norms alone, take the kernel that has everything.
+constexpr int bn_kernel_features(int feat, bool vec, int cluster) {
+  const int all = feat & BN_GATE_ROWS ? BN_POST | BN_GATE | BN_FULL | BN_GATE_ROWS : BN_POST | BN_GATE | BN_FULL;
+  return !vec || (cluster > 1 && (feat & (BN_GATE | BN_FULL))) ? all : feat;
+}
+
+// One for each pair of types (x's, then the residual's) and direction, each in a file of its own.
+#define FLCE_BN_ENTRY(NAME) \
+  cudaError_t NAME(const BlockNormParams& p, const BlockNormShape& s, bool vec, int feat, unsigned blocks, cudaStream_t stream)
+FLCE_BN_ENTRY(bn_forward_bf16_bf16);
+FLCE_BN_ENTRY(bn_backward_bf16_bf16);
+FLCE_BN_ENTRY(bn_forward_bf16_f32);
+FLCE_BN_ENTRY(bn_backward_bf16_f32);
+FLCE_BN_ENTRY(bn_forward_f16_f16);
+FLCE_BN_ENTRY(bn_backward_f16_f16);
+FLCE_BN_ENTRY(bn_forward_f16_f32);
+FLCE_BN_ENTRY(bn_backward_f16_f32);
+FLCE_BN_ENTRY(bn_forward_f32_f32);
+FLCE_BN_ENTRY(bn_backward_f32_f32);
+#undef FLCE_BN_ENTRY
 
 // out[s][j] = sum over rows of segment s of part[s * rows + r][j], for up to five arrays.
 struct BnSum {

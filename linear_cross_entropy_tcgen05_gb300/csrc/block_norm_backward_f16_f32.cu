@@ -1,0 +1,15 @@
+// block_norm_backward_f16_f32.cu -- the block norm's backward kernels for f16 activations and an f32 residual stream.
+#include "block_norm_kernels.cuh"
+
+namespace flce {
+
+cudaError_t bn_backward_f16_f32(const BlockNormParams& p, const BlockNormShape& s, bool vec, int feat, unsigned blocks,
+                                cudaStream_t stream) {
+  using TX = __half;
+  using TR = float;
+  constexpr bool BACKWARD = true;
+#define KERNEL flce_block_norm_backward_kernel
+  FLCE_BN_DISPATCH;
+}
+
+}  // namespace flce

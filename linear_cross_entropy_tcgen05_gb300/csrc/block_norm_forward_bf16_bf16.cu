@@ -1,0 +1,15 @@
+// block_norm_forward_bf16_bf16.cu -- the block norm's forward kernels for bf16 activations and a bf16 residual stream.
+#include "block_norm_kernels.cuh"
+
+namespace flce {
+
+cudaError_t bn_forward_bf16_bf16(const BlockNormParams& p, const BlockNormShape& s, bool vec, int feat, unsigned blocks,
+                                 cudaStream_t stream) {
+  using TX = __nv_bfloat16;
+  using TR = __nv_bfloat16;
+  constexpr bool BACKWARD = false;
+#define KERNEL flce_block_norm_forward_kernel
+  FLCE_BN_DISPATCH;
+}
+
+}  // namespace flce

@@ -1,0 +1,15 @@
+// block_norm_forward_f32_f32.cu -- the block norm's forward kernels for f32 activations and an f32 residual stream.
+#include "block_norm_kernels.cuh"
+
+namespace flce {
+
+cudaError_t bn_forward_f32_f32(const BlockNormParams& p, const BlockNormShape& s, bool vec, int feat, unsigned blocks,
+                               cudaStream_t stream) {
+  using TX = float;
+  using TR = float;
+  constexpr bool BACKWARD = false;
+#define KERNEL flce_block_norm_forward_kernel
+  FLCE_BN_DISPATCH;
+}
+
+}  // namespace flce

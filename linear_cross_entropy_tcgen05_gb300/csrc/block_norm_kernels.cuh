@@ -12,6 +12,8 @@
 // timing. Statistics and sums are in 32 bits; h and y are rounded once, y from the 32-bit h.
 #pragma once
 
+#include <math_constants.h>
+
 #include "block_norm.h"
 #include "elem_io.cuh"
 #include "flce_internal.h"
@@ -89,10 +91,12 @@ template <typename T> __device__ __forceinline__ T* row_at(void* base, int64_t r
 // step after that, instead of five a value). Two scratch buffers take turns, so one barrier a
 // sum is enough: a buffer is written again only after the barrier of the sum between. Words
 // of warps that are not there stay zero.
-struct RowSum {
+// CLUSTER: blocks share rows; code apart, for its registers.
+template <bool CLUSTER> struct RowSum {
   float* buf;      // [2][kWords] of this row group
   float* clus;     // [2][kBnMaxCluster][4] of this block
-  int nw, warp, lane, bar, threads, cluster, turn;
+  int nw, warp, lane, bar, threads, turn;
+  int blocks;  // of the cluster
   static constexpr int kMaxValues = 8;
   static constexpr int kWords = kMaxValues * kBnMaxThreads / 32;
 
@@ -120,7 +124,7 @@ struct RowSum {
   template <int NV> __device__ __forceinline__ void sum(float (&v)[NV]) {
     const float mine = scatter_sum(v);
     if (nw > 1) {
-      float* b = buf + turn * kWords;
+      float* b = buf + (CLUSTER ? turn & 1 : turn) * kWords;
       if (lane % (32 / NV) == 0) b[warp * NV + lane / (32 / NV)] = mine;
       named_barrier_sync(uint32_t(bar), uint32_t(threads));
       if constexpr (NV <= 4) {
@@ -161,8 +165,8 @@ struct RowSum {
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * (32 / NV));
     }
-    if (cluster > 1) exchange(v);
-    turn ^= 1;
+    if constexpr (CLUSTER) exchange(v);
+    turn = CLUSTER ? turn + 1 : turn ^ 1;
   }
 
   // Of the warps' column sums s and squared distances q from their own means (value i in lanes
@@ -173,7 +177,7 @@ struct RowSum {
   template <int NR> __device__ __forceinline__ void merge(float s, float q, float inv_d, float (&mean)[NR], float (&dist)[NR]) {
     static_assert(2 * NR <= kMaxValues, "values of a sum");
     if (nw > 1) {
-      float* b = buf + turn * kWords;
+      float* b = buf + (CLUSTER ? turn & 1 : turn) * kWords;
       if (lane % (32 / NR) == 0) {
         const int i = lane / (32 / NR);
         float* at = b + warp * 2 * NR + (i / 2) * 4 + i % 2;
@@ -201,7 +205,7 @@ struct RowSum {
 #pragma unroll 3
       for (int w = 0; w < full; ++w) add(w, 256.f, 1.f / 256.f);
       if (part > 0) add(full, float(part), part_inv);
-      const float n = 256.f * float(full) + float(part), inv_n = cluster > 1 ? (n > 0.f ? 1.f / n : 0.f) : inv_d;
+      const float n = 256.f * float(full) + float(part), inv_n = CLUSTER ? (n > 0.f ? 1.f / n : 0.f) : inv_d;
 #pragma unroll
       for (int i = 0; i < NR / 2; ++i) {
         const float2 m = fma2(total[i], both(inv_n), c[i]);  // this block's mean, less c
@@ -219,21 +223,22 @@ struct RowSum {
         dist[i] = __shfl_sync(0xffffffffu, q, i * (32 / NR));
       }
     }
-    if (cluster > 1) {
+    if constexpr (CLUSTER) {
       float v[2 * NR];
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         v[i] = mean[i];
         v[NR + i] = dist[i];
       }
-      const float* c = publish(v);
+      const float* c;
+      const bool ok = publish(v, c);
       float all[NR];
 #pragma unroll
-      for (int i = 0; i < NR; ++i) all[i] = dist[i] = 0.f;
-      for (int r = 0; r < cluster; ++r)
+      for (int i = 0; i < NR; ++i) all[i] = dist[i] = ok ? 0.f : CUDART_NAN_F;
+      for (int r = 0; r < blocks; ++r)
 #pragma unroll
         for (int i = 0; i < NR; ++i) all[i] += c[kMaxValues * r + i];
-      for (int r = 0; r < cluster; ++r) {
+      for (int r = 0; r < blocks; ++r) {
         const float n = block_columns(r), inv_n = n > 0.f ? 1.f / n : 0.f;
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
@@ -247,9 +252,9 @@ struct RowSum {
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       mean[i] *= inv_d;
-      dist[i] = fmaxf(dist[i], 0.f);
+      dist[i] = dist[i] < 0.f ? 0.f : dist[i];  // (a NaN stays)
     }
-    turn ^= 1;
+    turn = CLUSTER ? turn + 1 : turn ^ 1;
   }
   // Columns of the row that block r of the cluster has.
   int D;
@@ -257,24 +262,39 @@ struct RowSum {
     const int most = 8 * threads, left = D - r * most;
     return float(left < 0 ? 0 : left < most ? left : most);
   }
-  // Shows this block's values to the blocks of the cluster, and returns all blocks' values.
-  template <int NV> __device__ __forceinline__ const float* publish(const float (&v)[NV]) {
-    float* c = clus + turn * (kMaxValues * kBnMaxCluster);
-    const int tid = warp * 32 + lane;
-    if (tid < cluster) {
-      const uint32_t at = map_shared_to_rank(smem_addr(c + cluster_ctarank() * kMaxValues), uint32_t(tid));
+  // Shows this block's values to the blocks of the blocks; c: all blocks' values. The values go
+  // as stores that are counted on a barrier of the block that they go to, so nobody waits for
+  // anything else: a cluster barrier would also wait until the row's stores to global memory are
+  // visible (N = 32768, D = 8192 bf16: forward 491 us with it). A block sends the next but one
+  // sum's values only after it has all blocks' of the next, which they send when they have read
+  // these: two buffers and barriers are enough. Returns false after a wait of 2 s (never, unless a
+  // block of the cluster is gone).
+  template <int NV> __device__ __forceinline__ bool publish(const float (&v)[NV], const float*& c) {
+    const int use = turn & 1, tid = warp * 32 + lane;
+    uint64_t* done = reinterpret_cast<uint64_t*>(clus - 4) + use;
+    float* mine = clus + use * (kMaxValues * kBnMaxCluster);
+    if (tid == 0) mbar_arrive_expect_tx(done, uint32_t(blocks * NV * 4));
+    if (tid < blocks) {
+      const uint32_t at = map_shared_to_rank(smem_addr(mine + cluster_ctarank() * kMaxValues), uint32_t(tid));
+      const uint32_t bar_at = map_shared_to_rank(smem_addr(done), uint32_t(tid));
 #pragma unroll
-      for (int i = 0; i < NV; ++i) st_shared_cluster_u32(at + 4 * i, __float_as_uint(v[i]));
+      for (int i = 0; i < NV; i += 2) st_async_v2(at + 4 * i, __float_as_uint(v[i]), __float_as_uint(v[i + 1]), bar_at);
     }
-    cluster_sync_all();
-    return c;
+    c = mine;
+    const uint32_t a = smem_addr(done), parity = uint32_t(turn >> 1) & 1u;
+    if (mbar_try_wait_acq_cluster(a, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait_acq_cluster(a, parity))
+      if (global_timer_ns() - t0 > FLCE_WAIT_LIMIT_NS) return false;
+    return true;
   }
   // Sums over the blocks of the cluster.
   template <int NV> __device__ __forceinline__ void exchange(float (&v)[NV]) {
-    const float* c = publish(v);
+    const float* c;
+    const bool ok = publish(v, c);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = 0.f;
-    for (int r = 0; r < cluster; ++r)
+    for (int i = 0; i < NV; ++i) v[i] = ok ? 0.f : CUDART_NAN_F;
+    for (int r = 0; r < blocks; ++r)
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] += c[kMaxValues * r + i];
   }
@@ -380,25 +400,31 @@ template <bool VEC> __device__ __forceinline__ void cut8(float2 (&v)[4], int col
 }
 
 // at most kBnMaxThreads / 64 row groups use barriers
-constexpr int kRowSumWords = 2 * RowSum::kMaxValues * kBnMaxCluster + kBnMaxThreads / 64 * 2 * RowSum::kWords;
+constexpr int kRowSumWords = 4 + 2 * RowSum<false>::kMaxValues * kBnMaxCluster + kBnMaxThreads / 64 * 2 * RowSum<false>::kWords;
 
-__device__ __forceinline__ RowSum row_sum(float* scratch, const RowThread& r, int threads_per_row, int cluster, int D) {
-  RowSum rs;
+template <bool CLUSTER>
+__device__ __forceinline__ RowSum<CLUSTER> row_sum(float* scratch, const RowThread& r, int threads_per_row, int cluster, int D) {
+  RowSum<CLUSTER> rs;
   rs.D = D;
   const int cols = D - (r.col - 8 * r.t), most = 8 * threads_per_row;  // columns from this block's first on
   rs.full = (cols < 0 ? 0 : cols < most ? cols : most) / 256;
   rs.part = cols < 0 || cols >= most ? 0 : cols % 256;
   rs.part_inv = rs.part > 0 ? 1.f / float(rs.part) : 0.f;
-  rs.clus = scratch;
-  rs.buf = scratch + 2 * RowSum::kMaxValues * kBnMaxCluster + (threads_per_row > 32 ? r.group * 2 * RowSum::kWords : 0);
+  rs.clus = scratch + 4;  // behind the cluster's two barriers
+  rs.buf = scratch + 4 + 2 * RowSum<false>::kMaxValues * kBnMaxCluster + (threads_per_row > 32 ? r.group * 2 * RowSum<false>::kWords : 0);
   for (int i = int(threadIdx.x); i < kRowSumWords; i += int(blockDim.x)) scratch[i] = 0.f;
   __syncthreads();
+  if (CLUSTER && threadIdx.x == 0) {
+    mbar_init(reinterpret_cast<uint64_t*>(scratch), 1);
+    mbar_init(reinterpret_cast<uint64_t*>(scratch) + 1, 1);
+    fence_barrier_init();  // for the other blocks, which the kernel's first cluster barrier waits for
+  }
   rs.nw = threads_per_row / 32;
   rs.warp = r.t / 32;
   rs.lane = r.t % 32;
   rs.bar = 1 + r.group;
   rs.threads = threads_per_row;
-  rs.cluster = cluster;
+  rs.blocks = cluster;
   rs.turn = 0;
   return rs;
 }
@@ -407,8 +433,8 @@ __device__ __forceinline__ RowSum row_sum(float* scratch, const RowThread& r, in
 // rows; get(r, v) gives a row's eight values. A layer norm's warps first take the mean and the
 // squared distances from it over their own columns, so one sum over the row's warps is enough
 // and a large common offset costs no precision.
-template <int R, bool VEC, bool LAYER, typename F>
-__device__ __forceinline__ void row_stats(F&& get, int col, int D, bool layer, float eps, float inv_d, RowSum& rs,
+template <int R, bool VEC, bool LAYER, typename SUM, typename F>
+__device__ __forceinline__ void row_stats(F&& get, int col, int D, bool layer, float eps, float inv_d, SUM& rs,
                                           float (&mean)[R], float (&rstd)[R]) {
   if (LAYER && layer) {
     const float inv_n = rs.warp < rs.full ? 1.f / 256.f : rs.warp == rs.full ? rs.part_inv : 0.f;
@@ -448,17 +474,18 @@ __device__ __forceinline__ void row_stats(F&& get, int col, int D, bool layer, f
 
 // What a kernel's code has: the norm after the block, a gate (for groups of rows or for each), and
 // (FULL) the means of layer norms and biases. A kernel takes what has less at run time.
-template <typename TX, typename TR, bool VEC, int FEAT>
+template <typename TX, typename TR, bool VEC, bool CLUSTER, int FEAT>
 __global__ void __launch_bounds__(kBnMaxThreads, 1)
-    flce_block_norm_forward_kernel(const __grid_constant__ BlockNormParams p, int threads_per_row, int cluster, int batches, int per) {
+    flce_block_norm_forward_kernel(const __grid_constant__ BlockNormParams p, int threads_per_row, int blocks_per_row, int batches, int per) {
   constexpr int R = kBnRows;
+  const int cluster = CLUSTER ? blocks_per_row : 1;
   constexpr bool POST = (FEAT & BN_POST) != 0, GATE = (FEAT & BN_GATE) != 0, FULL = (FEAT & BN_FULL) != 0;
-  __shared__ __align__(16) float scratch[kRowSumWords];
-  extern __shared__ __align__(16) char ring_smem[];
+  __shared__ __align__(128) float scratch[kRowSumWords];
+  extern __shared__ __align__(128) char ring_smem[];  // (aligned to 16 bytes only, each access takes a line more: 12%)
   constexpr int kX = 0, kR = sizeof(TX) / 2, kG = kR + sizeof(TR) / 2;  // planes of x, residual and full gate
   constexpr int kParams = bn_shared_params(FEAT, false);
   const RowThread r0 = row_thread(threads_per_row, cluster);
-  RowSum rs = row_sum(scratch, r0, threads_per_row, cluster, p.D);
+  RowSum<CLUSTER> rs = row_sum<CLUSTER>(scratch, r0, threads_per_row, cluster, p.D);
   const int col = r0.col, D = p.D;
   const bool live = col < D;  // VEC: else a thread past the row, whose values are zero
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
@@ -489,52 +516,38 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     ring.init(ring_smem + (FULL ? kParams * 32 * threads_per_row : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
     for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
   }
-  if (cluster > 1) cluster_sync_all();
-  // c: what a row's value after the first norm is multiplied by, w1 scale act(gate), and c_b what
-  // is added, b1 scale act(gate)
-  float2 w2[4], c[4], c_b[4];
+  if (CLUSTER) cluster_sync_all();
+  // Without FULL, c is what a row's value after the first norm is multiplied by: w1 scale
+  // act(gate). With it w1 scale and b1 scale are in shared memory, and c is act(gate).
+  float2 w1[4], w2[4], c[4];
   const int t16 = 16 * r0.t, plane = 16 * threads_per_row;  // a parameter's values for this thread
   auto param = [&](int index, float2 (&f)[4]) FLCE_INLINE { shared_get(ring_smem, t16 + 2 * index * plane, plane, f); };
   auto set_param = [&](int index, const float2 (&f)[4]) FLCE_INLINE {
     if (r0.group == 0) shared_set(ring_smem, t16 + 2 * index * plane, plane, f);
   };
   constexpr int kW2 = 0, kB2 = 1, kW1 = 2, kB1 = 3;
-  load_weight<VEC>(p.w1, p.w1_dt, p.w_off, col, D, c);
+  load_weight<VEC>(p.w1, p.w1_dt, p.w_off, col, D, w1);
   load_weight<VEC>(p.w2, p.w2_dt, p.w_off, col, D, w2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = post ? mul2(c[i], both(p.scale)) : both(p.scale);
+  for (int i = 0; i < 4; ++i) {
+    w1[i] = post ? mul2(w1[i], both(p.scale)) : both(p.scale);
+    c[i] = FULL ? both(1.f) : w1[i];
+  }
   if (FULL) {
-    load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, c_b);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c_b[i] = mul2(c_b[i], both(p.scale));
-    float2 b2[4];
-    load_weight<VEC>(p.b2, p.b2_dt, 0.f, col, D, b2);
+    float2 b[4];
     set_param(kW2, w2);
-    set_param(kB2, b2);
-    if (GATE) {
-      set_param(kW1, c);
-      set_param(kB1, c_b);
-    }
+    set_param(kW1, w1);
+    load_weight<VEC>(p.b2, p.b2_dt, 0.f, col, D, b);
+    set_param(kB2, b);
+    load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = mul2(b[i], both(p.scale));
+    set_param(kB1, b);
     __syncthreads();
   }
-  float2 w1[4];
-  if (GATE && !FULL) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w1[i] = c[i];
-  }
   auto set_gate = [&](const float2(&a)[4]) FLCE_INLINE {
-    if (FULL) {
-      param(kW1, c);
-      param(kB1, c_b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = mul2(c[i], a[i]);
-        c_b[i] = mul2(c_b[i], a[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = mul2(w1[i], a[i]);
-    }
+    for (int i = 0; i < 4; ++i) c[i] = FULL ? a[i] : mul2(w1[i], a[i]);
   };
   const float inv_d = 1.f / float(D);
   int gate_end = lo;  // first row whose gate is not in c
@@ -552,7 +565,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   for (int r = 0; r < R; ++r) m1[r] = 0.f, r1[r] = 1.f;
   if (lo < hi) {
     if constexpr (VEC) ring.wait(batches - 1);
-    if (post) row_stats<R, VEC, FULL>([&](int r, float2 (&v)[4]) { get_x(batch, lo, r, v); }, col, D, p.layer, p.eps, inv_d, rs, m1, r1);
+    if (post) row_stats<R, VEC, FULL, RowSum<CLUSTER>>([&](int r, float2 (&v)[4]) { get_x(batch, lo, r, v); }, col, D, p.layer, p.eps, inv_d, rs, m1, r1);
   }
   for (int row = lo; row < hi; row += per) {
     const bool second = per > 1 && row + 1 < hi;  // the last batch may have one row
@@ -590,12 +603,18 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
       } else {
         unpack8(p.residual == nullptr ? raw_zero<TR>() : load8<TR, VEC>(static_cast<const TR*>(p.residual) + (row + r) * p.ld_residual, col, D), h[r]);
       }
+      if (FULL) {
+        float2 w[4], b[4];
+        param(kW1, w);
+        param(kB1, b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (FULL) {
-          u[i] = mul2(add2(u[i], both(-m1[r])), both(r1[r]));
-          h[r][i] = add2(h[r][i], fma2(u[i], c[i], c_b[i]));
-        } else {
+        for (int i = 0; i < 4; ++i) {
+          u[i] = fma2(mul2(add2(u[i], both(-m1[r])), both(r1[r])), w[i], b[i]);
+          h[r][i] = GATE ? fma2(u[i], c[i], h[r][i]) : add2(u[i], h[r][i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           if (POST) u[i] = mul2(u[i], both(r1[r]));
           h[r][i] = fma2(u[i], c[i], h[r][i]);
         }
@@ -617,7 +636,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     const int after = row + per;
     if (post && pre) {
       float mean[2 * R], rstd[2 * R];
-      row_stats<2 * R, VEC, FULL>(
+      row_stats<2 * R, VEC, FULL, RowSum<CLUSTER>>(
           [&](int r, float2 (&v)[4]) {
             if (r < R)
               get_h(r, v);
@@ -633,9 +652,9 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
         k1[r] = rstd[R + r];
       }
     } else if (pre) {
-      row_stats<R, VEC, FULL>(get_h, col, D, p.layer, p.eps, inv_d, rs, m2, r2);
+      row_stats<R, VEC, FULL, RowSum<CLUSTER>>(get_h, col, D, p.layer, p.eps, inv_d, rs, m2, r2);
     } else if (post) {
-      row_stats<R, VEC, FULL>([&](int r, float2 (&v)[4]) { get_x(batch, after, r, v); }, col, D, p.layer, p.eps, inv_d, rs, n1, k1);
+      row_stats<R, VEC, FULL, RowSum<CLUSTER>>([&](int r, float2 (&v)[4]) { get_x(batch, after, r, v); }, col, D, p.layer, p.eps, inv_d, rs, n1, k1);
     }
     if (pre) {
       float2 b2[4];
@@ -667,25 +686,26 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
       r1[r] = k1[r];
     }
   }
-  if (cluster > 1) cluster_sync_all();  // no block leaves while another may still write to it
+  if (CLUSTER) cluster_sync_all();  // no block leaves while another may still write to it
 }
 
 // With n = (v - m) r and g = upstream * w, a norm's gradient is r (g - mean(g) - n mean(g n)) =
 // r g - r mean(g) - (v - m) r^3 mean(g (v - m)): it is computed in the last form, from the row's
 // own values, so a norm costs two sums in which no normalised row is formed.
-template <typename TX, typename TR, bool VEC, int FEAT>
+template <typename TX, typename TR, bool VEC, bool CLUSTER, int FEAT>
 __global__ void __launch_bounds__(kBnMaxThreads, 1)
-    flce_block_norm_backward_kernel(const __grid_constant__ BlockNormParams p, int threads_per_row, int cluster, int batches, int per) {
+    flce_block_norm_backward_kernel(const __grid_constant__ BlockNormParams p, int threads_per_row, int blocks_per_row, int batches, int per) {
   constexpr int R = kBnRows;
+  const int cluster = CLUSTER ? blocks_per_row : 1;
   constexpr bool POST = (FEAT & BN_POST) != 0, GATE = (FEAT & BN_GATE) != 0, FULL = (FEAT & BN_FULL) != 0;
-  __shared__ __align__(16) float scratch[kRowSumWords];
-  extern __shared__ __align__(16) char ring_smem[];
+  __shared__ __align__(128) float scratch[kRowSumWords];
+  extern __shared__ __align__(128) char ring_smem[];  // (aligned to 16 bytes only, each access takes a line more: 12%)
   constexpr int kX = 0, kY = sizeof(TX) / 2, kH = 2 * kY, kDh = kH + sizeof(TR) / 2, kG = kDh + sizeof(TR) / 2;  // planes
   constexpr int kParams = bn_shared_params(FEAT, true);
   // in shared memory: a bias's sum, and with a gate that and both biases' sums
   constexpr bool OWN_B = POST && FULL, OWN_A = POST && GATE && FULL;
   const RowThread r0 = row_thread(threads_per_row, cluster);
-  RowSum rs = row_sum(scratch, r0, threads_per_row, cluster, p.D);
+  RowSum<CLUSTER> rs = row_sum<CLUSTER>(scratch, r0, threads_per_row, cluster, p.D);
   const int col = r0.col, D = p.D;
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
   constexpr bool gate_full = GATE && (FEAT & BN_GATE_ROWS) != 0;  // a gate for each row, else for groups of rows
@@ -749,7 +769,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     ring.init(ring_smem + kParams * 32 * threads_per_row + bn_own_params(FEAT, true) * 32 * int(blockDim.x), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
     for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
   }
-  if (cluster > 1) cluster_sync_all();
+  if (CLUSTER) cluster_sync_all();
   float2 w1[4], w2[4], a[4], dw1[4], db1[4], dw2[4], db2[4];
   const int t16 = 16 * r0.t, plane = 16 * threads_per_row;  // a parameter's values for this thread
   auto param = [&](int index, float2 (&f)[4]) FLCE_INLINE { shared_get(ring_smem, t16 + 2 * index * plane, plane, f); };
@@ -1098,7 +1118,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   }
   flush(p.part[2], dw2, 1.f);
   if (FULL) flush(p.part[3], db2, 1.f);
-  if (cluster > 1) cluster_sync_all();
+  if (CLUSTER) cluster_sync_all();
 }
 
 template <typename K>
@@ -1126,38 +1146,39 @@ cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& 
   return e;
 }
 
-// Unaligned rows take the kernels that have everything.
-#define FLCE_BN_DISPATCH(KERNEL, BWD)                                                                     \
-  if (!vec && p.gate_full) return bn_launch(KERNEL<TX, TR, false, 15>, p, s, blocks, 0, 15, BWD, stream); \
-  if (!vec) return bn_launch(KERNEL<TX, TR, false, 7>, p, s, blocks, 0, 7, BWD, stream);                  \
-  switch (feat) {                                                                                         \
-    case 0: return bn_launch(KERNEL<TX, TR, true, 0>, p, s, blocks, planes, 0, BWD, stream);              \
-    case 1: return bn_launch(KERNEL<TX, TR, true, 1>, p, s, blocks, planes, 1, BWD, stream);              \
-    case 2: return bn_launch(KERNEL<TX, TR, true, 2>, p, s, blocks, planes, 2, BWD, stream);              \
-    case 3: return bn_launch(KERNEL<TX, TR, true, 3>, p, s, blocks, planes, 3, BWD, stream);              \
-    case 4: return bn_launch(KERNEL<TX, TR, true, 4>, p, s, blocks, planes, 4, BWD, stream);              \
-    case 5: return bn_launch(KERNEL<TX, TR, true, 5>, p, s, blocks, planes, 5, BWD, stream);              \
-    case 6: return bn_launch(KERNEL<TX, TR, true, 6>, p, s, blocks, planes, 6, BWD, stream);              \
-    case 7: return bn_launch(KERNEL<TX, TR, true, 7>, p, s, blocks, planes, 7, BWD, stream);              \
-    case 10: return bn_launch(KERNEL<TX, TR, true, 10>, p, s, blocks, planes, 10, BWD, stream);           \
-    case 11: return bn_launch(KERNEL<TX, TR, true, 11>, p, s, blocks, planes, 11, BWD, stream);           \
-    case 14: return bn_launch(KERNEL<TX, TR, true, 14>, p, s, blocks, planes, 14, BWD, stream);           \
-    default: return bn_launch(KERNEL<TX, TR, true, 15>, p, s, blocks, planes, 15, BWD, stream);           \
-  }
-
-template <typename TX, typename TR>
-cudaError_t bn_forward_typed(const BlockNormParams& p, const BlockNormShape& s, bool vec, int feat, unsigned blocks,
-                             cudaStream_t stream) {
-  const int planes = bn_planes(int(sizeof(TX)), int(sizeof(TR)), p.gate_full, false);
-  FLCE_BN_DISPATCH(flce_block_norm_forward_kernel, false)
-}
-
-template <typename TX, typename TR>
-cudaError_t bn_backward_typed(const BlockNormParams& p, const BlockNormShape& s, bool vec, int feat, unsigned blocks,
-                              cudaStream_t stream) {
-  const int planes = bn_planes(int(sizeof(TX)), int(sizeof(TR)), p.gate_full, true);
-  FLCE_BN_DISPATCH(flce_block_norm_backward_kernel, true)
-}
+// The kernel of a feature set (as bn_kernel_features gives it).
+#define FLCE_BN_CASE(VEC, CLUSTER, FEAT) \
+  case FEAT: return bn_launch(KERNEL<TX, TR, VEC, CLUSTER, FEAT>, p, s, blocks, planes, FEAT, BACKWARD, stream)
+#define FLCE_BN_DISPATCH                                                                    \
+  const int planes = vec ? bn_planes(int(sizeof(TX)), int(sizeof(TR)), p.gate_full, BACKWARD) : 0; \
+  if (!vec && s.cluster > 1) {                                                              \
+    switch (feat) { FLCE_BN_CASE(false, true, 7); FLCE_BN_CASE(false, true, 15); }          \
+  } else if (!vec) {                                                                        \
+    switch (feat) { FLCE_BN_CASE(false, false, 7); FLCE_BN_CASE(false, false, 15); }        \
+  } else if (s.cluster > 1) {                                                               \
+    switch (feat) {                                                                         \
+      FLCE_BN_CASE(true, true, 0);                                                          \
+      FLCE_BN_CASE(true, true, 1);                                                          \
+      FLCE_BN_CASE(true, true, 7);                                                          \
+      FLCE_BN_CASE(true, true, 15);                                                         \
+    }                                                                                       \
+  } else {                                                                                  \
+    switch (feat) {                                                                         \
+      FLCE_BN_CASE(true, false, 0);                                                         \
+      FLCE_BN_CASE(true, false, 1);                                                         \
+      FLCE_BN_CASE(true, false, 2);                                                         \
+      FLCE_BN_CASE(true, false, 3);                                                         \
+      FLCE_BN_CASE(true, false, 4);                                                         \
+      FLCE_BN_CASE(true, false, 5);                                                         \
+      FLCE_BN_CASE(true, false, 6);                                                         \
+      FLCE_BN_CASE(true, false, 7);                                                         \
+      FLCE_BN_CASE(true, false, 10);                                                        \
+      FLCE_BN_CASE(true, false, 11);                                                        \
+      FLCE_BN_CASE(true, false, 14);                                                        \
+      FLCE_BN_CASE(true, false, 15);                                                        \
+    }                                                                                       \
+  }                                                                                         \
+  return cudaErrorInvalidValue
 
 }  // namespace
 }  // namespace flce

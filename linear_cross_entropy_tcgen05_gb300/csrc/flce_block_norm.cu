@@ -28,9 +28,11 @@ BlockNormShape bn_shape(int64_t D, int max_threads) {
   return s;
 }
 
-// Blocks (or clusters) that stay on the device together.
+// Blocks (or clusters) that stay on the device together, one block an SM: the rows on their way
+// in fill its shared memory. Clusters lie within a group of SMs, so not every SM is in one
+// (cudaOccupancyMaxActiveClusters gives 76, 36 and 15 on GB300).
 int64_t bn_resident(const BlockNormShape& s) {
-  return kSms / s.cluster;  // one an SM: the rows on their way in fill its shared memory
+  return s.cluster == 1 ? kSms : s.cluster == 2 ? kSms / 2 : s.cluster == 4 ? 36 : 15;
 }
 
 // Threads of a block for these tensors: half as many where the rows of the widest would leave no
@@ -39,7 +41,8 @@ int64_t bn_resident(const BlockNormShape& s) {
 int bn_threads(const flce_block_norm_desc* d, bool vec, int feat, bool backward) {
   if (!vec) return kBnMaxThreads;
   const int planes = bn_planes(elem_bytes(d->x_dtype), elem_bytes(d->residual_dtype), d->gate && d->gate_rows == d->N, backward);
-  return bn_ring(bn_shape(d->D, kBnMaxThreads), planes, feat, backward).batches >= 2 ? kBnMaxThreads : kBnMaxThreads / 2;
+  const BlockNormShape s = bn_shape(d->D, kBnMaxThreads);
+  return bn_ring(s, planes, bn_kernel_features(feat, vec, s.cluster), backward).batches >= 2 ? kBnMaxThreads : kBnMaxThreads / 2;
 }
 
 struct BwdPlan {
@@ -268,8 +271,10 @@ flce_status flce_block_norm_forward(const flce_block_norm_desc* d, void* h, void
   p.chunk_rows = cdiv(d->N, blocks * s.rows_per_block);
   blocks = cdiv(cdiv(d->N, p.chunk_rows), s.rows_per_block);
   const bool f32 = d->residual_dtype == FLCE_DTYPE_F32;
-  const auto fn = d->x_dtype == FLCE_DTYPE_BF16 ? bn_forward_bf16 : d->x_dtype == FLCE_DTYPE_F16 ? bn_forward_f16 : bn_forward_f32;
-  return api_cuda("block norm forward", fn(p, s, f32, vec, feat, unsigned(blocks), reinterpret_cast<cudaStream_t>(stream)));
+  const auto fn = d->x_dtype == FLCE_DTYPE_BF16  ? (f32 ? bn_forward_bf16_f32 : bn_forward_bf16_bf16)
+                  : d->x_dtype == FLCE_DTYPE_F16 ? (f32 ? bn_forward_f16_f32 : bn_forward_f16_f16)
+                                                 : bn_forward_f32_f32;
+  return api_cuda("block norm forward", fn(p, s, vec, bn_kernel_features(feat, vec, s.cluster), unsigned(blocks), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* h, const float* stats, const void* dh,
@@ -336,8 +341,11 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* 
   }
   if (p.part_gate) sums.a[sums.n++] = BnSum{p.part_gate, g->dgate, d->gate_rows, plan.chunks_per_group, d->gate_dtype};
   const bool f32 = d->residual_dtype == FLCE_DTYPE_F32;
-  const auto fn = d->x_dtype == FLCE_DTYPE_BF16 ? bn_backward_bf16 : d->x_dtype == FLCE_DTYPE_F16 ? bn_backward_f16 : bn_backward_f32;
-  if ((st = api_cuda("block norm backward", fn(p, plan.shape, f32, vec, feat, unsigned(plan.blocks), stream))) != FLCE_OK) return st;
+  const auto fn = d->x_dtype == FLCE_DTYPE_BF16  ? (f32 ? bn_backward_bf16_f32 : bn_backward_bf16_bf16)
+                  : d->x_dtype == FLCE_DTYPE_F16 ? (f32 ? bn_backward_f16_f32 : bn_backward_f16_f16)
+                                                 : bn_backward_f32_f32;
+  if ((st = api_cuda("block norm backward", fn(p, plan.shape, vec, bn_kernel_features(feat, vec, plan.shape.cluster),
+                                                   unsigned(plan.blocks), stream))) != FLCE_OK) return st;
   return api_cuda("block norm sums", bn_column_sums(sums, stream));
 }
 
