@@ -61,6 +61,30 @@ template <typename T> __device__ __forceinline__ void raw_store(T* p, const Raw8
   }
 }
 
+// The same for what is not read again soon: first to leave L2.
+template <typename T> __device__ __forceinline__ Raw8<T> raw_load_stream(const T* p) {
+  Raw8<T> r;
+  if constexpr (sizeof(T) == 2) {
+    r.v[0] = __ldcs(reinterpret_cast<const uint4*>(p));
+  } else {
+    asm volatile("ld.global.L2::evict_first.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r.v[0].x), "=r"(r.v[0].y), "=r"(r.v[0].z), "=r"(r.v[0].w), "=r"(r.v[1].x), "=r"(r.v[1].y),
+                   "=r"(r.v[1].z), "=r"(r.v[1].w)
+                 : "l"(p));
+  }
+  return r;
+}
+
+template <typename T> __device__ __forceinline__ void raw_store_stream(T* p, const Raw8<T>& r) {
+  if constexpr (sizeof(T) == 2) {
+    __stcs(reinterpret_cast<uint4*>(p), r.v[0]);
+  } else {
+    asm volatile("st.global.L2::evict_first.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r.v[0].x),
+                 "r"(r.v[0].y), "r"(r.v[0].z), "r"(r.v[0].w), "r"(r.v[1].x), "r"(r.v[1].y), "r"(r.v[1].z), "r"(r.v[1].w)
+                 : "memory");
+  }
+}
+
 __device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }

@@ -2,7 +2,8 @@
 //
 //   total = |s| (sum g^2)^(1/2), or |s| max |g|        out = g s min(1, max_norm / (total + eps))
 //
-// Bound by memory: one read for the norm, then a read and a write for the scaling. Two
+// Bound by memory: one read for the norm, then a read and a write for the scaling (measured on
+// 525 M fp32 values: 302 us and 650 us, 6.9 and 6.5 TB/s). Two
 // kernels over the same list of chunks, whatever the number of tensors: their addresses go to
 // the device as kernel parameters (no copy, no table kept between calls). The first writes one
 // partial sum a block; every block of the second adds all partial sums in the same fixed order
@@ -17,8 +18,14 @@ namespace flce {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kClipBlocks = 152 * 8;  // persistent blocks of one launch, at most
+// Persistent blocks of one launch, at most: those that stay on the device together. (Eight an SM
+// do not: the last of them begin when the others end, 525 M fp32 values 1065 us against 945.)
+constexpr int kClipPerSm = 4, kClipBlocks = 152 * kClipPerSm;
 constexpr int kFewTensors = 60, kManyTensors = 900;
+// Gradients that the scaling finds in L2 (129 MB) after the norm's pass: it takes the chunks in
+// the opposite order, and what went before them, like what it writes, leaves L2 first (218 M bf16
+// values into fp32: 290 us with none kept, 280 us with 60 MB, the same with 100).
+constexpr int64_t kClipKeepBytes = int64_t(60) << 20;
 
 struct ClipTensor {
   const void* grad;
@@ -33,6 +40,7 @@ template <int CAP> struct ClipTable {
   ClipTensor t[CAP];
   int count, chunks;
   int chunk_elems;  // a multiple of 8 * kClipThreads
+  int keep;         // last chunks of the norm's pass that stay in L2 for the scaling's
   int inf_norm;
   float max_norm, eps, scale;
   double* part;        // this launch's partial sums
@@ -63,25 +71,46 @@ template <typename T> __device__ __forceinline__ Raw8<T> clip_load(const T* g, i
   return pack8<T>(f);
 }
 
+// A thread's vectors of a chunk, kClipBatch of them in flight at a time. Those of a chunk that
+// lies within its tensor need no checks. STREAM: they leave L2 first.
+constexpr int kClipBatch = 4;
+template <typename T, bool STREAM, typename F>
+__device__ __forceinline__ void each_vector(const T* g, int64_t n, int64_t e0, int elems, F&& f) {
+  const bool inner = e0 >= 0 && e0 + elems <= n && elems % (8 * kClipThreads * kClipBatch) == 0;
+  if (inner) {
+    const T* at = g + e0 + threadIdx.x * 8;
+    for (int v = 0; v < elems; v += 8 * kClipThreads * kClipBatch) {
+      Raw8<T> r[kClipBatch];
+#pragma unroll
+      for (int k = 0; k < kClipBatch; ++k) {
+        const T* p = at + v + k * 8 * kClipThreads;
+        r[k] = STREAM ? raw_load_stream(p) : raw_load(p);
+      }
+#pragma unroll
+      for (int k = 0; k < kClipBatch; ++k) f(r[k], e0 + v + k * 8 * kClipThreads + int(threadIdx.x) * 8);
+    }
+    return;
+  }
+  for (int v = int(threadIdx.x) * 8; v < elems; v += kClipThreads * 8) f(clip_load(g, e0 + v, n), e0 + v);
+}
+
 // Squares of a chunk in 32 bits (at most 64 of a thread), chunks in 64 bits. Where a thread's
 // 32-bit sum may have lost something (overflow, or squares below the normal range) it takes
 // its values once more in 64 bits.
-template <typename T>
+template <typename T, bool STREAM>
 __device__ __forceinline__ double chunk_squares(const T* g, int64_t n, int64_t e0, int elems) {
-  float s[2] = {0.f, 0.f};
+  float2 s[2] = {both(0.f), both(0.f)};
   uint32_t any = 0;
   constexpr uint32_t kMagnitude = sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu;
-#pragma unroll 4
-  for (int v = int(threadIdx.x) * 8; v < elems; v += kClipThreads * 8) {
-    const Raw8<T> r = clip_load(g, e0 + v, n);
-    float f[8];
+  each_vector<T, STREAM>(g, n, e0, elems, [&](const Raw8<T>& r, int64_t) {
+    float2 f[4];
     unpack8(r, f);
 #pragma unroll
     for (const uint4& q : r.v) any |= q.x | q.y | q.z | q.w;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i & 1] = fmaf(f[i], f[i], s[i & 1]);
-  }
-  const float sum = s[0] + s[1];
+    for (int i = 0; i < 4; ++i) s[i & 1] = fma2(f[i], f[i], s[i & 1]);
+  });
+  const float sum = (s[0].x + s[0].y) + (s[1].x + s[1].y);
   if (sum > 1e-20f && sum < 1e30f) return double(sum);
   if ((any & kMagnitude) == 0) return 0.0;
   double d = 0.0;
@@ -94,17 +123,25 @@ __device__ __forceinline__ double chunk_squares(const T* g, int64_t n, int64_t e
 }
 
 // Largest magnitude as the bits of a float: NaN is above infinity, so it stays visible.
-template <typename T>
+template <typename T, bool STREAM>
 __device__ __forceinline__ uint32_t chunk_largest(const T* g, int64_t n, int64_t e0, int elems) {
   uint32_t m = 0;
-#pragma unroll 4
-  for (int v = int(threadIdx.x) * 8; v < elems; v += kClipThreads * 8) {
+  each_vector<T, STREAM>(g, n, e0, elems, [&](const Raw8<T>& r, int64_t) {
     float f[8];
-    unpack8(clip_load(g, e0 + v, n), f);
+    unpack8(r, f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-  }
+  });
   return m;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_norm(const T* g, int64_t n, int64_t e0, int elems, bool inf_norm, bool stream,
+                                           double& sum, uint32_t& largest) {
+  if (inf_norm)
+    largest = max(largest, stream ? chunk_largest<T, true>(g, n, e0, elems) : chunk_largest<T, false>(g, n, e0, elems));
+  else
+    sum += stream ? chunk_squares<T, true>(g, n, e0, elems) : chunk_squares<T, false>(g, n, e0, elems);
 }
 
 // Fixed-order sum (or largest, NaN above all) over the block; every thread gets it.
@@ -124,7 +161,7 @@ __device__ __forceinline__ double block_combine(double v, bool largest) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kClipThreads) flce_grad_norm_kernel(const __grid_constant__ ClipTable<CAP> tb) {
+__global__ void __launch_bounds__(kClipThreads, kClipPerSm) flce_grad_norm_kernel(const __grid_constant__ ClipTable<CAP> tb) {
   double sum = 0.0;
   uint32_t largest = 0;
   for (int c = int(blockIdx.x); c < tb.chunks; c += int(gridDim.x)) {
@@ -132,16 +169,13 @@ __global__ void __launch_bounds__(kClipThreads) flce_grad_norm_kernel(const __gr
     const int64_t e0 = int64_t(c - t.first) * tb.chunk_elems - misalign(t.grad, elem_bytes(t.dt));
     const int64_t left = t.n - e0;
     const int elems = int(left < tb.chunk_elems ? left : tb.chunk_elems);
-    if (tb.inf_norm) {
-      const uint32_t m = t.dt == ELEM_F32    ? chunk_largest(static_cast<const float*>(t.grad), t.n, e0, elems)
-                         : t.dt == ELEM_BF16 ? chunk_largest(static_cast<const __nv_bfloat16*>(t.grad), t.n, e0, elems)
-                                             : chunk_largest(static_cast<const __half*>(t.grad), t.n, e0, elems);
-      largest = max(largest, m);
-    } else {
-      sum += t.dt == ELEM_F32    ? chunk_squares(static_cast<const float*>(t.grad), t.n, e0, elems)
-             : t.dt == ELEM_BF16 ? chunk_squares(static_cast<const __nv_bfloat16*>(t.grad), t.n, e0, elems)
-                                 : chunk_squares(static_cast<const __half*>(t.grad), t.n, e0, elems);
-    }
+    const bool stream = c < tb.chunks - tb.keep;
+    if (t.dt == ELEM_F32)
+      chunk_norm(static_cast<const float*>(t.grad), t.n, e0, elems, tb.inf_norm, stream, sum, largest);
+    else if (t.dt == ELEM_BF16)
+      chunk_norm(static_cast<const __nv_bfloat16*>(t.grad), t.n, e0, elems, tb.inf_norm, stream, sum, largest);
+    else
+      chunk_norm(static_cast<const __half*>(t.grad), t.n, e0, elems, tb.inf_norm, stream, sum, largest);
   }
   const double v = block_combine(tb.inf_norm ? double(__uint_as_float(largest)) : sum, tb.inf_norm);
   if (threadIdx.x == 0) tb.part[blockIdx.x] = v;
@@ -165,21 +199,20 @@ template <typename TB> __device__ __forceinline__ float clip_factor(const TB& tb
 template <typename T, typename TO>
 __device__ __forceinline__ void chunk_scale(const T* g, TO* out, int64_t n, int64_t e0, int elems, float f) {
   const bool same = misalign(out, sizeof(TO)) == misalign(g, sizeof(T));
-#pragma unroll 4
-  for (int v = int(threadIdx.x) * 8; v < elems; v += kClipThreads * 8) {
-    const int64_t e = e0 + v;
-    float x[8];
-    unpack8(clip_load(g, e, n), x);
+  each_vector<T, false>(g, n, e0, elems, [&](const Raw8<T>& r, int64_t e) {
+    float2 x[4];
+    unpack8(r, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= f;
+    for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], both(f));
     if (same && e >= 0 && e + 8 <= n) {
-      raw_store(out + e, pack8<TO>(x));
+      raw_store_stream(out + e, pack8<TO>(x));
     } else {
+      const float y[8] = {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (e + i >= 0 && e + i < n) out[e + i] = from_f32<TO>(x[i]);
+        if (e + i >= 0 && e + i < n) out[e + i] = from_f32<TO>(y[i]);
     }
-  }
+  });
 }
 
 template <typename T>
@@ -194,13 +227,14 @@ __device__ __forceinline__ void chunk_scale_to(const ClipTensor& t, int64_t e0, 
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kClipThreads) flce_grad_scale_kernel(const __grid_constant__ ClipTable<CAP> tb) {
+__global__ void __launch_bounds__(kClipThreads, kClipPerSm) flce_grad_scale_kernel(const __grid_constant__ ClipTable<CAP> tb) {
   float total;
   const float f = clip_factor(tb, &total);
   if (blockIdx.x == 0 && threadIdx.x == 0 && tb.total != nullptr) *tb.total = total;
-  // the norm's last chunks first: they are still in L2
-  for (int i = int(blockIdx.x); i < tb.chunks; i += int(gridDim.x)) {
-    const int c = tb.chunks - 1 - i;
+  // a block's chunks of the norm's pass in the opposite order: the last are still in L2, on the
+  // side of the device that it is on
+  const int grid = int(gridDim.x), b = int(blockIdx.x);
+  for (int c = b + (tb.chunks - 1 - b) / grid * grid; b < tb.chunks && c >= 0; c -= grid) {
     const ClipTensor& t = tb.t[find_tensor(tb, c)];
     if (t.out == nullptr || (f == 1.f && t.out == t.grad)) continue;  // nothing to change
     const int64_t e0 = int64_t(c - t.first) * tb.chunk_elems - misalign(t.grad, elem_bytes(t.dt));
@@ -223,6 +257,7 @@ struct ClipCall {
   float* total;
   double* parts;
   bool scaling;
+  int bytes;  // of the largest element
   cudaStream_t stream;
 };
 
@@ -258,6 +293,7 @@ template <int CAP> flce_status clip_pass(const ClipCall& c, int elems, int pass,
     tb.chunks = int(chunks);
     tb.chunk_elems = elems;
     tb.inf_norm = c.inf_norm;
+    tb.keep = c.scaling ? int(kClipKeepBytes / (int64_t(elems) * c.bytes)) : 0;
     tb.max_norm = c.max_norm;
     tb.eps = c.eps;
     tb.scale = c.scale;
@@ -312,6 +348,7 @@ flce_status flce_clip_grad_norm(const flce_grad_tensor* tensors, int64_t count, 
   if (!api_aligned(total_norm, 4) || !api_aligned(workspace, 256)) return FLCE_ERR_ALIGNMENT;
   int64_t total = 0;
   bool scaling = false;
+  int bytes = 2;
   for (int64_t i = 0; i < count; ++i) {
     const flce_grad_tensor& t = tensors[i];
     if (t.n < 0) return bad("tensors", "a negative number of elements");
@@ -324,6 +361,7 @@ flce_status flce_clip_grad_norm(const flce_grad_tensor* tensors, int64_t count, 
       return FLCE_ERR_ALIGNMENT;
     total += t.n;
     scaling |= t.out != nullptr;
+    if (t.dtype == FLCE_DTYPE_F32) bytes = 4;
   }
   if (ws_bytes < flce_clip_grad_norm_workspace_size(count)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0, dev = -1;
@@ -339,7 +377,7 @@ flce_status flce_clip_grad_norm(const flce_grad_tensor* tensors, int64_t count, 
       return st;
   }
   const ClipCall c{tensors, count, std::isinf(norm_type), max_norm, eps, grad_scale, total_norm,
-                   static_cast<double*>(workspace), scaling, reinterpret_cast<cudaStream_t>(stream)};
+                   static_cast<double*>(workspace), scaling, bytes, reinterpret_cast<cudaStream_t>(stream)};
   const int elems = pick_chunk(total);
   int n_parts = 0;
   for (int pass = 0; pass < 2; ++pass) {
