@@ -77,15 +77,13 @@ constexpr int bn_planes(int x_bytes, int residual_bytes, bool gate_full, bool ba
 }
 
 // Batches of rows on their way in: as many as fit beside the parameters, of one row where there
-// is no room for two batches of two. At least two are needed: one in work, one landed. (Unaligned
-// rows are not copied: planes is 0.)
+// is no room for two batches of two. At least two are needed: one in work, one landed.
 struct BnRing {
   int per, batches, params_bytes;
 };
 constexpr BnRing bn_ring(const BlockNormShape& s, int planes, int feat, bool backward) {
   const int threads = s.threads_per_row * s.rows_per_block;
   BnRing r{kBnRows, 1, bn_shared_params(feat, backward) * 32 * s.threads_per_row + bn_own_params(feat, backward) * 32 * threads};
-  if (planes == 0) return r;
   const int room = kBnSmemBytes - r.params_bytes, row = planes * 16 * threads;
   if (room / (row * r.per) < 2) r.per = 1;
   r.batches = room / (row * r.per);

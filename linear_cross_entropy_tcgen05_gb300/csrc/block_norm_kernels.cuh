@@ -46,12 +46,28 @@ struct RowRing {
   __device__ __forceinline__ uint32_t after(uint32_t batch) const {
     return batch + batch_bytes == end ? first : batch + batch_bytes;
   }
-  template <typename T> __device__ __forceinline__ void copy(uint32_t row_at, int planes, const T* src) const {
+  // A thread's columns of a row into their planes.
+  template <typename T, bool VEC> __device__ __forceinline__ void copy(uint32_t to, int planes, const T* row, const Cols& cs) const {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T)) / 2; ++i)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(row_at + uint32_t((planes + i) * plane)),
-                   "l"(reinterpret_cast<const char*>(src) + 16 * i)
+      for (int i = 0; i < int(sizeof(T)) / 2; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + uint32_t((planes + i) * plane)),
+                     "l"(reinterpret_cast<const char*>(row + cs.col) + 16 * i)
+                     : "memory");
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (cs.at(i) < cs.D)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + uint32_t((planes + i / 4) * plane + i % 4 * 4)),
+                       "l"(row + cs.at(i))
+                       : "memory");
+    } else {
+      // 16-bit elements at odd places cannot be copied asynchronously
+      const Raw8<T> v = load8<T, false>(row, cs);
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + uint32_t(planes * plane)), "r"(v.v[0].x), "r"(v.v[0].y),
+                   "r"(v.v[0].z), "r"(v.v[0].w)
                    : "memory");
+    }
   }
   template <typename T> __device__ __forceinline__ void get(uint32_t batch, int r, int planes, float2 (&f)[4]) const {
     Raw8<T> v;
@@ -76,13 +92,13 @@ struct RowRing {
   }
 };
 
-// Address of a thread's columns in a row (computed where it is used: pointers that are kept
-// from row to row cost the registers that the sums need).
-template <typename T> __device__ __forceinline__ const T* row_at(const void* base, int64_t row, int64_t ld, int col) {
-  return static_cast<const T*>(base) + row * ld + col;
+// Address of a row (computed where it is used: pointers that are kept from row to row cost the
+// registers that the sums need).
+template <typename T> __device__ __forceinline__ const T* row_at(const void* base, int64_t row, int64_t ld) {
+  return static_cast<const T*>(base) + row * ld;
 }
-template <typename T> __device__ __forceinline__ T* row_at(void* base, int64_t row, int64_t ld, int col) {
-  return static_cast<T*>(base) + row * ld + col;
+template <typename T> __device__ __forceinline__ T* row_at(void* base, int64_t row, int64_t ld) {
+  return static_cast<T*>(base) + row * ld;
 }
 
 // Sums over the threads of a row, of NV values at once (those of several rows: a sum is all
@@ -92,7 +108,7 @@ template <typename T> __device__ __forceinline__ T* row_at(void* base, int64_t r
 // sum is enough: a buffer is written again only after the barrier of the sum between. Words
 // of warps that are not there stay zero.
 // CLUSTER: blocks share rows; code apart, for its registers.
-template <bool CLUSTER> struct RowSum {
+template <bool CLUSTER, bool VEC> struct RowSum {
   float* buf;      // [2][kWords] of this row group
   float* clus;     // [2][kBnMaxCluster][4] of this block
   int nw, warp, lane, bar, threads, turn;
@@ -186,7 +202,7 @@ template <bool CLUSTER> struct RowSum {
       }
       named_barrier_sync(uint32_t(bar), uint32_t(threads));
       float2 total[NR / 2], far[NR / 2], c[NR / 2];
-      const float first_inv = full > 0 ? 1.f / 256.f : part_inv;
+      const float first_inv = inv_columns(0);
 #pragma unroll
       for (int i = 0; i < NR / 2; ++i) {
         const float4 o = reinterpret_cast<const float4*>(b)[i];
@@ -203,9 +219,9 @@ template <bool CLUSTER> struct RowSum {
         }
       };
 #pragma unroll 3
-      for (int w = 0; w < full; ++w) add(w, 256.f, 1.f / 256.f);
-      if (part > 0) add(full, float(part), part_inv);
-      const float n = 256.f * float(full) + float(part), inv_n = CLUSTER ? (n > 0.f ? 1.f / n : 0.f) : inv_d;
+      for (int w = 0; w < (VEC ? full : nw); ++w) add(w, VEC ? 256.f : columns[w].x, VEC ? 1.f / 256.f : columns[w].y);
+      if (VEC && part > 0) add(full, float(part), part_inv);
+      const float n = CLUSTER ? block_columns(int(cluster_ctarank())) : float(D), inv_n = CLUSTER ? (n > 0.f ? 1.f / n : 0.f) : inv_d;
 #pragma unroll
       for (int i = 0; i < NR / 2; ++i) {
         const float2 m = fma2(total[i], both(inv_n), c[i]);  // this block's mean, less c
@@ -298,8 +314,15 @@ template <bool CLUSTER> struct RowSum {
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] += c[kMaxValues * r + i];
   }
-  int full, part;  // warps of this block with 256 columns, and the columns of the one after them
+  // Columns of the block's warps. VEC: `full` warps have 256 and the next one has `part`; else a
+  // table has each warp's and one over it.
+  int full, part;
   float part_inv;
+  const float2* columns;
+  __device__ __forceinline__ float inv_columns(int w) const {
+    if constexpr (!VEC) return columns[w].y;
+    return w < full ? 1.f / 256.f : w == full ? part_inv : 0.f;
+  }
 };
 
 struct RowThread {
@@ -338,29 +361,30 @@ __device__ __forceinline__ void derive8(const float2 (&a)[4], int act, float2 (&
 }
 
 template <typename TX, typename TR, bool VEC>
-__device__ __forceinline__ void load_gate(const BlockNormParams& p, int64_t grow, int col, float2 (&a)[4]) {
+__device__ __forceinline__ void load_gate(const BlockNormParams& p, int64_t grow, const Cols& cs, float2 (&a)[4]) {
   if (p.gate_res_type)
-    unpack8(load8<TR, VEC>(static_cast<const TR*>(p.gate) + grow * p.ld_gate, col, p.D), a);
+    unpack8(load8<TR, VEC>(static_cast<const TR*>(p.gate) + grow * p.ld_gate, cs), a);
   else
-    unpack8(load8<TX, VEC>(static_cast<const TX*>(p.gate) + grow * p.ld_gate, col, p.D), a);
+    unpack8(load8<TX, VEC>(static_cast<const TX*>(p.gate) + grow * p.ld_gate, cs), a);
   activate8(a, p.act);
 }
 
 // Parameters (zero past the row and where there are none), w + off; read once a block.
 template <bool VEC>
-__device__ __forceinline__ void load_weight(const void* w, int dt, float off, int col, int D, float2 (&f)[4]) {
+__device__ __forceinline__ void load_weight(const void* w, int dt, float off, const Cols& cs, float2 (&f)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = both(0.f);
-  if (w == nullptr || col >= D) return;
+  if (w == nullptr || cs.col >= cs.D) return;
   if (dt == ELEM_F32)
-    unpack8(load8<float, VEC>(static_cast<const float*>(w), col, D), f);
+    unpack8(load8<float, VEC>(static_cast<const float*>(w), cs), f);
   else if (dt == ELEM_BF16)
-    unpack8(load8<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w), col, D), f);
+    unpack8(load8<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w), cs), f);
   else
-    unpack8(load8<__half, VEC>(static_cast<const __half*>(w), col, D), f);
+    unpack8(load8<__half, VEC>(static_cast<const __half*>(w), cs), f);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    f[i] = make_float2(col + 2 * i < D ? f[i].x + off : 0.f, col + 2 * i + 1 < D ? f[i].y + off : 0.f);
+    f[i] = VEC ? make_float2(f[i].x + off, f[i].y + off)
+               : make_float2(cs.at(2 * i) < cs.D ? f[i].x + off : 0.f, cs.at(2 * i + 1) < cs.D ? f[i].y + off : 0.f);
 }
 
 // Eight values in shared memory, in two planes: a parameter's for a thread of a row, in the
@@ -388,38 +412,49 @@ __device__ __forceinline__ float dot8(const float2 (&a)[4], const float2 (&b)[4]
 }
 // Zeros in the columns past the row. VEC: a thread's columns are all in the row or all past it,
 // and what it reads there is zero already, so this is for what a mean was taken from.
-template <bool VEC> __device__ __forceinline__ void cut8(float2 (&v)[4], int col, int D) {
+template <bool VEC> __device__ __forceinline__ void cut8(float2 (&v)[4], const Cols& cs) {
   if constexpr (VEC) {
-    const float live = col < D ? 1.f : 0.f;
+    const float live = cs.col < cs.D ? 1.f : 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(live));
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = make_float2(col + 2 * i < D ? v[i].x : 0.f, col + 2 * i + 1 < D ? v[i].y : 0.f);
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_float2(cs.at(2 * i) < cs.D ? v[i].x : 0.f, cs.at(2 * i + 1) < cs.D ? v[i].y : 0.f);
   }
 }
 
 // at most kBnMaxThreads / 64 row groups use barriers
-constexpr int kRowSumWords = 4 + 2 * RowSum<false>::kMaxValues * kBnMaxCluster + kBnMaxThreads / 64 * 2 * RowSum<false>::kWords;
+constexpr int kRowSumWords = 4 + 2 * RowSum<false, true>::kMaxValues * kBnMaxCluster + kBnMaxThreads / 64 * 2 * RowSum<false, true>::kWords + 2 * kBnMaxThreads / 32;
 
-template <bool CLUSTER>
-__device__ __forceinline__ RowSum<CLUSTER> row_sum(float* scratch, const RowThread& r, int threads_per_row, int cluster, int D) {
-  RowSum<CLUSTER> rs;
+template <bool CLUSTER, bool VEC>
+__device__ __forceinline__ RowSum<CLUSTER, VEC> row_sum(float* scratch, const RowThread& r, int threads_per_row, int cluster, int D) {
+  RowSum<CLUSTER, VEC> rs;
   rs.D = D;
   const int cols = D - (r.col - 8 * r.t), most = 8 * threads_per_row;  // columns from this block's first on
   rs.full = (cols < 0 ? 0 : cols < most ? cols : most) / 256;
   rs.part = cols < 0 || cols >= most ? 0 : cols % 256;
   rs.part_inv = rs.part > 0 ? 1.f / float(rs.part) : 0.f;
+  rs.columns = reinterpret_cast<const float2*>(scratch + kRowSumWords - 2 * kBnMaxThreads / 32);
   rs.clus = scratch + 4;  // behind the cluster's two barriers
-  rs.buf = scratch + 4 + 2 * RowSum<false>::kMaxValues * kBnMaxCluster + (threads_per_row > 32 ? r.group * 2 * RowSum<false>::kWords : 0);
+  rs.buf = scratch + 4 + 2 * RowSum<false, true>::kMaxValues * kBnMaxCluster + (threads_per_row > 32 ? r.group * 2 * RowSum<false, true>::kWords : 0);
   for (int i = int(threadIdx.x); i < kRowSumWords; i += int(blockDim.x)) scratch[i] = 0.f;
   __syncthreads();
+  rs.nw = threads_per_row / 32;
+  if (!VEC && int(threadIdx.x) < rs.nw) {
+    float n = 0.f;  // of columns t + i threads_per_row, i = 0 ... 7, of warp threadIdx.x
+    for (int i = 0; i < 8; ++i) {
+      const int left = cols - i * threads_per_row - 32 * int(threadIdx.x);
+      n += float(left < 0 ? 0 : left < 32 ? left : 32);
+    }
+    const_cast<float2*>(rs.columns)[threadIdx.x] = make_float2(n, n > 0.f ? 1.f / n : 0.f);
+  }
+  if (!VEC) __syncthreads();
   if (CLUSTER && threadIdx.x == 0) {
     mbar_init(reinterpret_cast<uint64_t*>(scratch), 1);
     mbar_init(reinterpret_cast<uint64_t*>(scratch) + 1, 1);
     fence_barrier_init();  // for the other blocks, which the kernel's first cluster barrier waits for
   }
-  rs.nw = threads_per_row / 32;
   rs.warp = r.t / 32;
   rs.lane = r.t % 32;
   rs.bar = 1 + r.group;
@@ -434,10 +469,10 @@ __device__ __forceinline__ RowSum<CLUSTER> row_sum(float* scratch, const RowThre
 // squared distances from it over their own columns, so one sum over the row's warps is enough
 // and a large common offset costs no precision.
 template <int R, bool VEC, bool LAYER, typename SUM, typename F>
-__device__ __forceinline__ void row_stats(F&& get, int col, int D, bool layer, float eps, float inv_d, SUM& rs,
+__device__ __forceinline__ void row_stats(F&& get, const Cols& cs, bool layer, float eps, float inv_d, SUM& rs,
                                           float (&mean)[R], float (&rstd)[R]) {
   if (LAYER && layer) {
-    const float inv_n = rs.warp < rs.full ? 1.f / 256.f : rs.warp == rs.full ? rs.part_inv : 0.f;
+    const float inv_n = rs.inv_columns(rs.warp);
     float v1[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -453,7 +488,7 @@ __device__ __forceinline__ void row_stats(F&& get, int col, int D, bool layer, f
       const float m = __shfl_sync(0xffffffffu, s, r * (32 / R)) * inv_n;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = add2(v[i], both(-m));
-      cut8<VEC>(v, col, D);
+      cut8<VEC>(v, cs);
       v1[r] = dot8(v, v);
     }
     const float q = rs.scatter_sum(v1);
@@ -486,9 +521,10 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   constexpr int kX = 0, kR = sizeof(TX) / 2, kG = kR + sizeof(TR) / 2;  // planes of x, residual and full gate
   constexpr int kParams = bn_shared_params(FEAT, false);
   const RowThread r0 = row_thread(threads_per_row, cluster);
-  RowSum<CLUSTER> rs = row_sum<CLUSTER>(scratch, r0, threads_per_row, cluster, p.D);
-  const int col = r0.col, D = p.D;
-  const bool live = col < D;  // VEC: else a thread past the row, whose values are zero
+  RowSum<CLUSTER, VEC> rs = row_sum<CLUSTER, VEC>(scratch, r0, threads_per_row, cluster, p.D);
+  const int col = VEC ? r0.col : r0.col - 7 * r0.t, D = p.D;  // VEC or not, a block has 8 columns a thread
+  const Cols cs{col, VEC ? 1 : threads_per_row, D};
+  const bool live = col < D;  // else a thread past the row, whose values are zero
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
   constexpr bool gate_full = GATE && (FEAT & BN_GATE_ROWS) != 0;  // a gate for each row, else for groups of rows
   const int lo = int(r0.worker * p.chunk_rows < p.N ? r0.worker * p.chunk_rows : p.N);
@@ -500,23 +536,21 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     for (int r = 0; r < R; ++r) {
       if (live && r < per && next + r < hi) {
         const uint32_t to = at + uint32_t(r * ring.row_bytes);
-        ring.copy(to, kX, row_at<TX>(p.x, next + r, p.ld_x, col));
-        if (p.residual != nullptr) ring.copy(to, kR, row_at<TR>(p.residual, next + r, p.ld_residual, col));
+        ring.copy<TX, VEC>(to, kX, row_at<TX>(p.x, next + r, p.ld_x), cs);
+        if (p.residual != nullptr) ring.copy<TR, VEC>(to, kR, row_at<TR>(p.residual, next + r, p.ld_residual), cs);
         if (gate_full) {
           if (p.gate_res_type)
-            ring.copy(to, kG, row_at<TR>(p.gate, next + r, p.ld_gate, col));
+            ring.copy<TR, VEC>(to, kG, row_at<TR>(p.gate, next + r, p.ld_gate), cs);
           else
-            ring.copy(to, kG, row_at<TX>(p.gate, next + r, p.ld_gate, col));
+            ring.copy<TX, VEC>(to, kG, row_at<TX>(p.gate, next + r, p.ld_gate), cs);
         }
       }
     }
     next += per;
     ring.commit();
   };
-  if constexpr (VEC) {
-    ring.init(ring_smem + (FULL ? kParams * 32 * threads_per_row : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
-    for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
-  }
+  ring.init(ring_smem + (FULL ? kParams * 32 * threads_per_row : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
+  for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
   if (CLUSTER) cluster_sync_all();
   // Without FULL, c is what a row's value after the first norm is multiplied by: w1 scale
   // act(gate). With it w1 scale and b1 scale are in shared memory, and c is act(gate).
@@ -527,8 +561,8 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     if (r0.group == 0) shared_set(ring_smem, t16 + 2 * index * plane, plane, f);
   };
   constexpr int kW2 = 0, kB2 = 1, kW1 = 2, kB1 = 3;
-  load_weight<VEC>(p.w1, p.w1_dt, p.w_off, col, D, w1);
-  load_weight<VEC>(p.w2, p.w2_dt, p.w_off, col, D, w2);
+  load_weight<VEC>(p.w1, p.w1_dt, p.w_off, cs, w1);
+  load_weight<VEC>(p.w2, p.w2_dt, p.w_off, cs, w2);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     w1[i] = post ? mul2(w1[i], both(p.scale)) : both(p.scale);
@@ -538,9 +572,9 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     float2 b[4];
     set_param(kW2, w2);
     set_param(kW1, w1);
-    load_weight<VEC>(p.b2, p.b2_dt, 0.f, col, D, b);
+    load_weight<VEC>(p.b2, p.b2_dt, 0.f, cs, b);
     set_param(kB2, b);
-    load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, b);
+    load_weight<VEC>(p.b1, p.b1_dt, 0.f, cs, b);
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = mul2(b[i], both(p.scale));
     set_param(kB1, b);
@@ -555,18 +589,12 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   // The first norm of a batch and the second norm of the batch before it share a sum: the
   // latency of a batch is one sum, and what comes before and after it is independent work.
   uint32_t batch = ring.first;
-  auto get_x = [&](uint32_t at, int first, int r, float2 (&v)[4]) FLCE_INLINE {
-    if constexpr (VEC)
-      ring.get<TX>(at, r, kX, v);
-    else
-      unpack8(r < per && first + r < hi ? load8<TX, VEC>(static_cast<const TX*>(p.x) + (first + r) * p.ld_x, col, D) : raw_zero<TX>(), v);
-  };
   float m1[R], r1[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) m1[r] = 0.f, r1[r] = 1.f;
   if (lo < hi) {
-    if constexpr (VEC) ring.wait(batches - 1);
-    if (post) row_stats<R, VEC, FULL, RowSum<CLUSTER>>([&](int r, float2 (&v)[4]) { get_x(batch, lo, r, v); }, col, D, p.layer, p.eps, inv_d, rs, m1, r1);
+    ring.wait(batches - 1);
+    if (post) row_stats<R, VEC, FULL, RowSum<CLUSTER, VEC>>([&](int r, float2 (&v)[4]) { ring.get<TX>(batch, r, kX, v); }, cs, p.layer, p.eps, inv_d, rs, m1, r1);
   }
   for (int row = lo; row < hi; row += per) {
     const bool second = per > 1 && row + 1 < hi;  // the last batch may have one row
@@ -580,30 +608,22 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
       }
       if (gate_full) {
         float2 a[4];
-        if constexpr (VEC) {
-          if (p.gate_res_type)
-            ring.get<TR>(batch, r, kG, a);
-          else
-            ring.get<TX>(batch, r, kG, a);
-          activate8(a, p.act);
-        } else {
-          load_gate<TX, TR, VEC>(p, row + r, col, a);
-        }
+        if (p.gate_res_type)
+          ring.get<TR>(batch, r, kG, a);
+        else
+          ring.get<TX>(batch, r, kG, a);
+        activate8(a, p.act);
         set_gate(a);
       } else if (gate && row + r >= gate_end) {
         const int g = (row + r) / int(p.gate_group);
         float2 a[4];
-        load_gate<TX, TR, VEC>(p, g, col, a);
+        load_gate<TX, TR, VEC>(p, g, cs, a);
         set_gate(a);
         gate_end = int((g + 1) * p.gate_group);
       }
       float2 u[4];
-      get_x(batch, row, r, u);
-      if constexpr (VEC) {
-        ring.get<TR>(batch, r, kR, h[r]);
-      } else {
-        unpack8(p.residual == nullptr ? raw_zero<TR>() : load8<TR, VEC>(static_cast<const TR*>(p.residual) + (row + r) * p.ld_residual, col, D), h[r]);
-      }
+      ring.get<TX>(batch, r, kX, u);
+      ring.get<TR>(batch, r, kR, h[r]);
       if (FULL) {
         float2 w[4], b[4];
         param(kW1, w);
@@ -620,31 +640,28 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
           h[r][i] = fma2(u[i], c[i], h[r][i]);
         }
       }
-      store8_at<TR, VEC>(row_at<TR>(p.h, row + r, D, col), col, D, h[r]);
+      store8<TR, VEC>(row_at<TR>(p.h, row + r, D), cs, h[r]);
     }
     float m2[R], r2[R], n1[R], k1[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) m2[r] = r2[r] = n1[r] = 0.f, k1[r] = 1.f;
-    if constexpr (VEC) {
-      fetch(batch);
-      batch = ring.after(batch);
-      ring.wait(batches - 1);
-    }
+    fetch(batch);
+    batch = ring.after(batch);
+    ring.wait(batches - 1);
     auto get_h = [&](int r, float2 (&v)[4]) FLCE_INLINE {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = h[r][i];
     };
-    const int after = row + per;
     if (post && pre) {
       float mean[2 * R], rstd[2 * R];
-      row_stats<2 * R, VEC, FULL, RowSum<CLUSTER>>(
+      row_stats<2 * R, VEC, FULL, RowSum<CLUSTER, VEC>>(
           [&](int r, float2 (&v)[4]) {
             if (r < R)
               get_h(r, v);
             else
-              get_x(batch, after, r - R, v);
+              ring.get<TX>(batch, r - R, kX, v);
           },
-          col, D, p.layer, p.eps, inv_d, rs, mean, rstd);
+          cs, p.layer, p.eps, inv_d, rs, mean, rstd);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         m2[r] = mean[r];
@@ -653,9 +670,9 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
         k1[r] = rstd[R + r];
       }
     } else if (pre) {
-      row_stats<R, VEC, FULL, RowSum<CLUSTER>>(get_h, col, D, p.layer, p.eps, inv_d, rs, m2, r2);
+      row_stats<R, VEC, FULL, RowSum<CLUSTER, VEC>>(get_h, cs, p.layer, p.eps, inv_d, rs, m2, r2);
     } else if (post) {
-      row_stats<R, VEC, FULL, RowSum<CLUSTER>>([&](int r, float2 (&v)[4]) { get_x(batch, after, r, v); }, col, D, p.layer, p.eps, inv_d, rs, n1, k1);
+      row_stats<R, VEC, FULL, RowSum<CLUSTER, VEC>>([&](int r, float2 (&v)[4]) { ring.get<TX>(batch, r, kX, v); }, cs, p.layer, p.eps, inv_d, rs, n1, k1);
     }
     if (pre) {
       float2 b2[4];
@@ -673,7 +690,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
           else
             h[r][i] = mul2(mul2(h[r][i], both(r2[r])), w2[i]);
         }
-        store8_at<TX, VEC>(row_at<TX>(p.y, row + r, D, col), col, D, h[r]);
+        store8<TX, VEC>(row_at<TX>(p.y, row + r, D), cs, h[r]);
       }
     }
     if (p.stats != nullptr && col == 0) {
@@ -707,8 +724,9 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   // in shared memory: a bias's sum, and with a gate that and both biases' sums
   constexpr bool OWN_B = POST && FULL, OWN_A = POST && GATE && FULL;
   const RowThread r0 = row_thread(threads_per_row, cluster);
-  RowSum<CLUSTER> rs = row_sum<CLUSTER>(scratch, r0, threads_per_row, cluster, p.D);
-  const int col = r0.col, D = p.D;
+  RowSum<CLUSTER, VEC> rs = row_sum<CLUSTER, VEC>(scratch, r0, threads_per_row, cluster, p.D);
+  const int col = VEC ? r0.col : r0.col - 7 * r0.t, D = p.D;  // VEC or not, a block has 8 columns a thread
+  const Cols cs{col, VEC ? 1 : threads_per_row, D};
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
   constexpr bool gate_full = GATE && (FEAT & BN_GATE_ROWS) != 0;  // a gate for each row, else for groups of rows
   const int workers = int(gridDim.x) / cluster * (int(blockDim.x) / threads_per_row);
@@ -746,15 +764,15 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
           if (r > 0 && (r >= per || ahead.row + r >= ahead.hi)) continue;
           const uint32_t to = at + uint32_t(r * ring.row_bytes);
           const int row = ahead.row + r;
-          ring.copy(to, kX, row_at<TX>(p.x, row, p.ld_x, col));
-          if (pre) ring.copy(to, kH, row_at<TR>(p.h_in, row, D, col));
-          if (p.dh != nullptr) ring.copy(to, kDh, row_at<TR>(p.dh, row, p.ld_dh, col));
-          if (pre && p.dy != nullptr) ring.copy(to, kY, row_at<TX>(p.dy, row, p.ld_dy, col));
+          ring.copy<TX, VEC>(to, kX, row_at<TX>(p.x, row, p.ld_x), cs);
+          if (pre) ring.copy<TR, VEC>(to, kH, row_at<TR>(p.h_in, row, D), cs);
+          if (p.dh != nullptr) ring.copy<TR, VEC>(to, kDh, row_at<TR>(p.dh, row, p.ld_dh), cs);
+          if (pre && p.dy != nullptr) ring.copy<TX, VEC>(to, kY, row_at<TX>(p.dy, row, p.ld_dy), cs);
           if (gate_full) {
             if (p.gate_res_type)
-              ring.copy(to, kG, row_at<TR>(p.gate, row, p.ld_gate, col));
+              ring.copy<TR, VEC>(to, kG, row_at<TR>(p.gate, row, p.ld_gate), cs);
             else
-              ring.copy(to, kG, row_at<TX>(p.gate, row, p.ld_gate, col));
+              ring.copy<TX, VEC>(to, kG, row_at<TX>(p.gate, row, p.ld_gate), cs);
           }
         }
       }
@@ -767,10 +785,9 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     ring.commit();
     stat_slot = stat_slot + 1 == batches ? 0 : stat_slot + 1;
   };
-  if constexpr (VEC) {
-    ring.init(ring_smem + kParams * 32 * threads_per_row + bn_own_params(FEAT, true) * 32 * int(blockDim.x), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
-    for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
-  }
+  ring.init(ring_smem + kParams * 32 * threads_per_row + bn_own_params(FEAT, true) * 32 * int(blockDim.x),
+            kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
+  for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
   if (CLUSTER) cluster_sync_all();
   float2 w1[4], w2[4], a[4], dw1[4], db1[4], dw2[4], db2[4];
   const int t16 = 16 * r0.t, plane = 16 * threads_per_row;  // a parameter's values for this thread
@@ -786,8 +803,8 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     shared_set(ring_smem, own_at + 2 * index * own_plane, own_plane, f);
   };
   constexpr int kDb1 = 0, kA = 1, kDb2 = 2;
-  load_weight<VEC>(p.w2, p.w2_dt, p.w_off, col, D, w2);
-  if (POST) load_weight<VEC>(p.w1, p.w1_dt, p.w_off, col, D, w1);
+  load_weight<VEC>(p.w2, p.w2_dt, p.w_off, cs, w2);
+  if (POST) load_weight<VEC>(p.w1, p.w1_dt, p.w_off, cs, w1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     a[i] = both(1.f);
@@ -803,33 +820,23 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   if (OWN_B) set_own(kDb1, db1);
   const float inv_d = 1.f / float(D), inv_d0 = p.layer ? inv_d : 0.f;
   const float live = live_col ? 1.f : 0.f;  // threads past the row: their values stay zero
-  // values of a row of the batch in slot `at`, whose first row is `first`
-  auto get_x = [&](uint32_t at, int first, int r, float m1, float2 (&v)[4]) FLCE_INLINE {
-    if constexpr (VEC) ring.get<TX>(at, r, kX, v);
-    else unpack8(load8<TX, VEC>(static_cast<const TX*>(p.x) + (first + r) * p.ld_x, col, D), v);
+  // values of row r of the batch in slot `at`
+  auto get_x = [&](uint32_t at, int r, float m1, float2 (&v)[4]) FLCE_INLINE {
+    ring.get<TX>(at, r, kX, v);
     if (FULL && POST) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = add2(v[i], both(-m1));
     }
   };
-  auto get_h = [&](uint32_t at, int first, int r, float m2, float2 (&v)[4]) FLCE_INLINE {
-    if constexpr (VEC) ring.get<TR>(at, r, kH, v);
-    else unpack8(load8<TR, VEC>(static_cast<const TR*>(p.h_in) + int64_t(first + r) * D, col, D), v);
+  auto get_h = [&](uint32_t at, int r, float m2, float2 (&v)[4]) FLCE_INLINE {
+    ring.get<TR>(at, r, kH, v);
     if (FULL) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = add2(v[i], both(-m2));
     }
   };
-  auto get_dy = [&](uint32_t at, int first, int r, float2 (&v)[4]) FLCE_INLINE {
-    if constexpr (VEC) ring.get<TX>(at, r, kY, v);
-    else unpack8(p.dy == nullptr ? raw_zero<TX>() : load8<TX, VEC>(static_cast<const TX*>(p.dy) + (first + r) * p.ld_dy, col, D), v);
-  };
-  auto get_dh = [&](uint32_t at, int first, int r, float2 (&v)[4]) FLCE_INLINE {
-    if constexpr (VEC) ring.get<TR>(at, r, kDh, v);
-    else unpack8(p.dh == nullptr ? raw_zero<TR>() : load8<TR, VEC>(static_cast<const TR*>(p.dh) + (first + r) * p.ld_dh, col, D), v);
-  };
-  auto get_stats = [&](int slot, int first, int r) FLCE_INLINE {
-    float4 s = VEC ? warp_stats[threadIdx.x / 32][slot][r] : stats[first + r];
+  auto get_stats = [&](int slot, int r) FLCE_INLINE {
+    float4 s = warp_stats[threadIdx.x / 32][slot][r];
     s.y = post ? s.y * live : live;
     s.w *= live;
     return s;
@@ -848,10 +855,10 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     for (int r = 0; r < R; ++r) {
       s1[r] = s0[r] = 0.f;
       if (r > 0 && (r >= per || w.row + r >= w.hi)) continue;
-      const float4 st = get_stats(slot, w.row, r);
+      const float4 st = get_stats(slot, r);
       float2 n[4], g[4];
-      get_h(at, w.row, r, st.z, n);
-      get_dy(at, w.row, r, g);
+      get_h(at, r, st.z, n);
+      ring.get<TX>(at, r, kY, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], w2[i]);
       s1[r] = dot8(g, n);
@@ -885,7 +892,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   int slot = 0;
   auto enter = [&](int chunk) FLCE_INLINE {  // a chunk has one gate row
     if (gate && !gate_full && chunk < p.chunks) {
-      load_gate<TX, TR, VEC>(p, chunk / int(p.chunks_per_group), col, a);
+      load_gate<TX, TR, VEC>(p, chunk / int(p.chunks_per_group), cs, a);
       if (OWN_A) set_own(kA, a);
     }
   };
@@ -894,10 +901,8 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
 #pragma unroll
   for (int r = 0; r < R; ++r) s1[r] = s0[r] = t1[r] = t0[r] = 0.f;
   if (now.chunk < p.chunks && pre) {
-    if constexpr (VEC) {
-      ring.wait(batches - 1);
-      __syncwarp();
-    }
+    ring.wait(batches - 1);
+    __syncwarp();
     second_norm(batch, slot, now, s1, s0);
     total(t1, t0, s1, s0);
   }
@@ -906,7 +911,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     const bool second = per > 1 && row + 1 < now.hi;  // a chunk's last batch may have one row
     Rows next = now;
     step(next);
-    if (!pre && VEC) {
+    if (!pre) {
       ring.wait(batches - 1);
       __syncwarp();
     }
@@ -916,12 +921,12 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     for (int r = 0; r < R; ++r) {
       t1[r] = t0[r] = 0.f;
       if (r > 0 && !second) continue;
-      const float4 st = get_stats(slot, row, r);
-      get_dh(batch, row, r, d[r]);
+      const float4 st = get_stats(slot, r);
+      ring.get<TR>(batch, r, kDh, d[r]);
       if (pre) {
         float2 n[4], g[4];
-        get_h(batch, row, r, st.z, n);
-        get_dy(batch, row, r, g);
+        get_h(batch, r, st.z, n);
+        ring.get<TX>(batch, r, kY, g);
         if (FULL) param(kW2, w2);
         if (FULL) {
           if (OWN_A) own(kDb2, db2);
@@ -938,25 +943,21 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
           d[r][i] = fma2(g[i], w2[i], d[r][i]);
           dw2[i] = fma2(g[i], n[i], dw2[i]);
         }
-        if (!VEC && FULL) cut8<VEC>(d[r], col, D);
+        if (!VEC && FULL) cut8<VEC>(d[r], cs);
       }
-      if (p.dres != nullptr) store8_at<TR, VEC>(static_cast<TR*>(p.dres) + int64_t(row + r) * D + col, col, D, d[r]);
+      if (p.dres != nullptr) store8<TR, VEC>(row_at<TR>(p.dres, row + r, D), cs, d[r]);
       float2 x[4];
-      if (POST || GATE) get_x(batch, row, r, st.x, x);
+      if (POST || GATE) get_x(batch, r, st.x, x);
       if (gate_full) {
-        if constexpr (VEC) {
-          if (p.gate_res_type)
-            ring.get<TR>(batch, r, kG, a);
-          else
-            ring.get<TX>(batch, r, kG, a);
-          activate8(a, p.act);
-        } else {
-          load_gate<TX, TR, VEC>(p, row + r, col, a);
-        }
+        if (p.gate_res_type)
+          ring.get<TR>(batch, r, kG, a);
+        else
+          ring.get<TX>(batch, r, kG, a);
+        activate8(a, p.act);
         if (p.dgate != nullptr) {  // d u scale act', u = (x - m) r w1 + b1, or x
           float2 e[4], da[4];
           derive8(a, p.act, da);
-          if (FULL && post) load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, e);
+          if (FULL && post) load_weight<VEC>(p.b1, p.b1_dt, 0.f, cs, e);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float2 u = x[i];
@@ -965,9 +966,9 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
             e[i] = mul2(mul2(u, d[r][i]), mul2(da[i], both(p.scale)));
           }
           if (p.gate_res_type)
-            store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(row + r) * D, col, D, e);
+            store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(row + r) * D, cs, e);
           else
-            store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(row + r) * D, col, D, e);
+            store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(row + r) * D, cs, e);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[r][i] = mul2(d[r][i], a[i]);
@@ -998,10 +999,8 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     const uint32_t batch_next = ring.after(batch);
     const int slot_next = slot + 1 == batches ? 0 : slot + 1;
     if (pre && next.chunk < p.chunks) {
-      if constexpr (VEC) {
-        ring.wait(batches - 2);
-        __syncwarp();
-      }
+      ring.wait(batches - 2);
+      __syncwarp();
       second_norm(batch_next, slot_next, next, s1, s0);
     }
     if (pre || post) total(t1, t0, s1, s0);
@@ -1010,9 +1009,9 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
       for (int r = 0; r < R; ++r) {
         if (r > 0 && !second) continue;
         if (post) {
-          const float4 st = get_stats(slot, row, r);
+          const float4 st = get_stats(slot, r);
           float2 x[4];
-          get_x(batch, row, r, st.x, x);
+          get_x(batch, r, st.x, x);
           const float s = st.y * p.scale;
           const float2 k1 = both(-(t1[r] * st.y * inv_d) * st.y * s), k0 = both(-s * (t0[r] * inv_d0)), k = both(s);
 #pragma unroll
@@ -1026,13 +1025,11 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[r][i] = mul2(d[r][i], both(p.scale));
         }
-        store8_at<TX, VEC>(static_cast<TX*>(p.dx) + int64_t(row + r) * D + col, col, D, d[r]);
+        store8<TX, VEC>(row_at<TX>(p.dx, row + r, D), cs, d[r]);
       }
     }
-    if constexpr (VEC) {
-      __syncwarp();  // the warp has read the batch's statistics
-      fetch(batch);
-    }
+    __syncwarp();  // the warp has read the batch's statistics
+    fetch(batch);
     // The end of a gate group's chunk. With P = sum of d n and Q = sum of d over its rows (d before
     // the gate, n = (x - m) r), the gate's gradient is (w1 P + b1 Q) scale act', and the chunk's
     // part of w1's and b1's is scale a P and scale a Q.
@@ -1043,7 +1040,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
       if (FULL && POST) param(kW1, w1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) q[i] = both(0.f);
-      if (FULL && POST) load_weight<VEC>(p.b1, p.b1_dt, 0.f, col, D, q);
+      if (FULL && POST) load_weight<VEC>(p.b1, p.b1_dt, 0.f, cs, q);
       derive8(a, p.act, da);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -1053,11 +1050,11 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
       }
       if (p.dgate == nullptr) {
       } else if (p.part_gate != nullptr) {
-        store8<float, VEC>(p.part_gate + int64_t(now.chunk) * D, col, D, e);
+        store8<float, VEC>(p.part_gate + int64_t(now.chunk) * D, cs, e);
       } else if (p.gate_res_type) {
-        store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, col, D, e);
+        store8<TR, VEC>(static_cast<TR*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, cs, e);
       } else {
-        store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, col, D, e);
+        store8<TX, VEC>(static_cast<TX*>(p.dgate) + int64_t(now.chunk / int(p.chunks_per_group)) * D, cs, e);
       }
       // the worker's sums of w1 and b1 over its chunks are in the workspace
       auto add_part = [&](float* part, const float2 (&v)[4]) FLCE_INLINE {
@@ -1066,10 +1063,10 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
         float2 sum[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = both(0.f);
-        if (now.chunk != int(r0.worker)) unpack8(load8<float, VEC>(at, col, D), sum);
+        if (now.chunk != int(r0.worker)) unpack8(load8<float, VEC>(at, cs), sum);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = fma2(v[i], mul2(a[i], both(p.scale)), sum[i]);
-        store8<float, VEC>(at, col, D, sum);
+        store8<float, VEC>(at, cs, sum);
       };
       if (POST) add_part(p.part[0], dw1);
       if (POST && FULL) add_part(p.part[1], db1);
@@ -1104,7 +1101,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = mul2(s[i], both(scale));
-    store8<float, VEC>(part + block * D, col, D, s);
+    store8<float, VEC>(part + block * D, cs, s);
   };
   if (OWN_A) own(kDb2, db2);
   if (OWN_B) {
@@ -1115,8 +1112,8 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
     if (POST) flush(p.part[0], dw1, p.scale);
     if (POST && FULL) flush(p.part[1], db1, p.scale);
   } else if (r0.worker >= p.chunks) {  // a worker without a chunk: its sums are zero
-    if (POST && p.part[0] != nullptr) store8<float, VEC>(p.part[0] + r0.worker * D, col, D, dw1);
-    if (POST && FULL && p.part[1] != nullptr) store8<float, VEC>(p.part[1] + r0.worker * D, col, D, dw1);
+    if (POST && p.part[0] != nullptr) store8<float, VEC>(p.part[0] + r0.worker * D, cs, dw1);
+    if (POST && FULL && p.part[1] != nullptr) store8<float, VEC>(p.part[1] + r0.worker * D, cs, dw1);
   }
   flush(p.part[2], dw2, 1.f);
   if (FULL) flush(p.part[3], db2, 1.f);
@@ -1152,7 +1149,7 @@ cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& 
 #define FLCE_BN_CASE(VEC, CLUSTER, FEAT) \
   case FEAT: return bn_launch(KERNEL<TX, TR, VEC, CLUSTER, FEAT>, p, s, blocks, planes, FEAT, BACKWARD, stream)
 #define FLCE_BN_DISPATCH                                                                    \
-  const int planes = vec ? bn_planes(int(sizeof(TX)), int(sizeof(TR)), p.gate_full, BACKWARD) : 0; \
+  const int planes = bn_planes(int(sizeof(TX)), int(sizeof(TR)), p.gate_full, BACKWARD);    \
   if (!vec && s.cluster > 1) {                                                              \
     switch (feat) { FLCE_BN_CASE(false, true, 7); FLCE_BN_CASE(false, true, 15); }          \
   } else if (!vec) {                                                                        \

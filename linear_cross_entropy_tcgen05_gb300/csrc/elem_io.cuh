@@ -179,40 +179,33 @@ template <typename T> __device__ __forceinline__ Raw8<T> pack8(const float2 (&f)
   return pack8<T>(g);
 }
 
-// Elements [col, col + 8) of a row of D elements; columns past the row read as zero and are
-// not written. VEC: rows are aligned to eight elements and D is a multiple of eight.
-template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> load8(const T* row, int col, int D) {
+// A thread's eight columns of a row of D: col, col + 1, ... where rows are aligned to eight elements
+// and D is a multiple of eight (VEC: one access), else col, col + step, ... with neighbouring
+// threads on neighbouring columns. Columns past the row read as zero and are not written.
+struct Cols {
+  int col, step, D;
+  __device__ __forceinline__ int at(int i) const { return col + i * step; }
+};
+
+template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> load8(const T* row, const Cols& c) {
   if constexpr (VEC) {
-    return col < D ? raw_load(row + col) : raw_zero<T>();
+    return c.col < c.D ? raw_load(row + c.col) : raw_zero<T>();
   } else {
     float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = col + i < D ? to_f32(row[col + i]) : 0.f;
+    for (int i = 0; i < 8; ++i) f[i] = c.at(i) < c.D ? to_f32(row[c.at(i)]) : 0.f;
     return pack8<T>(f);
   }
 }
 
-template <typename T, bool VEC> __device__ __forceinline__ void store8(T* row, int col, int D, const float (&f)[8]) {
+template <typename T, bool VEC> __device__ __forceinline__ void store8(T* row, const Cols& c, const float2 (&f)[4]) {
   if constexpr (VEC) {
-    if (col < D) raw_store(row + col, pack8<T>(f));
+    if (c.col < c.D) raw_store(row + c.col, pack8<T>(f));
   } else {
+    const float g[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (col + i < D) row[col + i] = from_f32<T>(f[i]);
-  }
-}
-
-template <typename T, bool VEC> __device__ __forceinline__ void store8(T* row, int col, int D, const float2 (&f)[4]) {
-  const float g[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
-  store8<T, VEC>(row, col, D, g);
-}
-
-// The same where `at` is the address of column col.
-template <typename T, bool VEC> __device__ __forceinline__ void store8_at(T* at, int col, int D, const float2 (&f)[4]) {
-  if constexpr (VEC) {
-    if (col < D) raw_store(at, pack8<T>(f));
-  } else {
-    store8<T, VEC>(at - col, col, D, f);
+      if (c.at(i) < c.D) row[c.at(i)] = from_f32<T>(g[i]);
   }
 }
 

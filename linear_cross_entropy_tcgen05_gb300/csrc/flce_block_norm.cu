@@ -39,7 +39,6 @@ int64_t bn_resident(const BlockNormShape& s) {
 // room for two batches of them (fp32
 // rows of 4096 columns with a gate for each), so that clusters share them.
 int bn_threads(const flce_block_norm_desc* d, bool vec, int feat, bool backward) {
-  if (!vec) return kBnMaxThreads;
   const int planes = bn_planes(elem_bytes(d->x_dtype), elem_bytes(d->residual_dtype), d->gate && d->gate_rows == d->N, backward);
   const BlockNormShape s = bn_shape(d->D, kBnMaxThreads);
   return bn_ring(s, planes, bn_kernel_features(feat, vec, s.cluster), backward).batches >= 2 ? kBnMaxThreads : kBnMaxThreads / 2;
