@@ -46,8 +46,11 @@ struct RowRing {
   __device__ __forceinline__ uint32_t after(uint32_t batch) const {
     return batch + batch_bytes == end ? first : batch + batch_bytes;
   }
-  // A thread's columns of a row into their planes.
-  template <typename T, bool VEC> __device__ __forceinline__ void copy(uint32_t to, int planes, const T* row, const Cols& cs) const {
+  // A thread's columns of a row into their planes. What cannot be copied asynchronously, 16-bit
+  // elements at odd places, is returned, for land(): all are on their way before the first is
+  // waited for.
+  template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> copy(uint32_t to, int planes, const T* row, const Cols& cs) const {
+    Raw8<T> v{};
     if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < int(sizeof(T)) / 2; ++i)
@@ -55,19 +58,23 @@ struct RowRing {
                      "l"(reinterpret_cast<const char*>(row + cs.col) + 16 * i)
                      : "memory");
     } else if constexpr (sizeof(T) == 4) {
+      const Cols c = cs.afresh();
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (cs.at(i) < cs.D)
+        if (c.at(i) < c.D)
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + uint32_t((planes + i / 4) * plane + i % 4 * 4)),
-                       "l"(row + cs.at(i))
+                       "l"(row + c.at(i))
                        : "memory");
     } else {
-      // 16-bit elements at odd places cannot be copied asynchronously
-      const Raw8<T> v = load8<T, false>(row, cs);
+      v = load8<T, false>(row, cs);
+    }
+    return v;
+  }
+  template <typename T, bool VEC> __device__ __forceinline__ void land(uint32_t to, int planes, const Raw8<T>& v) const {
+    if constexpr (!VEC && sizeof(T) == 2)
       asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + uint32_t(planes * plane)), "r"(v.v[0].x), "r"(v.v[0].y),
                    "r"(v.v[0].z), "r"(v.v[0].w)
                    : "memory");
-    }
   }
   template <typename T> __device__ __forceinline__ void get(uint32_t batch, int r, int planes, float2 (&f)[4]) const {
     Raw8<T> v;
@@ -418,9 +425,9 @@ template <bool VEC> __device__ __forceinline__ void cut8(float2 (&v)[4], const C
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(live));
   } else {
+    const Cols c = cs.afresh();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = make_float2(cs.at(2 * i) < cs.D ? v[i].x : 0.f, cs.at(2 * i + 1) < cs.D ? v[i].y : 0.f);
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(c.at(2 * i) < c.D ? v[i].x : 0.f, c.at(2 * i + 1) < c.D ? v[i].y : 0.f);
   }
 }
 
@@ -523,7 +530,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   const RowThread r0 = row_thread(threads_per_row, cluster);
   RowSum<CLUSTER, VEC> rs = row_sum<CLUSTER, VEC>(scratch, r0, threads_per_row, cluster, p.D);
   const int col = VEC ? r0.col : r0.col - 7 * r0.t, D = p.D;  // VEC or not, a block has 8 columns a thread
-  const Cols cs{col, VEC ? 1 : threads_per_row, D};
+  const Cols cs{col, VEC ? 1 : threads_per_row, D, true};
   const bool live = col < D;  // else a thread past the row, whose values are zero
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
   constexpr bool gate_full = GATE && (FEAT & BN_GATE_ROWS) != 0;  // a gate for each row, else for groups of rows
@@ -532,19 +539,25 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   RowRing ring{};
   int next = lo;  // the row that is copied next
   auto fetch = [&](uint32_t at) FLCE_INLINE {
+    Raw8<TX> x[R], gx[R];
+    Raw8<TR> res[R], gr[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (live && r < per && next + r < hi) {
-        const uint32_t to = at + uint32_t(r * ring.row_bytes);
-        ring.copy<TX, VEC>(to, kX, row_at<TX>(p.x, next + r, p.ld_x), cs);
-        if (p.residual != nullptr) ring.copy<TR, VEC>(to, kR, row_at<TR>(p.residual, next + r, p.ld_residual), cs);
-        if (gate_full) {
-          if (p.gate_res_type)
-            ring.copy<TR, VEC>(to, kG, row_at<TR>(p.gate, next + r, p.ld_gate), cs);
-          else
-            ring.copy<TX, VEC>(to, kG, row_at<TX>(p.gate, next + r, p.ld_gate), cs);
-        }
-      }
+      if (!live || r >= per || next + r >= hi) continue;
+      const uint32_t to = at + uint32_t(r * ring.row_bytes);
+      x[r] = ring.copy<TX, VEC>(to, kX, row_at<TX>(p.x, next + r, p.ld_x), cs);
+      if (p.residual != nullptr) res[r] = ring.copy<TR, VEC>(to, kR, row_at<TR>(p.residual, next + r, p.ld_residual), cs);
+      if (gate_full && p.gate_res_type) gr[r] = ring.copy<TR, VEC>(to, kG, row_at<TR>(p.gate, next + r, p.ld_gate), cs);
+      if (gate_full && !p.gate_res_type) gx[r] = ring.copy<TX, VEC>(to, kG, row_at<TX>(p.gate, next + r, p.ld_gate), cs);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (!live || r >= per || next + r >= hi) continue;
+      const uint32_t to = at + uint32_t(r * ring.row_bytes);
+      ring.land<TX, VEC>(to, kX, x[r]);
+      if (p.residual != nullptr) ring.land<TR, VEC>(to, kR, res[r]);
+      if (gate_full && p.gate_res_type) ring.land<TR, VEC>(to, kG, gr[r]);
+      if (gate_full && !p.gate_res_type) ring.land<TX, VEC>(to, kG, gx[r]);
     }
     next += per;
     ring.commit();
@@ -726,7 +739,7 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
   const RowThread r0 = row_thread(threads_per_row, cluster);
   RowSum<CLUSTER, VEC> rs = row_sum<CLUSTER, VEC>(scratch, r0, threads_per_row, cluster, p.D);
   const int col = VEC ? r0.col : r0.col - 7 * r0.t, D = p.D;  // VEC or not, a block has 8 columns a thread
-  const Cols cs{col, VEC ? 1 : threads_per_row, D};
+  const Cols cs{col, VEC ? 1 : threads_per_row, D, false};
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
   constexpr bool gate_full = GATE && (FEAT & BN_GATE_ROWS) != 0;  // a gate for each row, else for groups of rows
   const int workers = int(gridDim.x) / cluster * (int(blockDim.x) / threads_per_row);
@@ -764,16 +777,22 @@ __global__ void __launch_bounds__(kBnMaxThreads, 1)
           if (r > 0 && (r >= per || ahead.row + r >= ahead.hi)) continue;
           const uint32_t to = at + uint32_t(r * ring.row_bytes);
           const int row = ahead.row + r;
-          ring.copy<TX, VEC>(to, kX, row_at<TX>(p.x, row, p.ld_x), cs);
-          if (pre) ring.copy<TR, VEC>(to, kH, row_at<TR>(p.h_in, row, D), cs);
-          if (p.dh != nullptr) ring.copy<TR, VEC>(to, kDh, row_at<TR>(p.dh, row, p.ld_dh), cs);
-          if (pre && p.dy != nullptr) ring.copy<TX, VEC>(to, kY, row_at<TX>(p.dy, row, p.ld_dy), cs);
+          const Raw8<TX> x = ring.copy<TX, VEC>(to, kX, row_at<TX>(p.x, row, p.ld_x), cs);
+          Raw8<TR> h = raw_zero<TR>(), dh = raw_zero<TR>();
+          Raw8<TX> dy = raw_zero<TX>();
+          if (pre) h = ring.copy<TR, VEC>(to, kH, row_at<TR>(p.h_in, row, D), cs);
+          if (p.dh != nullptr) dh = ring.copy<TR, VEC>(to, kDh, row_at<TR>(p.dh, row, p.ld_dh), cs);
+          if (pre && p.dy != nullptr) dy = ring.copy<TX, VEC>(to, kY, row_at<TX>(p.dy, row, p.ld_dy), cs);
           if (gate_full) {
             if (p.gate_res_type)
-              ring.copy<TR, VEC>(to, kG, row_at<TR>(p.gate, row, p.ld_gate), cs);
+              ring.land<TR, VEC>(to, kG, ring.copy<TR, VEC>(to, kG, row_at<TR>(p.gate, row, p.ld_gate), cs));
             else
-              ring.copy<TX, VEC>(to, kG, row_at<TX>(p.gate, row, p.ld_gate), cs);
+              ring.land<TX, VEC>(to, kG, ring.copy<TX, VEC>(to, kG, row_at<TX>(p.gate, row, p.ld_gate), cs));
           }
+          ring.land<TX, VEC>(to, kX, x);
+          ring.land<TR, VEC>(to, kH, h);
+          ring.land<TR, VEC>(to, kDh, dh);
+          ring.land<TX, VEC>(to, kY, dy);
         }
       }
       ahead.row += per;

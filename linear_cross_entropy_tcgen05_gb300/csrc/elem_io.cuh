@@ -184,7 +184,15 @@ template <typename T> __device__ __forceinline__ Raw8<T> pack8(const float2 (&f)
 // threads on neighbouring columns. Columns past the row read as zero and are not written.
 struct Cols {
   int col, step, D;
+  bool kept;  // a kernel with registers to spare keeps the offsets
   __device__ __forceinline__ int at(int i) const { return col + i * step; }
+  // The same columns, to the compiler others: kept from one tensor to the next, their eight
+  // offsets and addresses cost the registers that the sums need.
+  __device__ __forceinline__ Cols afresh() const {
+    Cols c = *this;
+    if (!kept) asm("" : "+r"(c.col), "+r"(c.step));
+    return c;
+  }
 };
 
 template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> load8(const T* row, const Cols& c) {
@@ -192,8 +200,9 @@ template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> load8(const T
     return c.col < c.D ? raw_load(row + c.col) : raw_zero<T>();
   } else {
     float f[8];
+    const Cols d = c.afresh();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c.at(i) < c.D ? to_f32(row[c.at(i)]) : 0.f;
+    for (int i = 0; i < 8; ++i) f[i] = d.at(i) < d.D ? to_f32(row[d.at(i)]) : 0.f;
     return pack8<T>(f);
   }
 }
@@ -203,9 +212,10 @@ template <typename T, bool VEC> __device__ __forceinline__ void store8(T* row, c
     if (c.col < c.D) raw_store(row + c.col, pack8<T>(f));
   } else {
     const float g[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+    const Cols d = c.afresh();
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c.at(i) < c.D) row[c.at(i)] = from_f32<T>(g[i]);
+      if (d.at(i) < d.D) row[d.at(i)] = from_f32<T>(g[i]);
   }
 }
 
