@@ -5,6 +5,7 @@ the formulas."""
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -38,10 +39,10 @@ class FlceBlockNormGrads(ctypes.Structure):
 
 def declare(lib) -> None:
     """Argument types of this module's entry points."""
-    desc, grads, sz, i = ctypes.POINTER(FlceBlockNormDesc), ctypes.POINTER(FlceBlockNormGrads), ctypes.c_size_t, ctypes.c_int
-    lib.flce_block_norm_forward.argtypes, lib.flce_block_norm_forward.restype = [desc, _VP, _VP, _VP, _VP], i
+    sz, i = ctypes.c_size_t, ctypes.c_int  # (the descriptors go as addresses: of a structure, or of packed bytes)
+    lib.flce_block_norm_forward.argtypes, lib.flce_block_norm_forward.restype = [_VP] * 5, i
     lib.flce_block_norm_workspace_size.argtypes, lib.flce_block_norm_workspace_size.restype = [_I64, _I64, _I64], sz
-    lib.flce_block_norm_backward.argtypes = [desc, _VP, _VP, _VP, _I64, _VP, _I64, grads, _VP, sz, _VP]
+    lib.flce_block_norm_backward.argtypes = [_VP, _VP, _VP, _VP, _I64, _VP, _I64, _VP, _VP, sz, _VP]
     lib.flce_block_norm_backward.restype = i
 
 
@@ -109,72 +110,87 @@ def _gate_rows(gate, x) -> int:
     raise ValueError(f"gate {tuple(gate.shape)} does not group the rows of x {tuple(x.shape)}")
 
 
+_PACK = struct.Struct("3q7q3q9i3f")  # flce_block_norm_desc
+_GRADS = struct.Struct("7q")  # flce_block_norm_grads: dx, dresidual, dgate, dpost_weight, dpost_bias, dweight, dbias
+
+
 def _describe(x, residual, weight, bias, post_weight, post_bias, gate, norm, eps, scale, gate_activation,
               weight_offset):
-    """The descriptor of a call and x's rows; raises on what the library cannot take."""
-    if x.dtype not in DTYPES:
+    """A call's flce_block_norm_desc as bytes, its rows, gate rows and the addresses in it; raises
+    on what the library cannot take."""
+    xd, dev = DTYPES.get(x.dtype), x.device
+    if xd is None:
         raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must have at least one column")
-    D, dev = x.shape[-1], x.device
     if dev.type != "cuda":
         raise ValueError("x must be a CUDA tensor")
-    d = FlceBlockNormDesc()
+    D = x.shape[-1]
     rows = _rows(x, D, "x")
-    d.N, d.D, d.x, d.ld_x, d.x_dtype = rows.shape[0], D, x.data_ptr(), _row_stride(rows), DTYPES[x.dtype]
-    d.residual_dtype = d.x_dtype
+    N, px, ld_x = rows.shape[0], x.data_ptr(), _row_stride(rows)
+    pr = pg = ld_r = ld_g = gate_rows = gd = 0
+    rd = xd
     if residual is not None:
         if residual.shape != x.shape or residual.device != dev:
             raise ValueError(f"residual must have x's shape {tuple(x.shape)} and device, got {tuple(residual.shape)}")
         if residual.dtype != x.dtype and residual.dtype != torch.float32:
             raise TypeError(f"residual must have x's type or float32, got {residual.dtype}")
-        r = _rows(residual, D, "residual")
-        d.residual, d.ld_residual, d.residual_dtype = residual.data_ptr(), _row_stride(r), DTYPES[residual.dtype]
+        pr, ld_r, rd = residual.data_ptr(), _row_stride(_rows(residual, D, "residual")), DTYPES[residual.dtype]
     if gate is not None:
         if gate.device != dev:
             raise ValueError("gate must be on x's device")
-        d.gate_rows = _gate_rows(gate, x)
-        if gate.dtype not in DTYPES or DTYPES[gate.dtype] not in (d.x_dtype, d.residual_dtype):
+        gate_rows, gd = _gate_rows(gate, x), DTYPES.get(gate.dtype)
+        if gd != xd and gd != rd:
             raise TypeError(f"gate must have x's or the residual's type, got {gate.dtype}")
-        g = _rows(gate if gate.dim() > 1 else gate.unsqueeze(0), D, "gate")
-        d.gate, d.ld_gate, d.gate_dtype = gate.data_ptr(), _row_stride(g), DTYPES[gate.dtype]
-    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("weight", weight), ("bias", bias)):
-        if t is None:
-            continue
-        if t.shape != (D,) or t.device != dev:
-            raise ValueError(f"{name} must be [{D}] on x's device, got {tuple(t.shape)}")
-        if t.dtype not in DTYPES:
-            raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        setattr(d, name, t.data_ptr())
-        setattr(d, name + "_dtype", DTYPES[t.dtype])
-    if bias is not None and weight is None or post_bias is not None and post_weight is None:
+        pg, ld_g = gate.data_ptr(), _row_stride(_rows(gate if gate.dim() > 1 else gate.unsqueeze(0), D, "gate"))
+    if (bias is not None and weight is None) or (post_bias is not None and post_weight is None):
         raise ValueError("a bias needs its weight")
+    pw, wd = _param("post_weight", post_weight, D, dev)
+    pb, bd = _param("post_bias", post_bias, D, dev)
+    qw, vd = _param("weight", weight, D, dev)
+    qb, cd = _param("bias", bias, D, dev)
     if norm not in NORMS:
         raise ValueError(f"norm must be one of {sorted(NORMS)}")
     if gate_activation not in GATE_ACTIVATIONS:
         raise ValueError(f"gate_activation must be one of {sorted(GATE_ACTIVATIONS)}")
-    d.norm, d.gate_activation = NORMS[norm], GATE_ACTIVATIONS[gate_activation]
-    d.eps, d.scale, d.weight_offset = eps, scale, weight_offset
-    return d
+    words = _PACK.pack(N, D, gate_rows, px, pr, pg, pw, pb, qw, qb, ld_x, ld_r, ld_g, xd, rd, gd, wd, bd, vd, cd,
+                       NORMS[norm], GATE_ACTIVATIONS[gate_activation], eps, scale, weight_offset)
+    return words, N, gate_rows, (px, qw, qb, pw, pb, pg), ld_x
 
 
-def _describes(d, x, weight, bias, post_weight, post_bias, gate) -> bool:
-    """Whether d still holds for these tensors: the ones of the forward, where they were."""
-    for t, p in ((x, d.x), (weight, d.weight), (bias, d.bias), (post_weight, d.post_weight), (post_bias, d.post_bias),
-                 (gate, d.gate)):
+def _param(name: str, t, D: int, dev):
+    """Address and type of a parameter [D], or zeros."""
+    if t is None:
+        return 0, 0
+    if t.dim() != 1 or t.shape[0] != D or t.device != dev:
+        raise ValueError(f"{name} must be [{D}] on x's device, got {tuple(t.shape)}")
+    dt = DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    if D > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), dt
+
+
+def _still(desc, x, weight, bias, post_weight, post_bias, gate) -> bool:
+    """Whether desc holds for these tensors too: the ones of the forward, where they were."""
+    for t, p in zip((x, weight, bias, post_weight, post_bias, gate), desc[3]):
         if t is not None and t.data_ptr() != p:
             return False
-    return x.stride(-2) == d.ld_x if x.dim() > 1 and x.shape[-2] > 1 else False
+    return x.dim() > 1 and x.shape[-2] > 1 and x.stride(-2) == desc[4]
 
 
-def _forward(d, x, h_dtype, want_y: bool, want_stats: bool):
-    h = torch.empty(x.shape, dtype=h_dtype, device=x.device)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_y else None
-    stats = torch.empty((d.N, 4), dtype=torch.float32, device=x.device) if want_stats else None
-    if d.N > 0:
-        _call_on(x.device, "flce_block_norm_forward", load_library().flce_block_norm_forward, ctypes.byref(d), h.data_ptr(),
+def _forward(desc, x, h_dtype, want_y: bool, want_stats: bool):
+    words, N, _, _, _ = desc
+    dev = x.device
+    plain = x.is_contiguous()
+    h = torch.empty_like(x) if plain and h_dtype == x.dtype else torch.empty(x.shape, dtype=h_dtype, device=dev)
+    y = None
+    if want_y:
+        y = torch.empty_like(x) if plain else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    stats = torch.empty((N, 4), dtype=torch.float32, device=dev) if want_stats else None
+    if N > 0:
+        _call_on(dev, "flce_block_norm_forward", load_library().flce_block_norm_forward, words, h.data_ptr(),
                  None if y is None else y.data_ptr(), None if stats is None else stats.data_ptr())
     return h, y, stats
 
@@ -186,11 +202,11 @@ class BlockNormFunction(torch.autograd.Function):
     def forward(ctx, x, residual, weight, bias, post_weight, post_bias, gate, norm, eps, scale, gate_activation,
                 weight_offset):
         opts = (norm, eps, scale, gate_activation, weight_offset)
-        d = _describe(x, residual, weight, bias, post_weight, post_bias, gate, *opts)
-        h, y, stats = _forward(d, x, x.dtype if residual is None else residual.dtype, weight is not None, True)
+        desc = _describe(x, residual, weight, bias, post_weight, post_bias, gate, *opts)
+        h, y, stats = _forward(desc, x, x.dtype if residual is None else residual.dtype, weight is not None, True)
         # the residual's values are not needed again, only its type (h has it)
         ctx.save_for_backward(x, weight, bias, post_weight, post_bias, gate, h, stats)
-        ctx.opts, ctx.desc = opts, d
+        ctx.opts, ctx.desc = opts, desc
         ctx.set_materialize_grads(False)
         return h, y
 
@@ -201,16 +217,17 @@ class BlockNormFunction(torch.autograd.Function):
             return (None,) * 12
         x, weight, bias, post_weight, post_bias, gate, h, stats = ctx.saved_tensors
         want, dev, D = ctx.needs_input_grad, x.device, x.shape[-1]
-        d = ctx.desc
-        if not _describes(d, x, weight, bias, post_weight, post_bias, gate):  # a saved-tensor hook gave other tensors
-            d = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
-        grads, out = FlceBlockNormGrads(), [None] * 12
-        for i, name, t in ((0, "dx", x), (1, "dresidual", h), (2, "dweight", weight), (3, "dbias", bias),
-                           (4, "dpost_weight", post_weight), (5, "dpost_bias", post_bias), (6, "dgate", gate)):
+        desc = ctx.desc
+        if not _still(desc, x, weight, bias, post_weight, post_bias, gate):  # a saved-tensor hook gave other tensors
+            desc = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
+        words, N, gate_rows = desc[:3]
+        out = [None] * 12
+        at = [0] * 7
+        for i, t in enumerate((x, h, weight, bias, post_weight, post_bias, gate)):
             if want[i]:
                 out[i] = torch.empty(t.shape, dtype=t.dtype, device=dev)
-                setattr(grads, name, out[i].data_ptr())
-        if d.N == 0:
+                at[i] = out[i].data_ptr()
+        if N == 0:
             for t in out:
                 if t is not None:
                     t.zero_()
@@ -218,10 +235,11 @@ class BlockNormFunction(torch.autograd.Function):
         dh, ld_dh, _dh = _upstream(dh, D, h.dtype)
         dy, ld_dy, _dy = _upstream(dy, D, x.dtype)
         lib = load_library()
-        need = lib.flce_block_norm_workspace_size(d.N, D, d.gate_rows)
+        need = lib.flce_block_norm_workspace_size(N, D, gate_rows)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _call_on(dev, "flce_block_norm_backward", lib.flce_block_norm_backward, ctypes.byref(d), h.data_ptr(),
-                 stats.data_ptr(), dh, ld_dh, dy, ld_dy, ctypes.byref(grads), ws.data_ptr(), need)
+        _call_on(dev, "flce_block_norm_backward", lib.flce_block_norm_backward, words, h.data_ptr(),
+                 stats.data_ptr(), dh, ld_dh, dy, ld_dy,
+                 _GRADS.pack(at[0], at[1], at[6], at[4], at[5], at[2], at[3]), ws.data_ptr(), need)
         return tuple(out)
 
 
@@ -259,8 +277,8 @@ def block_norm(x, residual=None, weight=None, *, bias=None, post_weight=None, po
     args = (x, residual, weight, bias, post_weight, post_bias, gate)
     if torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in args]):
         return BlockNormFunction.apply(*args, norm, eps, scale, gate_activation, weight_offset)
-    d = _describe(*args, norm, eps, scale, gate_activation, weight_offset)
-    h, y, _ = _forward(d, x, x.dtype if residual is None else residual.dtype, weight is not None, False)
+    desc = _describe(*args, norm, eps, scale, gate_activation, weight_offset)
+    h, y, _ = _forward(desc, x, x.dtype if residual is None else residual.dtype, weight is not None, False)
     return h, y
 
 

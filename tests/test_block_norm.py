@@ -87,6 +87,16 @@ def test_python_gate_rows():
             _gate_rows(gate, x)
 
 
+def test_packed_descriptors():
+    """The packed forms have the layout of the structures."""
+    from linear_cross_entropy_tcgen05_gb300 import norm_ops as ops
+    assert ops._PACK.size == ctypes.sizeof(flce.FlceBlockNormDesc) == 152
+    assert ops._GRADS.size == ctypes.sizeof(flce.FlceBlockNormGrads)
+    values = list(range(1, 23)) + [0.5, 0.25, 0.125]
+    d = flce.FlceBlockNormDesc.from_buffer_copy(ops._PACK.pack(*values))
+    assert [getattr(d, n) for n, _ in d._fields_] == values
+
+
 def test_module_refuses():
     with pytest.raises(ValueError):
         flce.BlockNorm(8, norm="batch")
