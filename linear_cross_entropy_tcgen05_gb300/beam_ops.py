@@ -104,7 +104,8 @@ def beam_select(logits, scores, num: int | None = None, finished=None, pad_token
     if K < 1 or V < 1 or not 1 <= num <= K * V:
         raise ValueError(f"num must be between 1 and the {K * V} candidates, got {num}")
     out = torch.empty((B, num), dtype=torch.float32, device=dev)
-    parents, tokens = torch.empty((2, B, num), dtype=torch.int32, device=dev).unbind(0)
+    parents = torch.empty((B, num), dtype=torch.int32, device=dev)
+    tokens = torch.empty_like(parents)
     if B > 0:
         lib = load_library()
         need = lib.flce_beam_select_workspace_size(B, K, V, num)

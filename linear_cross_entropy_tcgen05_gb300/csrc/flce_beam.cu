@@ -2,15 +2,19 @@
 // the reordering of the states that go with the beams.
 //
 // Selection: s[b, k, v] = score[b, k] + z[b, k, v] - lse_v z[b, k, :], the M best of K V, the
-// lowest flat index first where they are equal. Bound by reading the logits once: a block takes a
-// segment of a row into registers, from which it gets the segment's maximum and sum of
-// exponentials and its M best logits (a row's order is its logits' order); a second kernel
-// joins the segments and beams of a request. The order between beams depends on their lse, so
-// segments are joined and scores compared in 64 bits.
+// lowest flat index first where they are equal. Bound by reading the logits once, so that pass
+// selects nothing: it leaves the maximum and the sum of exponentials of every piece of a row. One
+// block a request then finds from the maxima a threshold that M candidates reach, and looks for
+// them in the few pieces that can have any (from L2). The order between beams depends on their
+// lse, so sums are joined and scores compared in 64 bits. (Selecting in every segment in the first
+// pass took 101 us for 256 rows of 256000 bf16 logits, half of it waiting at barriers.)
 //
 // Reordering: out[.., b K + j, ..] = in[.., b K + parent[b, j], ..] for any number of tensors in
 // one launch. A thread reads the same few bytes of all K beams before it writes any of them, so
 // it works in place, without a second buffer; in place a beam that is its own parent costs nothing.
+// Bound by memory: a cache of 128 beams and 1.07 GB in 191 us, 82% of the DRAM's time (parents that
+// several beams share are read once).
+#include <cfloat>
 #include <cmath>
 
 #include <math_constants.h>
@@ -22,19 +26,20 @@
 namespace flce {
 namespace {
 
-constexpr int kBeamThreads = 256;
+constexpr int kBeamThreads = 256, kJoinThreads = 512;
 constexpr int kMaxBeams = 32, kMaxSelect = 64;
-constexpr int kListCap = 512;  // candidates that are ranked against one another
+constexpr int kListCap = 2048;   // candidates that are ranked against one another
+constexpr int kPiecesCap = 2048;  // pieces that may have some
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Order-preserving bits of a float: larger value, larger bits.
-__device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t b = __float_as_uint(v);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+// 2^x; results below the normal range, beside a largest term of 1, are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-__device__ __forceinline__ float unordered(uint32_t b) {
-  return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
-}
+
+// Order-preserving bits of a score: larger value, larger bits. Zero is below every score.
 __device__ __forceinline__ uint64_t ordered64(double v) {
   const uint64_t b = uint64_t(__double_as_longlong(v == 0.0 ? 0.0 : v));  // -0 and 0 are equal
   return b >> 63 ? ~b : b | (uint64_t(1) << 63);
@@ -43,350 +48,456 @@ __device__ __forceinline__ double unordered64(uint64_t b) {
   return __longlong_as_double(int64_t(b >> 63 ? b & ~(uint64_t(1) << 63) : ~b));
 }
 
-// A candidate inside a row: the logit's ordered bits, then the complement of the token, so that
-// of equal logits the lower token is the larger key. Zero is no candidate.
-__device__ __forceinline__ uint64_t logit_key(float z, uint32_t token) {
-  return (uint64_t(ordered(z == 0.f ? 0.f : z)) << 32) | uint32_t(~token);  // -0 and 0 are equal
-}
-
 struct SelectParams {
   const void* logits;
   int64_t ld_batch, ld_beam;
   const float* scores;
   const uint8_t* finished;
   int B, K, V, M;
-  int segments, pad_token;
-  float2* seg_stat;   // [B K][segments] maximum, sum of exp(z - maximum)
-  uint64_t* seg_best; // [B K][segments][M] keys, descending, 0 past the segment's candidates
+  int pieces;      // of a row
+  int pad_token;
+  float2* stat;    // [B K][pieces] maximum, sum of exp(z - maximum)
   float* out_scores;
   int32_t *out_parents, *out_tokens;
 };
 
-// The `need`-th largest of `n` values (n <= kBeamThreads, all distinct or zero) from the first n
-// threads' values: each counts the larger ones.
-template <typename KEY> __device__ __forceinline__ void rank_among(const KEY* keys, int n, int need, KEY* out) {
-  const int i = int(threadIdx.x);
-  if (i < n) {
-    const KEY mine = keys[i];
-    int above = 0;
-    for (int j = 0; j < n; ++j) above += keys[j] > mine || (keys[j] == mine && j < i) ? 1 : 0;
-    if (above == need - 1) *out = mine;
-  }
-}
-
-// Groups of lanes whose maxima give the threshold: about twice as many as candidates wanted, so
-// that about 1.4 M random values reach it.
-__device__ __forceinline__ int group_lanes(int M) {
-  int lanes = 32;  // 8 warps: 8 groups of 32 lanes ... 256 of one
-  while (lanes > 1 && (kBeamThreads / lanes) < 2 * M) lanes >>= 1;
-  return lanes;
-}
-
-template <typename T, int NV>
-__global__ void __launch_bounds__(kBeamThreads) flce_beam_rows_kernel(const SelectParams p) {
-  __shared__ float s_group[kBeamThreads];
-  __shared__ float s_max[kBeamThreads / 32], s_sum[kBeamThreads / 32];
-  __shared__ float s_least;
-  __shared__ int s_count;
-  __shared__ uint64_t s_list[kListCap];
-  const int row = int(blockIdx.y), seg = int(blockIdx.x), tid = int(threadIdx.x);
-  const int b = row / p.K, k = row - b * p.K;
-  if (p.finished != nullptr && p.finished[row]) return;  // its only candidate needs no logits
-  const T* z = static_cast<const T*>(p.logits) + int64_t(b) * p.ld_batch + int64_t(k) * p.ld_beam;
-  const int mis = int((reinterpret_cast<uintptr_t>(z) & uintptr_t(8 * sizeof(T) - 1)) / sizeof(T));
-  constexpr int kSeg = kBeamThreads * 8 * NV;
-  const int e0 = seg * kSeg - mis + tid * 8;  // of this thread's first vector; the others follow kBeamThreads vectors apart
+// A lane's vectors of a piece: NV of eight logits, 256 apart, from the row's last vector boundary in
+// memory before its first logit; -inf outside the row.
+template <typename T, int NV> struct Piece {
   Raw8<T> raw[NV];
+  int e0;  // the first logit of the lane's first vector
+  __device__ __forceinline__ void load(const T* z, int V, int piece, int lane) {
+    const int mis = int((reinterpret_cast<uintptr_t>(z) & uintptr_t(8 * sizeof(T) - 1)) / sizeof(T));
+    e0 = piece * 256 * NV - mis + lane * 8;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int e = e0 + j * kBeamThreads * 8;
-    if (e >= 0 && e + 8 <= p.V) {
-      raw[j] = raw_load(z + e);
-    } else {
-      float f[8];
+    for (int j = 0; j < NV; ++j) {
+      const int e = e0 + j * 256;
+      if (e >= 0 && e + 8 <= V) {
+        raw[j] = raw_load(z + e);
+      } else {
+        float f[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = e + i >= 0 && e + i < p.V ? to_f32(z[e + i]) : -CUDART_INF_F;
-      raw[j] = pack8<T>(f);
+        for (int i = 0; i < 8; ++i) f[i] = e + i >= 0 && e + i < V ? to_f32(z[e + i]) : -CUDART_INF_F;
+        raw[j] = pack8<T>(f);
+      }
     }
   }
-  if (tid == 0) s_count = 0;
+};
+
+template <typename T> __device__ __forceinline__ const T* row_of(const SelectParams& p, int b, int k) {
+  return static_cast<const T*>(p.logits) + int64_t(b) * p.ld_batch + int64_t(k) * p.ld_beam;
+}
+
+// The pass over the logits: a warp takes a piece of 256 NV of them into registers, and its maximum
+// and sum of exponentials out. Nothing is selected here, so no warp waits for another: bound by
+// memory and, for 16-bit logits, nearly as much by the exponentials (16 a clock and SM). 256 rows of
+// 256000 bf16 logits: 24 us, 5.5 TB/s.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kBeamThreads) flce_beam_rows_kernel(const SelectParams p) {
+  const int row = int(blockIdx.y), piece = int(blockIdx.x) * (kBeamThreads / 32) + int(threadIdx.x) / 32;
+  const int lane = int(threadIdx.x) % 32;
+  if (piece >= p.pieces) return;
+  if (p.finished != nullptr && p.finished[row]) return;  // its only candidate needs no logits
+  const int b = row / p.K;
+  Piece<T, NV> z;
+  z.load(row_of<T>(p, b, row - b * p.K), p.V, piece, lane);
   float m = -CUDART_INF_F;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    float f[8];
-    unpack8(raw[j], f);
+    float2 f[4];
+    unpack8(z.raw[j], f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, f[i]);
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(f[i].x, f[i].y));
   }
-  float sum = 0.f;
-  if (m != -CUDART_INF_F) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float f[8];
-      unpack8(raw[j], f);
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // (x - m) log2 e and not x log2 e - m log2 e: the largest term is 1 exactly. A piece of -inf alone
+  // has the sum 0; a NaN or +inf makes it NaN (fmaxf passes over a NaN, the sum does not).
+  const float base = m == -CUDART_INF_F ? 0.f : m;
+  float2 s2 = both(0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += exp2f((f[i] - m) * kLog2e);
-    }
-  } else {
-    // fmaxf passes over NaN: a thread of NaN and -inf alone would miss it
+  for (int j = 0; j < NV; ++j) {
+    float2 f[4];
+    unpack8(z.raw[j], f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float f[8];
-      unpack8(raw[j], f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum += f[i] != f[i] ? f[i] : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const float2 d = mul2(add2(f[i], both(-base)), both(kLog2e));
+      s2 = add2(s2, make_float2(ex2(d.x), ex2(d.y)));
     }
   }
-  // maximum and sum of the warp, then of the block; group maxima on the way
-  const int lanes = group_lanes(p.M);
-  float wm = m;
-  if (lanes == 1) s_group[tid] = wm;
+  float s = s2.x + s2.y;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-    if (lanes == 2 * o && tid % lanes == 0) s_group[tid / lanes] = wm;
-  }
-  float ws = m == -CUDART_INF_F ? sum : sum * exp2f((m - wm) * kLog2e);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-  if (tid % 32 == 0) {
-    s_max[tid / 32] = wm;
-    s_sum[tid / 32] = ws;
-  }
-  __syncthreads();
-  rank_among(s_group, kBeamThreads / lanes, p.M, &s_least);
-  const int64_t at = int64_t(row) * p.segments + seg;
-  if (tid == kBeamThreads - 1) {
-    float bm = s_max[0], bs = 0.f;
-    for (int w = 1; w < kBeamThreads / 32; ++w) bm = fmaxf(bm, s_max[w]);
-    for (int w = 0; w < kBeamThreads / 32; ++w) bs += s_max[w] == -CUDART_INF_F ? s_sum[w] : s_sum[w] * exp2f((s_max[w] - bm) * kLog2e);
-    p.seg_stat[at] = make_float2(bm, bs);
-  }
-  __syncthreads();
-  const float least = s_least;
-  if (!(m < least)) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float f[8];
-      unpack8(raw[j], f);
-      const int e = e0 + j * kBeamThreads * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (!(f[i] < least) && e + i >= 0 && e + i < p.V) {
-          const int n = atomicAdd(&s_count, 1);  // the order of the list does not matter: it is ranked
-          if (n < kListCap) s_list[n] = logit_key(f[i], uint32_t(e + i));
-        }
-    }
-  }
-  __syncthreads();
-  const int count = s_count;
-  uint64_t* best = p.seg_best + at * p.M;
-  if (count <= kListCap) {
-    for (int i = tid; i < count; i += kBeamThreads) {
-      const uint64_t mine = s_list[i];
-      int above = 0;
-      for (int j = 0; j < count; ++j) above += s_list[j] > mine ? 1 : 0;
-      if (above < p.M) best[above] = mine;
-    }
-    for (int i = count + tid; i < p.M; i += kBeamThreads) best[i] = 0;
-    return;
-  }
-  // many equal or sorted values: the M best one after the other
-  uint64_t below = ~uint64_t(0);
-  for (int n = 0; n < p.M; ++n) {
-    uint64_t mine = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float f[8];
-      unpack8(raw[j], f);
-      const int e = e0 + j * kBeamThreads * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (e + i >= 0 && e + i < p.V) {
-          const uint64_t key = logit_key(f[i], uint32_t(e + i));
-          mine = key < below && key > mine ? key : mine;
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, mine, o);
-      mine = other > mine ? other : mine;
-    }
-    __syncthreads();
-    if (tid % 32 == 0) s_list[tid / 32] = mine;
-    __syncthreads();
-    for (int w = 0; w < kBeamThreads / 32; ++w) mine = s_list[w] > mine ? s_list[w] : mine;
-    if (tid == 0) best[n] = mine;
-    below = mine;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) p.stat[int64_t(row) * p.pieces + piece] = make_float2(m, s);
 }
 
-// A candidate of a request: ordered bits of its score, then the lower flat index.
-struct Candidate {
-  uint64_t score;
-  uint32_t row, token;
-};
-__device__ __forceinline__ bool better(const Candidate& a, const Candidate& b) {
-  return a.score != b.score ? a.score > b.score : a.row != b.row ? a.row < b.row : a.token < b.token;
-}
-__device__ __forceinline__ Candidate no_candidate() { return Candidate{0, ~0u, ~0u}; }
-__device__ __forceinline__ Candidate shuffle_best(Candidate c, int o) {
-  Candidate d;
-  d.score = __shfl_xor_sync(0xffffffffu, c.score, o);
-  d.row = __shfl_xor_sync(0xffffffffu, c.row, o);
-  d.token = __shfl_xor_sync(0xffffffffu, c.token, o);
-  return better(d, c) ? d : c;
-}
+enum BeamState : int { BEAM_LIVE = 0, BEAM_NONE = 1, BEAM_FINISHED = 2 };
 
-constexpr uint64_t kMinusInf = 0x000fffffffffffffull;  // ordered64(-inf)
-
-// One block a request: lse of its beams, then the M best of their segments' best.
-__global__ void __launch_bounds__(kBeamThreads) flce_beam_join_kernel(const SelectParams p) {
-  __shared__ double s_base[kMaxBeams];  // score - lse; NaN: the beam has no candidate
-  __shared__ int s_dead[kMaxBeams];     // 0 live, 1 no candidate, 2 finished
-  __shared__ Candidate s_group[kBeamThreads], s_list[kListCap];
-  __shared__ Candidate s_least;
-  __shared__ int s_count;
+// One block a request. lse of its beams; a threshold that at least M candidates reach, from the
+// maxima of disjoint sets of them (the M-th largest of such maxima does); the candidates that reach
+// it, from the few pieces whose maximum does; and their ranks among one another. The threshold
+// and the test against it are in 32 bits with a margin, the scores and the order in 64. All of it
+// is latency: 8 us for one request of four beams, 20 us for 16 beams of 256000 tokens and 32
+// candidates (512 threads; 33 us with 256). More equal or sorted logits than the list holds take the
+// slower ways at the end (8 rows of 128256 equal logits 0.3 ms, sorted ones 6 ms).
+template <typename T, int NV>
+__global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const SelectParams p) {
+  constexpr int kWarps = kJoinThreads / 32;
+  __shared__ float s_part_max[kMaxBeams];  // at least as many as warps
+  __shared__ double s_part_sum[kMaxBeams];
+  __shared__ double s_base[kMaxBeams];  // score - lse, or a finished beam's score
+  __shared__ float s_base32[kMaxBeams];
+  __shared__ int s_state[kMaxBeams], s_beam[kMaxBeams], s_n_live, s_n_done;
+  __shared__ __align__(16) float s_set[kJoinThreads];
+  __shared__ float s_least;
+  __shared__ double s_border;
+  __shared__ int s_pieces[kPiecesCap];
+  __shared__ int s_n_pieces, s_count;
+  __shared__ __align__(16) uint64_t s_score[kListCap], s_place[kListCap];  // place: beam, then token
   const int b = int(blockIdx.x), tid = int(threadIdx.x), warp = tid / 32, lane = tid % 32;
-  for (int k = warp; k < p.K; k += kBeamThreads / 32) {
-    const int64_t row = int64_t(b) * p.K + k;
-    const float score = p.scores[row];
-    if (p.finished != nullptr && p.finished[row]) {
-      if (lane == 0) {
-        s_base[k] = double(score);
-        s_dead[k] = isfinite(score) ? 2 : 1;
-      }
-      continue;
-    }
-    const float2* st = p.seg_stat + row * p.segments;
+  const float2* stat = p.stat + int64_t(b) * p.K * p.pieces;
+  // a beam's pieces are shared by the warps that there are for it
+  const int per_beam = kWarps > p.K ? kWarps / p.K : 1;
+  for (int u = warp; u < p.K * per_beam; u += kWarps) {
+    const int k = u / per_beam, first = (u - k * per_beam) * 32 + lane;
+    if (p.finished != nullptr && p.finished[int64_t(b) * p.K + k]) continue;
+    const float2* st = stat + k * p.pieces;
     float m = -CUDART_INF_F;
-    for (int s = lane; s < p.segments; s += 32) m = fmaxf(m, st[s].x);
+#pragma unroll 4
+    for (int s = first; s < p.pieces; s += 32 * per_beam) m = fmaxf(m, st[s].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     double sum = 0.0;
-    for (int s = lane; s < p.segments; s += 32) {
+#pragma unroll 4
+    for (int s = first; s < p.pieces; s += 32 * per_beam) {
       const float2 v = st[s];
-      sum += double(v.x == -CUDART_INF_F ? v.y : v.y * expf(v.x - m));
+      sum += double(v.x == -CUDART_INF_F ? v.y : v.y * ex2((v.x - m) * kLog2e));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
-      const double lse = double(m) + log(sum);
-      s_base[k] = double(score) - lse;
-      s_dead[k] = isfinite(score) && isfinite(lse) ? 0 : 1;
+      s_part_max[u] = m;
+      s_part_sum[u] = sum;
     }
   }
-  if (tid == 0) s_count = 0;
   __syncthreads();
-  // candidate j of list l: a live beam's segments have their M best, a beam that is finished
-  // or has none a list of its own (its padding token, then the lowest tokens at -inf)
-  const int lists = p.K * p.segments;
-  auto candidate = [&](int l, int j) {
-    const int k = l / p.segments, s = l - k * p.segments;
-    if (s_dead[k] == 0) {
-      const uint64_t key = p.seg_best[((int64_t(b) * p.K + k) * p.segments + s) * p.M + j];
-      if (key == 0) return no_candidate();
-      const float z = unordered(uint32_t(key >> 32));
-      const double v = z == -CUDART_INF_F ? -CUDART_INF : s_base[k] + double(z);
-      return Candidate{ordered64(v), uint32_t(k), ~uint32_t(key)};
+  if (warp == 0) {
+    int state = BEAM_NONE;
+    if (lane < p.K) {
+      const int k = lane;
+      const int64_t row = int64_t(b) * p.K + k;
+      const float score = p.scores[row];
+      double base = double(score);
+      if (p.finished == nullptr || !p.finished[row]) {
+        float m = -CUDART_INF_F;
+        for (int w = 0; w < per_beam; ++w) m = fmaxf(m, s_part_max[k * per_beam + w]);
+        double sum = 0.0;
+        for (int w = 0; w < per_beam; ++w) {
+          const float x = s_part_max[k * per_beam + w];
+          sum += x == -CUDART_INF_F ? s_part_sum[k * per_beam + w] : s_part_sum[k * per_beam + w] * double(ex2((x - m) * kLog2e));
+        }
+        const double lse = double(m) + log(sum);
+        base -= lse;
+        if (isfinite(score) && isfinite(lse)) state = BEAM_LIVE;
+      } else if (isfinite(score)) {
+        state = BEAM_FINISHED;
+      }
+      s_base[k] = base;
+      s_base32[k] = float(fmin(fmax(base, -double(FLT_MAX)), double(FLT_MAX)));
+      s_state[k] = state;
     }
-    if (s > 0 || j >= p.V) return no_candidate();
-    if (s_dead[k] == 1) return Candidate{kMinusInf, uint32_t(k), uint32_t(j)};
-    if (j == 0) return Candidate{ordered64(s_base[k]), uint32_t(k), uint32_t(p.pad_token)};
-    return Candidate{kMinusInf, uint32_t(k), uint32_t(j - 1 < p.pad_token ? j - 1 : j)};
-  };
-  Candidate mine = no_candidate();
-  for (int l = tid; l < lists; l += kBeamThreads) {
-    const Candidate c = candidate(l, 0);
-    if (better(c, mine)) mine = c;
+    // the live beams, then the finished ones
+    const uint32_t live = __ballot_sync(0xffffffffu, state == BEAM_LIVE), done = __ballot_sync(0xffffffffu, state == BEAM_FINISHED);
+    const uint32_t below = (1u << lane) - 1;
+    if (state == BEAM_LIVE) s_beam[__popc(live & below)] = lane;
+    if (state == BEAM_FINISHED) s_beam[__popc(live) + __popc(done & below)] = lane;
+    if (lane == 0) {
+      s_n_live = __popc(live);
+      s_n_done = __popc(done);
+    }
   }
-  Candidate g = mine;
-  const int lanes = group_lanes(p.M), groups = kBeamThreads / lanes;
-  if (lanes == 1) s_group[tid] = g;
+  if (tid == 0) s_n_pieces = s_count = 0;
+  __syncthreads();
+  // What the maxima are known of: the live beams' pieces, then the finished beams. (Beams without a
+  // candidate are not among them: at a request's first step all but one are.)
+  const int live_pieces = s_n_live * p.pieces, all = live_pieces + s_n_done;
+  auto piece_best = [&](int i) {
+    if (i >= live_pieces) return s_base32[s_beam[s_n_live + i - live_pieces]];
+    const int l = i / p.pieces, k = s_beam[l];
+    return s_base32[k] + stat[k * p.pieces + (i - l * p.pieces)].x;
+  };
+  // Each thread's set: some of these, or where they are few, tokens.
+  float best = -CUDART_INF_F, size = 0.f;
+  const bool by_piece = all >= 4 * p.M;
+  if (by_piece) {
+    for (int i = tid; i < all; i += kJoinThreads) best = fmaxf(best, piece_best(i));
+  } else {
+    if (tid < s_n_done) best = piece_best(live_pieces + tid);
+    for (int l = 0; l < s_n_live; ++l) {
+      const int k = s_beam[l];
+      const T* z = row_of<T>(p, b, k);
+      float m = -CUDART_INF_F;
+      for (int v = tid; v < p.V; v += kJoinThreads) m = fmaxf(m, to_f32(z[v]));
+      best = fmaxf(best, s_base32[k] + m);
+    }
+  }
+  for (int k = lane; k < p.K; k += 32)
+    if (s_state[k] != BEAM_NONE) size = fmaxf(size, fabsf(s_base32[k]));
+  // Sets of neighbouring lanes are joined to about twice as many as candidates wanted: about 1.4 M
+  // random values reach the M-th largest of 2 M maxima.
+  const int values = by_piece ? all : p.V, active = values < kJoinThreads ? values : kJoinThreads;
+  int lanes = 1;
+  while (active / lanes >= 4 * p.M && lanes < 32) lanes *= 2;
+  if (lanes == 1) s_set[tid] = best;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    g = shuffle_best(g, o);
-    if (lanes == 2 * o && tid % lanes == 0) s_group[tid / lanes] = g;
+    best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+    size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, o));
+    if (lanes == 2 * o && tid % lanes == 0) s_set[tid / lanes] = best;
   }
   __syncthreads();
-  if (tid < groups) {
-    const Candidate c = s_group[tid];
+  const int sets = kJoinThreads / lanes;
+  if (tid < sets) {
+    const float mine = s_set[tid];
     int above = 0;
-    for (int j = 0; j < groups; ++j) above += better(s_group[j], c) || (j < tid && !better(c, s_group[j])) ? 1 : 0;
-    if (above == p.M - 1) s_least = c;
+#pragma unroll 4
+    for (int j = 0; j < sets; j += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(s_set + j);
+      above += int(q.x > mine || (q.x == mine && j < tid)) + int(q.y > mine || (q.y == mine && j + 1 < tid)) +
+               int(q.z > mine || (q.z == mine && j + 2 < tid)) + int(q.w > mine || (q.w == mine && j + 3 < tid));
+    }
+    if (above == p.M - 1) {
+      // base, logit and their sum are rounded once each: 4 steps of the largest of them are ample
+      const float v = mine - 16.f * 0x1p-24f * (fabsf(mine) + 2.f * size);
+      s_least = v == v ? v : -CUDART_INF_F;
+    }
   }
   __syncthreads();
-  const Candidate least = s_least;
-  for (int l = tid; l < lists; l += kBeamThreads)
-    for (int j = 0; j < p.M; ++j) {
-      const Candidate c = candidate(l, j);
-      if (c.score == 0 || better(least, c)) break;  // lists descend
-      const int n = atomicAdd(&s_count, 1);
-      if (n < kListCap) s_list[n] = c;
+  const float least = s_least;
+  auto wanted = [&](float v) { return v >= least && v > -CUDART_INF_F; };
+  auto add = [&](double score, int k, int token) {
+    const int n = atomicAdd(&s_count, 1);  // the order of the list does not matter: it is ranked
+    if (n < kListCap) {
+      s_score[n] = ordered64(score);
+      s_place[n] = uint64_t(k) << 32 | uint32_t(token);
+    }
+  };
+  if (tid < p.K && s_state[tid] == BEAM_FINISHED && wanted(s_base32[tid])) add(s_base[tid], tid, p.pad_token);
+  for (int i = tid; i < live_pieces; i += kJoinThreads)
+    if (wanted(piece_best(i))) {
+      const int n = atomicAdd(&s_n_pieces, 1);
+      if (n < kPiecesCap) s_pieces[n] = i;
     }
   __syncthreads();
-  const int count = s_count;
-  auto put = [&](int n, const Candidate& c) {
-    const int64_t o = int64_t(b) * p.M + n;
-    p.out_scores[o] = float(unordered64(c.score));
-    p.out_parents[o] = int32_t(c.row);
-    p.out_tokens[o] = int32_t(c.token);
+  // every candidate of a piece that is wanted, to f(score, beam, token); by one warp
+  auto scan = [&](int i, auto&& f) {
+    const int l = i / p.pieces, k = s_beam[l];
+    const float base32 = s_base32[k];
+    Piece<T, NV> z;
+    z.load(row_of<T>(p, b, k), p.V, i - l * p.pieces, lane);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float v[8];
+      unpack8(z.raw[j], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (wanted(base32 + v[e])) f(s_base[k] + double(v[e]), k, z.e0 + j * 256 + e);
+    }
   };
-  if (count <= kListCap) {
-    for (int i = tid; i < count; i += kBeamThreads) {
-      const Candidate c = s_list[i];
+  const int n_pieces = s_n_pieces;
+  if (n_pieces <= kPiecesCap)
+    for (int i = warp; i < n_pieces; i += kWarps) scan(s_pieces[i], add);
+  __syncthreads();
+  const int count = s_count;
+  const int64_t out = int64_t(b) * p.M;
+  auto put = [&](int n, uint64_t score, uint64_t place) {
+    p.out_scores[out + n] = float(unordered64(score));
+    p.out_parents[out + n] = int32_t(place >> 32);
+    p.out_tokens[out + n] = int32_t(uint32_t(place));
+  };
+  // the best of the list's n candidates, by rank
+  auto rank = [&](int n) {
+    // four threads count those above a candidate, a quarter of the list each
+    const int part = tid % 4, quarter = (n + 3) / 4;
+    for (int i = tid / 4; i < (n + 7) / 8 * 8; i += kJoinThreads / 4) {  // whole warps: they shuffle
+      const uint64_t score = i < n ? s_score[i] : ~uint64_t(0), place = i < n ? s_place[i] : 0;
+      const int end = (part + 1) * quarter < n ? (part + 1) * quarter : n;
       int above = 0;
-      for (int j = 0; j < count; ++j) above += better(s_list[j], c) ? 1 : 0;
-      if (above < p.M) put(above, c);
+#pragma unroll 4
+      for (int j = part * quarter; j < end; ++j)
+        above += int(s_score[j] > score) + int(s_score[j] == score && s_place[j] < place);
+      above += __shfl_xor_sync(0xffffffffu, above, 1);
+      above += __shfl_xor_sync(0xffffffffu, above, 2);
+      if (part == 0 && i < n && above < p.M) put(above, score, place);
+    }
+  };
+  const bool fits = n_pieces <= kPiecesCap && count <= kListCap;
+  int strictly = 0;
+  double border = 0.0;
+  if (fits) {
+    rank(count);
+  } else {
+    // Thousands reach the threshold, most of them equal (a mask of the type's lowest value that
+    // leaves fewer than M tokens, say). With the threshold in 64 bits, those above it first.
+    double top = -CUDART_INF;
+    if (by_piece) {
+      for (int i = tid; i < all; i += kJoinThreads) {
+        const int l = i / p.pieces, k = i < live_pieces ? s_beam[l] : s_beam[s_n_live + i - live_pieces];
+        top = fmax(top, s_base[k] + (i < live_pieces ? double(stat[k * p.pieces + (i - l * p.pieces)].x) : 0.0));
+      }
+    } else {
+      if (tid < s_n_done) top = s_base[s_beam[s_n_live + tid]];
+      for (int l = 0; l < s_n_live; ++l) {
+        const int k = s_beam[l];
+        const T* z = row_of<T>(p, b, k);
+        for (int v = tid; v < p.V; v += kJoinThreads) top = fmax(top, s_base[k] + double(to_f32(z[v])));
+      }
+    }
+    for (int o = 1; o < lanes; o <<= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+    __syncthreads();  // the list is used again
+    double* set64 = reinterpret_cast<double*>(s_score);
+    if (tid % lanes == 0) set64[tid / lanes] = top;
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    if (tid < sets) {
+      const double mine = set64[tid];
+      int above = 0;
+      for (int j = 0; j < sets; ++j) above += int(set64[j] > mine || (set64[j] == mine && j < tid));
+      if (above == p.M - 1) s_border = mine;
+    }
+    __syncthreads();
+    border = s_border;
+    if (tid < p.K && s_state[tid] == BEAM_FINISHED && s_base[tid] > border) add(s_base[tid], tid, p.pad_token);
+    for (int i = warp; i < live_pieces; i += kWarps) {
+      const int l = i / p.pieces, k = s_beam[l];
+      if (s_base[k] + double(stat[k * p.pieces + (i - l * p.pieces)].x) <= border) continue;
+      scan(i, [&](double score, int beam, int token) {
+        if (score > border) add(score, beam, token);
+      });
+    }
+    __syncthreads();
+    strictly = s_count;
+    if (strictly <= kListCap) rank(strictly);
+  }
+  if (!fits && strictly <= kListCap) {
+    // then as many at the threshold as are wanted, lowest index first
+    if (warp != 0) return;
+    int have = strictly;
+    auto take = [&](uint32_t mine, int k, int token) {  // bits of a lane's eight tokens from `token` on
+      int before = __popc(mine), total = before;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, total, o);
+        if (lane >= o) total += v;
+      }
+      int n = have + total - before;
+      for (int e = 0; e < 8; ++e)
+        if (mine >> e & 1) {
+          if (n < p.M) put(n, ordered64(border), uint64_t(k) << 32 | uint32_t(token + e));
+          ++n;
+        }
+      have += __shfl_sync(0xffffffffu, total, 31);
+    };
+    for (int k = 0; k < p.K && have < p.M; ++k) {
+      if (s_state[k] == BEAM_FINISHED) take(lane == 0 && s_base[k] == border ? 1u : 0u, k, p.pad_token);
+      if (s_state[k] != BEAM_LIVE) continue;
+      for (int p0 = 0; p0 < p.pieces && have < p.M; p0 += 32) {
+        const int piece = p0 + lane;
+        const bool has = piece < p.pieces && s_base[k] + double(stat[k * p.pieces + piece].x) >= border;
+        for (uint32_t todo = __ballot_sync(0xffffffffu, has); todo != 0 && have < p.M; todo &= todo - 1) {
+          Piece<T, NV> z;
+          z.load(row_of<T>(p, b, k), p.V, p0 + __ffs(int(todo)) - 1, lane);
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            float v[8];
+            unpack8(z.raw[j], v);
+            uint32_t mine = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (v[e] > -CUDART_INF_F && s_base[k] + double(v[e]) == border) mine |= 1u << e;
+            take(mine, k, z.e0 + j * 256);
+          }
+        }
+      }
     }
     return;
   }
-  Candidate last{~uint64_t(0), 0, 0};
-  for (int n = 0; n < p.M; ++n) {
-    mine = no_candidate();
-    for (int l = tid; l < lists; l += kBeamThreads)
-      for (int j = 0; j < p.M; ++j) {
-        const Candidate c = candidate(l, j);
-        if (c.score == 0) break;
-        if (!better(last, c)) continue;
-        if (better(c, mine)) mine = c;
-        break;
-      }
+  if (!fits) {
+    // Thousands of different ones, all in a few places (sorted logits): the M best one after the other.
+    uint64_t last_score = ~uint64_t(0), last_place = 0;
+    for (int n = 0; n < p.M; ++n) {
+      uint64_t score = 0, place = ~uint64_t(0);
+      auto offer = [&](double v, int k, int token) {
+        const uint64_t s = ordered64(v), at = uint64_t(k) << 32 | uint32_t(token);
+        if (s > last_score || (s == last_score && at <= last_place)) return;
+        if (s > score || (s == score && at < place)) score = s, place = at;
+      };
+      if (tid < p.K && s_state[tid] == BEAM_FINISHED) offer(s_base[tid], tid, p.pad_token);
+      for (int i = warp; i < live_pieces; i += kWarps)
+        if (wanted(piece_best(i))) scan(i, offer);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine = shuffle_best(mine, o);
-    __syncthreads();
-    if (lane == 0) s_group[warp] = mine;
-    __syncthreads();
-    for (int w = 0; w < kBeamThreads / 32; ++w)
-      if (better(s_group[w], mine)) mine = s_group[w];
-    if (tid == 0) put(n, mine);
-    last = mine;
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t s = __shfl_xor_sync(0xffffffffu, score, o), at = __shfl_xor_sync(0xffffffffu, place, o);
+        if (s > score || (s == score && at < place)) score = s, place = at;
+      }
+      __syncthreads();
+      if (lane == 0) {
+        s_score[warp] = score;
+        s_place[warp] = place;
+      }
+      __syncthreads();
+      for (int w = 0; w < kWarps; ++w)
+        if (s_score[w] > score || (s_score[w] == score && s_place[w] < place)) score = s_score[w], place = s_place[w];
+      if (tid == 0) put(n, score, place);
+      last_score = score;
+      last_place = place;
+    }
+  }
+  // What is no candidate fills the rest, lowest index first: all tokens of a beam without any, all but
+  // the padding of a finished one, the masked ones of a live one.
+  if (warp != 0 || !fits || count >= p.M) return;
+  int have = count;
+  for (int k = 0; k < p.K && have < p.M; ++k) {
+    const T* z = row_of<T>(p, b, k);
+    for (int v0 = 0; v0 < p.V && have < p.M; v0 += 32) {
+      const int v = v0 + lane;
+      bool none = v < p.V;
+      if (none && s_state[k] == BEAM_FINISHED) none = v != p.pad_token;
+      if (none && s_state[k] == BEAM_LIVE) none = to_f32(z[v]) == -CUDART_INF_F;
+      const uint32_t who = __ballot_sync(0xffffffffu, none);
+      const int n = have + __popc(who & ((1u << lane) - 1));
+      if (none && n < p.M) put(n, ordered64(-CUDART_INF), uint64_t(k) << 32 | uint32_t(v));
+      have += __popc(who);
+    }
   }
 }
 
-// Vectors of eight logits a thread: the more, the fewer segments to join, as long as there are
-// blocks enough for the device.
+// Vectors of eight logits a lane: the more, the fewer pieces, as long as there are warps enough for
+// the device.
 int pick_vectors(int64_t rows, int64_t V) {
   for (int nv = 4; nv > 1; nv /= 2)
-    if (rows * ((V + kBeamThreads * 8 * nv - 1) / (kBeamThreads * 8 * nv)) >= 152 * 4) return nv;
+    if (rows * ((V + 256 * nv - 1) / (256 * nv)) >= 152 * 32) return nv;
   return 1;
 }
 
-int64_t select_segments(int64_t rows, int64_t V) {
-  const int64_t seg = int64_t(kBeamThreads) * 8 * pick_vectors(rows, V);
-  return (V + 7 + seg - 1) / seg;  // a misaligned row starts up to seven elements into its first vector
+int64_t select_pieces(int64_t rows, int64_t V) {
+  const int64_t piece = 256 * pick_vectors(rows, V);
+  return (V + 7 + piece - 1) / piece;  // a misaligned row starts up to seven logits into its first vector
 }
 
-template <typename T> cudaError_t launch_rows(const SelectParams& p, int nv, cudaStream_t stream) {
-  const dim3 grid(unsigned(p.segments), unsigned(p.B * p.K));
-  if (nv == 4)
-    flce_beam_rows_kernel<T, 4><<<grid, kBeamThreads, 0, stream>>>(p);
-  else if (nv == 2)
-    flce_beam_rows_kernel<T, 2><<<grid, kBeamThreads, 0, stream>>>(p);
-  else
-    flce_beam_rows_kernel<T, 1><<<grid, kBeamThreads, 0, stream>>>(p);
+template <typename T, int NV> cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
+  const dim3 grid(unsigned((p.pieces + kBeamThreads / 32 - 1) / (kBeamThreads / 32)), unsigned(p.B * p.K));
+  flce_beam_rows_kernel<T, NV><<<grid, kBeamThreads, 0, stream>>>(p);
+  count_launch();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  flce_beam_join_kernel<T, NV><<<unsigned(p.B), kJoinThreads, 0, stream>>>(p);
   count_launch();
   return cudaGetLastError();
+}
+
+template <typename T> cudaError_t launch_select_typed(const SelectParams& p, int nv, cudaStream_t stream) {
+  return nv == 4 ? launch_select<T, 4>(p, stream) : nv == 2 ? launch_select<T, 2>(p, stream) : launch_select<T, 1>(p, stream);
 }
 
 // ---------------------------------------------------------------------------------
@@ -532,17 +643,6 @@ flce_status reorder_states(const flce_beam_state* states, int64_t count, const i
   return FLCE_OK;
 }
 
-struct SelectLayout {
-  size_t best, total;
-};
-SelectLayout select_layout(int64_t rows, int64_t V, int64_t M) {
-  SelectLayout l{};
-  const size_t n = size_t(rows) * size_t(select_segments(rows, V));
-  l.best = api_align256(n * sizeof(float2));
-  l.total = l.best + api_align256(n * size_t(M) * sizeof(uint64_t));
-  return l;
-}
-
 bool select_sizes_ok(int64_t B, int64_t K, int64_t V, int64_t M) {
   return B >= 1 && K >= 1 && V >= 1 && M >= 1 && B <= 65535 && K <= kMaxBeams && B * K <= 65535 &&
          V < (int64_t(1) << 30) && M <= kMaxSelect;
@@ -557,7 +657,7 @@ extern "C" {
 
 size_t flce_beam_select_workspace_size(int64_t B, int64_t K, int64_t V, int64_t M) {
   if (!select_sizes_ok(B, K, V, M)) return 0;
-  return select_layout(B * K, V, M).total;
+  return api_align256(size_t(B * K) * size_t(select_pieces(B * K, V)) * sizeof(float2));
 }
 
 flce_status flce_beam_select(const void* logits, int32_t dtype, int64_t B, int64_t K, int64_t V, int64_t ld_batch,
@@ -575,8 +675,7 @@ flce_status flce_beam_select(const void* logits, int32_t dtype, int64_t B, int64
   if (!api_aligned(logits, uintptr_t(elem_bytes(dtype))) || !api_aligned(scores, 4) || !api_aligned(out_scores, 4) ||
       !api_aligned(out_parents, 4) || !api_aligned(out_tokens, 4) || !api_aligned(workspace, 256))
     return FLCE_ERR_ALIGNMENT;
-  const SelectLayout l = select_layout(B * K, V, M);
-  if (ws_bytes < l.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < flce_beam_select_workspace_size(B, K, V, M)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0, dev = -1;
   flce_status st = api_device(&sms, &dev);
   if (st != FLCE_OK) return st;
@@ -595,22 +694,18 @@ flce_status flce_beam_select(const void* logits, int32_t dtype, int64_t B, int64
   p.K = int(K);
   p.V = int(V);
   p.M = int(M);
-  p.segments = int(select_segments(B * K, V));
+  p.pieces = int(select_pieces(B * K, V));
   p.pad_token = pad_token;
-  p.seg_stat = reinterpret_cast<float2*>(workspace);
-  p.seg_best = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + l.best);
+  p.stat = reinterpret_cast<float2*>(workspace);
   p.out_scores = out_scores;
   p.out_parents = out_parents;
   p.out_tokens = out_tokens;
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const int nv = pick_vectors(B * K, V);
-  const cudaError_t e = dtype == FLCE_DTYPE_F32    ? launch_rows<float>(p, nv, stream)
-                        : dtype == FLCE_DTYPE_BF16 ? launch_rows<__nv_bfloat16>(p, nv, stream)
-                                                   : launch_rows<__half>(p, nv, stream);
-  if ((st = api_cuda("beam rows", e)) != FLCE_OK) return st;
-  flce_beam_join_kernel<<<unsigned(B), kBeamThreads, 0, stream>>>(p);
-  count_launch();
-  return api_cuda("beam join", cudaGetLastError());
+  const cudaError_t e = dtype == FLCE_DTYPE_F32    ? launch_select_typed<float>(p, nv, stream)
+                        : dtype == FLCE_DTYPE_BF16 ? launch_select_typed<__nv_bfloat16>(p, nv, stream)
+                                                   : launch_select_typed<__half>(p, nv, stream);
+  return api_cuda("beam select", e);
 }
 
 flce_status flce_beam_reorder(const flce_beam_state* states, int64_t count, const int32_t* parents, int64_t ld_parents,

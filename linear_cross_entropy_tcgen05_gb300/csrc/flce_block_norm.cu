@@ -190,10 +190,10 @@ bool desc_vec(const flce_block_norm_desc* d) {
          rows_vec(d->bias, 8, d->bias_dtype);
 }
 
-// Column sums of the partial sums: 32 columns a block, 16 threads down the rows of each, then
-// one adds the 16. It reads what the backward kernel wrote a moment ago (from L2) and is a
+// Column sums of the partial sums: 32 columns a block, 32 threads down the rows of each, then
+// one adds the 32. It reads what the backward kernel wrote a moment ago (from L2) and is a
 // small part of it.
-constexpr int kSumRows = 16;
+constexpr int kSumRows = 32;
 
 __global__ void __launch_bounds__(32 * kSumRows) flce_block_norm_sums_kernel(const BnSums s) {
   __shared__ float part[kSumRows][33];
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(32 * kSumRows) flce_block_norm_sums_kernel(con
     float v = 0.f;
     if (col < s.D) {
       const float* at = a.part + seg * a.rows * s.D + col;
-#pragma unroll 4
+#pragma unroll 5
       for (int64_t r = ty; r < a.rows; r += kSumRows) v += at[r * s.D];
     }
     part[ty][lane] = v;

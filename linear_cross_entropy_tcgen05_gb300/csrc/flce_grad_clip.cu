@@ -71,11 +71,11 @@ template <typename T> __device__ __forceinline__ Raw8<T> clip_load(const T* g, i
   return pack8<T>(f);
 }
 
-// A thread's vectors of a chunk, kClipBatch of them in flight at a time. Those of a chunk that
-// lies within its tensor need no checks. STREAM: they leave L2 first.
-constexpr int kClipBatch = 4;
+// A thread's vectors of a chunk, a batch of them (128 bytes) in flight at a time. Those of a chunk
+// that lies within its tensor need no checks. STREAM: they leave L2 first.
 template <typename T, bool STREAM, typename F>
 __device__ __forceinline__ void each_vector(const T* g, int64_t n, int64_t e0, int elems, F&& f) {
+  constexpr int kClipBatch = 16 / sizeof(T);
   const bool inner = e0 >= 0 && e0 + elems <= n && elems % (8 * kClipThreads * kClipBatch) == 0;
   if (inner) {
     const T* at = g + e0 + threadIdx.x * 8;

@@ -75,6 +75,35 @@ def test_first_step_and_dead_beams(gpu_lib):
         assert bool((got[0][b] == -math.inf).all()) and got[2][b].tolist() == list(range(8)) and not got[1][b].any()
 
 
+@pytest.mark.parametrize("B,K,V,M", [(2, 4, 128256, 8), (3, 16, 50257, 32), (1, 8, 5000, 64)])
+def test_first_step_of_long_rows(gpu_lib, B, K, V, M):
+    z, s = make(B, K, V, "bf16", seed=3)
+    s[:, 1:] = -math.inf
+    check(z, s, M)
+    s[:, 0], s[:, K - 1] = -math.inf, -3.0
+    check(z, s, M)
+
+
+def test_few_tokens_left_in_long_rows(gpu_lib):
+    """Constrained decoding: a few tokens, or one run of them, and many rows of equal values."""
+    z, s = make(2, 4, 60000, "bf16")
+    keep = z.clone()
+    z.fill_(-math.inf)
+    for v in (5, 777, 30001, 59999):
+        z[:, :, v] = keep[:, :, v]
+    check(z, s, 8)
+    check(z, s, 40)
+    z[:, :, 1000:6000] = keep[:, :, 1000:6000]
+    check(z, s, 16)
+    z[:, :, 1000:6000] = 2.5
+    check(z, s, 16)
+    z.fill_(torch.finfo(z.dtype).min)  # masked with the lowest value: thousands of equal scores far below
+    for v in (5, 59999):
+        z[:, :, v] = keep[:, :, v]
+    check(z, s, 8)
+    check(z, s, 24)
+
+
 @pytest.mark.parametrize("dtype", list(T))
 def test_masked_tokens(gpu_lib, dtype):
     """Rows with few, one and no tokens left, with -inf and with the type's lowest value."""
