@@ -116,8 +116,8 @@ _GRADS = struct.Struct("7q")  # flce_block_norm_grads: dx, dresidual, dgate, dpo
 
 def _describe(x, residual, weight, bias, post_weight, post_bias, gate, norm, eps, scale, gate_activation,
               weight_offset):
-    """A call's flce_block_norm_desc as bytes, its rows, gate rows and the addresses in it; raises
-    on what the library cannot take."""
+    """A call's flce_block_norm_desc as bytes, its rows and gate rows; raises on what the library
+    cannot take."""
     xd, dev = DTYPES.get(x.dtype), x.device
     if xd is None:
         raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
@@ -155,7 +155,7 @@ def _describe(x, residual, weight, bias, post_weight, post_bias, gate, norm, eps
         raise ValueError(f"gate_activation must be one of {sorted(GATE_ACTIVATIONS)}")
     words = _PACK.pack(N, D, gate_rows, px, pr, pg, pw, pb, qw, qb, ld_x, ld_r, ld_g, xd, rd, gd, wd, bd, vd, cd,
                        NORMS[norm], GATE_ACTIVATIONS[gate_activation], eps, scale, weight_offset)
-    return words, N, gate_rows, (px, qw, qb, pw, pb, pg), ld_x
+    return words, N, gate_rows
 
 
 def _param(name: str, t, D: int, dev):
@@ -172,16 +172,8 @@ def _param(name: str, t, D: int, dev):
     return t.data_ptr(), dt
 
 
-def _still(desc, x, weight, bias, post_weight, post_bias, gate) -> bool:
-    """Whether desc holds for these tensors too: the ones of the forward, where they were."""
-    for t, p in zip((x, weight, bias, post_weight, post_bias, gate), desc[3]):
-        if t is not None and t.data_ptr() != p:
-            return False
-    return x.dim() > 1 and x.shape[-2] > 1 and x.stride(-2) == desc[4]
-
-
 def _forward(desc, x, h_dtype, want_y: bool, want_stats: bool):
-    words, N, _, _, _ = desc
+    words, N, _ = desc
     dev = x.device
     plain = x.is_contiguous()
     h = torch.empty_like(x) if plain and h_dtype == x.dtype else torch.empty(x.shape, dtype=h_dtype, device=dev)
@@ -206,7 +198,7 @@ class BlockNormFunction(torch.autograd.Function):
         h, y, stats = _forward(desc, x, x.dtype if residual is None else residual.dtype, weight is not None, True)
         # the residual's values are not needed again, only its type (h has it)
         ctx.save_for_backward(x, weight, bias, post_weight, post_bias, gate, h, stats)
-        ctx.opts, ctx.desc = opts, desc
+        ctx.opts = opts
         ctx.set_materialize_grads(False)
         return h, y
 
@@ -217,10 +209,9 @@ class BlockNormFunction(torch.autograd.Function):
             return (None,) * 12
         x, weight, bias, post_weight, post_bias, gate, h, stats = ctx.saved_tensors
         want, dev, D = ctx.needs_input_grad, x.device, x.shape[-1]
-        desc = ctx.desc
-        if not _still(desc, x, weight, bias, post_weight, post_bias, gate):  # a saved-tensor hook gave other tensors
-            desc = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
-        words, N, gate_rows = desc[:3]
+        # described anew: the residual may be gone (h stands in for its type), and a saved-tensor hook
+        # may have brought the others back elsewhere or with other strides
+        words, N, gate_rows = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
         out = [None] * 12
         at = [0] * 7
         for i, t in enumerate((x, h, weight, bias, post_weight, post_bias, gate)):

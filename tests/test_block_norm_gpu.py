@@ -272,6 +272,41 @@ def test_on_another_stream_and_in_a_graph(gpu_lib):
     assert torch.equal(dx, want[3]["x"]) and torch.equal(dw, want[3]["weight"])
 
 
+def test_residual_freed_before_the_backward(gpu_lib):
+    """The backward pass needs no residual: its memory may be back with the driver by then."""
+    case = (4096, 1024, "bf16", "f32", "rms", False, 0, "none", False)
+    t, dh, dy = make(case)
+    want = run(case, t, dh, dy)
+    x, w = (t[k].clone().requires_grad_() for k in ("x", "weight"))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    residual = t.pop("residual").clone()  # 16 MB: a segment of its own
+    h, y = flce.block_norm(x, residual, w, **options(case))
+    del residual
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    got = torch.autograd.grad([h, y], [x, w], [dh, dy])
+    assert torch.equal(got[0], want[3]["x"]) and torch.equal(got[1], want[3]["weight"])
+
+
+def test_saved_tensors_brought_back_elsewhere(gpu_lib):
+    """Saved-tensor hooks that give back contiguous copies of strided inputs."""
+    case = (6, 512, "bf16", "f32", "layer", True, 3, "tanh", True)
+    t, dh, dy = make(case)
+    want = run(case, t, dh, dy)
+    wide = {k: torch.zeros(v.shape[0], 2 * v.shape[1], dtype=v.dtype, device=DEV)[:, :v.shape[1]].copy_(v)
+            for k, v in t.items() if k in ("x", "gate")}
+    t.update(wide)
+    l = leaves(t)
+    for v in l.values():
+        v.requires_grad_()
+    with torch.autograd.graph.saved_tensors_hooks(lambda s: s.detach().cpu(), lambda s: s.to(DEV).contiguous()):
+        h, y = flce.block_norm(**t, **options(case))
+    got = torch.autograd.grad([h, y], list(l.values()), [dh, dy])
+    for (k, g) in zip(l, got):
+        assert torch.equal(g, want[3][k]), k
+
+
 def test_refuses_host_memory_and_mixed_types(gpu_lib):
     x = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
     w = torch.ones(64, device=DEV)
