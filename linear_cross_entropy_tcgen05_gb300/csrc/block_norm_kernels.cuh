@@ -31,13 +31,14 @@ namespace {
 // Slots whose tensor or columns are not there are zeroed once and never copied to.
 struct RowRing {
   uint32_t first, end;       // this thread's first plane of the ring's first batch, and past its last
-  int plane, row_bytes;      // bytes of a plane (16 a thread) and of a row's planes
+  int plane;                 // bytes of a plane (16 a thread)
+  int row_bytes;             // from a batch's row to its next; 0 where it has one, which is read in the next one's place
   uint32_t batch_bytes;
 
   __device__ __forceinline__ void init(char* smem, int planes, int batches, int rows) {
     plane = 16 * int(blockDim.x);
-    row_bytes = planes * plane;
-    batch_bytes = uint32_t(rows * row_bytes);
+    row_bytes = rows > 1 ? planes * plane : 0;
+    batch_bytes = uint32_t(rows * planes * plane);
     first = smem_addr(smem) + 16u * threadIdx.x;
     end = first + uint32_t(batches) * batch_bytes;
     for (uint32_t at = first; at < end; at += uint32_t(plane))

@@ -106,6 +106,12 @@ def test_against_the_formulas(gpu_lib, case):
     assert all(torch.equal(again[k], v) for k, v in grads.items())
 
 
+def test_batches_of_one_row(gpu_lib):
+    """Rows so wide that two do not fit a batch, several for each block."""
+    test_against_the_formulas(gpu_lib, (700, 4096, "f32", "f32", "layer", True, -1, "tanh", True))
+    test_against_the_formulas(gpu_lib, (200, 16384, "bf16", "f32", "layer", True, 8, "sigmoid", True))
+
+
 def test_without_a_weight(gpu_lib):
     case = (50, 384, "bf16", "f32", "rms", True, 1, "tanh", False)
     t, dh, _ = make(case)
