@@ -8,11 +8,11 @@
 
 namespace flce {
 
-// A row is worked on by bn_threads(D) threads of eight columns each: at most 512 a block,
-// beyond that the blocks of a cluster (up to 8) share the row.
-constexpr int kBnMaxThreads = 512;
+// A row is worked on by threads of eight columns each, all in one block where they fit, beyond
+// that the blocks of a cluster (up to 8) share the row.
+constexpr int kBnMaxThreads = 640;
 constexpr int kBnMaxCluster = 8;
-constexpr int kBnSmemBytes = 212 << 10;  // shared memory for parameters and rows on their way in
+constexpr int kBnSmemBytes = 220 << 10;  // shared memory for parameters and rows on their way in
 constexpr int64_t kBnMaxD = 16384;
 
 struct BlockNormShape {
@@ -48,9 +48,16 @@ struct BlockNormParams {
 };
 
 // What the code of a kernel has: the norm after the block, a gate (for groups of rows, or GATE_ROWS:
-// for each row), and (FULL) the means
-// of layer norms and biases. A kernel takes what has less at run time.
-enum BnFeature : int { BN_POST = 1, BN_GATE = 2, BN_FULL = 4, BN_GATE_ROWS = 8 };
+// for each row), and (FULL) the means of layer norms and biases. A kernel takes what has less at
+// run time. WIDE: blocks of up to 640 threads.
+enum BnFeature : int { BN_POST = 1, BN_GATE = 2, BN_FULL = 4, BN_GATE_ROWS = 8, BN_WIDE = 16 };
+// Threads of a block at most. 640 leave 96 registers for each: enough for the forward kernels
+// of aligned rows in one block (the others would spill), but those with FULL are slower for it
+// (N = 32768, D = 2048 bf16, layer norms, 16 gates: 147 us against 126), so they come in both.
+constexpr int kBnThreads = 512;
+__host__ __device__ constexpr int bn_max_threads(int feat, bool vec, bool clusters) {
+  return vec && !clusters && (!(feat & BN_FULL) || (feat & BN_WIDE)) ? kBnMaxThreads : kBnThreads;
+}
 // Parameters that a kernel keeps in shared memory (the others have room for theirs in registers).
 __host__ __device__ constexpr int bn_shared_params(int feat, bool backward) {
   if (!(feat & BN_FULL)) return 0;
@@ -92,9 +99,11 @@ constexpr BnRing bn_ring(const BlockNormShape& s, int planes, int feat, bool bac
 }
 
 // The features of the kernel that a call with these takes: unaligned rows, and rows shared by
-// clusters unless they have RMS norms alone, take the kernel that has everything.
-constexpr int bn_kernel_features(int feat, bool vec, int cluster) {
+// clusters unless they have RMS norms alone, take the kernel that has everything, and so do wide
+// blocks of the FULL ones.
+constexpr int bn_kernel_features(int feat, bool vec, int cluster, bool wide) {
   const int all = feat & BN_GATE_ROWS ? BN_POST | BN_GATE | BN_FULL | BN_GATE_ROWS : BN_POST | BN_GATE | BN_FULL;
+  if (wide && (feat & BN_FULL)) return all | BN_WIDE;
   return !vec || (cluster > 1 && (feat & (BN_GATE | BN_FULL))) ? all : feat;
 }
 

@@ -9,7 +9,7 @@ cudaError_t bn_backward_f32_f32(const BlockNormParams& p, const BlockNormShape& 
   using TR = float;
   constexpr bool BACKWARD = true;
 #define KERNEL flce_block_norm_backward_kernel
-  FLCE_BN_DISPATCH;
+  FLCE_BN_DISPATCH();
 }
 
 }  // namespace flce

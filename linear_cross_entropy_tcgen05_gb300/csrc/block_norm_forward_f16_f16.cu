@@ -9,7 +9,7 @@ cudaError_t bn_forward_f16_f16(const BlockNormParams& p, const BlockNormShape& s
   using TR = __half;
   constexpr bool BACKWARD = false;
 #define KERNEL flce_block_norm_forward_kernel
-  FLCE_BN_DISPATCH;
+  FLCE_BN_DISPATCH(FLCE_BN_WIDE_CASES);
 }
 
 }  // namespace flce

@@ -9,7 +9,7 @@ cudaError_t bn_forward_f32_f32(const BlockNormParams& p, const BlockNormShape& s
   using TR = float;
   constexpr bool BACKWARD = false;
 #define KERNEL flce_block_norm_forward_kernel
-  FLCE_BN_DISPATCH;
+  FLCE_BN_DISPATCH(FLCE_BN_WIDE_CASES);
 }
 
 }  // namespace flce

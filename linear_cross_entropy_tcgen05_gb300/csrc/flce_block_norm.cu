@@ -16,6 +16,8 @@ namespace {
 // size is a function of the sizes alone.
 constexpr int kSms = 152;
 
+constexpr int kBnFewThreads = 256;
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 BlockNormShape bn_shape(int64_t D, int max_threads) {
@@ -35,13 +37,32 @@ int64_t bn_resident(const BlockNormShape& s) {
   return s.cluster == 1 ? kSms : s.cluster == 2 ? kSms / 2 : s.cluster == 4 ? 36 : 15;
 }
 
-// Threads of a block for these tensors: half as many where the rows of the widest would leave no
-// room for two batches of them (fp32
-// rows of 4096 columns with a gate for each), so that clusters share them.
-int bn_threads(const flce_block_norm_desc* d, bool vec, int feat, bool backward) {
+// How a call's rows are shared out, and the features of its kernel. Wide blocks are taken by rows
+// that 512 threads would share in clusters, and by FULL kernels where they have room for more
+// rows, if there are rows for more (N = 32768, D = 5120 bf16: 230 us against 297 in clusters; N =
+// 16384, D = 2304, layer norms: 106 us against 122; but N = 48, D = 5120: 12.5 us against 11.3; and
+// RMS norms at N = 32768, D = 2560: 126 us against 117). Blocks have half as many threads where
+// rows of 512 would leave no room for two batches of them (fp32 rows of 4096 columns with a
+// gate for each), so that clusters share them.
+struct BnKernel {
+  BlockNormShape shape;
+  int max_threads, feat;
+};
+BnKernel bn_pick(const flce_block_norm_desc* d, bool vec, int feat, bool backward) {
   const int planes = bn_planes(elem_bytes(d->x_dtype), elem_bytes(d->residual_dtype), d->gate && d->gate_rows == d->N, backward);
-  const BlockNormShape s = bn_shape(d->D, kBnMaxThreads);
-  return bn_ring(s, planes, bn_kernel_features(feat, vec, s.cluster), backward).batches >= 2 ? kBnMaxThreads : kBnMaxThreads / 2;
+  auto fits = [&](const BlockNormShape& s, int f) { return bn_ring(s, planes, f, backward).batches >= 2; };
+  const BlockNormShape s = bn_shape(d->D, kBnThreads);
+  if (!backward && vec) {
+    const BlockNormShape w = bn_shape(d->D, kBnMaxThreads);
+    const int f = bn_kernel_features(feat, vec, 1, true);
+    if (w.cluster == 1 && (s.cluster > 1 || ((feat & BN_FULL) && w.rows_per_block > s.rows_per_block)) &&
+        d->N > bn_resident(s) * s.rows_per_block && fits(w, f))
+      return BnKernel{w, kBnMaxThreads, f};
+  }
+  const int f = bn_kernel_features(feat, vec, s.cluster, false);
+  if (fits(s, f)) return BnKernel{s, kBnThreads, f};
+  const BlockNormShape few = bn_shape(d->D, kBnFewThreads);
+  return BnKernel{few, kBnFewThreads, bn_kernel_features(feat, vec, few.cluster, false)};
 }
 
 struct BwdPlan {
@@ -191,8 +212,9 @@ bool desc_vec(const flce_block_norm_desc* d) {
 }
 
 // Column sums of the partial sums: 32 columns a block, 32 threads down the rows of each, then
-// one adds the 32. It reads what the backward kernel wrote a moment ago (from L2) and is a
-// small part of it.
+// one adds the 32. It reads what the backward kernel wrote a moment ago (from L2) and is bound by
+// the latency of a column's loads: 7 us for 152 partial sums of two parameters, D = 4096, 11 us
+// with biases and gates, of a backward pass of 130 and 180 us.
 constexpr int kSumRows = 32;
 
 __global__ void __launch_bounds__(32 * kSumRows) flce_block_norm_sums_kernel(const BnSums s) {
@@ -240,7 +262,8 @@ extern "C" {
 size_t flce_block_norm_workspace_size(int64_t N, int64_t D, int64_t gate_rows) {
   if (N < 1 || D < 1 || N >= (int64_t(1) << 30) || D > kBnMaxD || gate_rows < 0 || gate_rows > N) return 0;
   if (gate_rows > 0 && N % gate_rows != 0) return 0;
-  const size_t a = bwd_plan(N, D, gate_rows, kBnMaxThreads).total, b = bwd_plan(N, D, gate_rows, kBnMaxThreads / 2).total;
+  const size_t a = bwd_plan(N, D, gate_rows, kBnThreads).total;
+  const size_t b = bwd_plan(N, D, gate_rows, kBnFewThreads).total;
   return a > b ? a : b;
 }
 
@@ -263,8 +286,8 @@ flce_status flce_block_norm_forward(const flce_block_norm_desc* d, void* h, void
   p.y = y;
   p.stats = stats;
   const bool vec = desc_vec(d) && rows_vec(h, d->D, d->residual_dtype) && rows_vec(y, d->D, d->x_dtype);
-  const int feat = bn_features(d);
-  const BlockNormShape s = bn_shape(d->D, bn_threads(d, vec, feat, false));
+  const BnKernel k = bn_pick(d, vec, bn_features(d), false);
+  const BlockNormShape& s = k.shape;
   const int64_t need = cdiv(d->N, s.rows_per_block), resident = bn_resident(s);
   int64_t blocks = need < resident ? need : resident;
   p.chunk_rows = cdiv(d->N, blocks * s.rows_per_block);
@@ -273,7 +296,7 @@ flce_status flce_block_norm_forward(const flce_block_norm_desc* d, void* h, void
   const auto fn = d->x_dtype == FLCE_DTYPE_BF16  ? (f32 ? bn_forward_bf16_f32 : bn_forward_bf16_bf16)
                   : d->x_dtype == FLCE_DTYPE_F16 ? (f32 ? bn_forward_f16_f32 : bn_forward_f16_f16)
                                                  : bn_forward_f32_f32;
-  return api_cuda("block norm forward", fn(p, s, vec, bn_kernel_features(feat, vec, s.cluster), unsigned(blocks), reinterpret_cast<cudaStream_t>(stream)));
+  return api_cuda("block norm forward", fn(p, s, vec, k.feat, unsigned(blocks), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* h, const float* stats, const void* dh,
@@ -311,8 +334,8 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* 
   const bool vec = desc_vec(d) && rows_vec(h, d->D, d->residual_dtype) && rows_vec(dh, ld_dh, d->residual_dtype) &&
                    rows_vec(dy, ld_dy, d->x_dtype) && rows_vec(g->dx, d->D, d->x_dtype) &&
                    rows_vec(g->dresidual, d->D, d->residual_dtype) && rows_vec(g->dgate, d->D, d->gate_dtype);
-  const int feat = bn_features(d);
-  const BwdPlan plan = bwd_plan(d->N, d->D, d->gate_rows, bn_threads(d, vec, feat, true));
+  const BnKernel k = bn_pick(d, vec, bn_features(d), true);
+  const BwdPlan plan = bwd_plan(d->N, d->D, d->gate_rows, k.max_threads);
   char* ws = static_cast<char*>(workspace);
   BlockNormParams p = bn_params(d);
   p.stats = const_cast<float*>(stats);
@@ -343,8 +366,8 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* d, const void* 
   const auto fn = d->x_dtype == FLCE_DTYPE_BF16  ? (f32 ? bn_backward_bf16_f32 : bn_backward_bf16_bf16)
                   : d->x_dtype == FLCE_DTYPE_F16 ? (f32 ? bn_backward_f16_f32 : bn_backward_f16_f16)
                                                  : bn_backward_f32_f32;
-  if ((st = api_cuda("block norm backward", fn(p, plan.shape, vec, bn_kernel_features(feat, vec, plan.shape.cluster),
-                                                   unsigned(plan.blocks), stream))) != FLCE_OK) return st;
+  st = api_cuda("block norm backward", fn(p, plan.shape, vec, k.feat, unsigned(plan.blocks), stream));
+  if (st != FLCE_OK) return st;
   return api_cuda("block norm sums", bn_column_sums(sums, stream));
 }
 

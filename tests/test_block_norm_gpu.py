@@ -112,6 +112,22 @@ def test_batches_of_one_row(gpu_lib):
     test_against_the_formulas(gpu_lib, (200, 16384, "bf16", "f32", "layer", True, 8, "sigmoid", True))
 
 
+WIDE = [  # rows enough for blocks of up to 640 threads, forward
+    (700, 5120, "bf16", "bf16", "rms", True, 0, "none", False),
+    (200, 4104, "f32", "f32", "rms", False, 0, "none", False),
+    (400, 4608, "f16", "f32", "layer", True, -1, "tanh", True),
+    (320, 4616, "bf16", "bf16", "layer", True, 4, "sigmoid", True),
+    (301, 2408, "f32", "f32", "layer", False, -1, "sigmoid", False),
+    (1300, 1520, "bf16", "f32", "layer", True, 13, "tanh", True),
+    (3001, 264, "f16", "f16", "layer", True, 0, "none", False),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: "-".join(map(str, c)))
+def test_wide_blocks(gpu_lib, case):
+    test_against_the_formulas(gpu_lib, case)
+
+
 def test_without_a_weight(gpu_lib):
     case = (50, 384, "bf16", "f32", "rms", True, 1, "tanh", False)
     t, dh, _ = make(case)
