@@ -99,6 +99,7 @@ def beam_select(logits, scores, num: int | None = None, finished=None, pad_token
         if finished.shape != scores.shape:
             raise ValueError("finished must have the scores' shape")
         finished = finished.contiguous()
+    scores = scores.contiguous()
     B, K, V = logits.shape
     num = K if num is None else int(num)
     if K < 1 or V < 1 or not 1 <= num <= K * V:
@@ -111,8 +112,7 @@ def beam_select(logits, scores, num: int | None = None, finished=None, pad_token
         need = lib.flce_beam_select_workspace_size(B, K, V, num)
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
         _call_on(dev, "flce_beam_select", lib.flce_beam_select,
-                 *_select_args(logits, scores if scores.is_contiguous() else scores.contiguous(), finished, pad_token, num,
-                               out, parents, tokens, ws, need))
+                 *_select_args(logits, scores, finished, pad_token, num, out, parents, tokens, ws, need))
     return out, parents, tokens
 
 

@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
     }
   }
   // What is no candidate fills the rest, lowest index first: all tokens of a beam without any, all but
-  // the padding of a finished one, the masked ones of a live one.
+  // the padding of a finished one, the masked ones of a live one (with scores of -inf, or, under
+  // two masks of the type's lowest value, of less than fp32 has).
   if (warp != 0 || !fits || count >= p.M) return;
   int have = count;
   for (int k = 0; k < p.K && have < p.M; ++k) {
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
       const int v = v0 + lane;
       bool none = v < p.V;
       if (none && s_state[k] == BEAM_FINISHED) none = v != p.pad_token;
-      if (none && s_state[k] == BEAM_LIVE) none = to_f32(z[v]) == -CUDART_INF_F;
+      if (none && s_state[k] == BEAM_LIVE) none = !(s_base32[k] + to_f32(z[v]) > -CUDART_INF_F);
       const uint32_t who = __ballot_sync(0xffffffffu, none);
       const int n = have + __popc(who & ((1u << lane) - 1));
       if (none && n < p.M) put(n, ordered64(-CUDART_INF), uint64_t(k) << 32 | uint32_t(v));

@@ -123,6 +123,18 @@ def test_masked_tokens(gpu_lib, dtype):
     check(z, s, 64)
 
 
+def test_scores_below_the_range_still_fill(gpu_lib):
+    """Masks of the lowest value on tokens and on a beam: sums that fp32 does not have come last."""
+    low = torch.finfo(torch.float32).min
+    z = torch.full((1, 2, 3), low, device=DEV)
+    z[..., 0] = 0.0
+    s = torch.tensor([[0.0, low]], device=DEV)
+    scores, parents, tokens = (v[0].tolist() for v in flce.beam_select(z, s, 6))
+    # beam 0: 0 and twice low; beam 1: low, equal to those and after them, and twice 2 low
+    assert list(zip(parents, tokens)) == [(0, 0), (0, 1), (0, 2), (1, 0), (1, 1), (1, 2)]
+    assert scores == [0.0, low, low, low, -math.inf, -math.inf]
+
+
 def test_bad_logits(gpu_lib):
     """A NaN or an infinity in a row takes the row out, wherever it stands."""
     for bad in (math.nan, math.inf):
