@@ -88,10 +88,13 @@ constexpr int bn_planes(int x_bytes, int residual_bytes, bool gate_full, bool ba
 struct BnRing {
   int per, batches, params_bytes;
 };
-constexpr BnRing bn_ring(const BlockNormShape& s, int planes, int feat, bool backward) {
+// Bytes of a row of a ring. Unaligned rows have 16 bytes more for each warp's plane.
+constexpr int kBnWarpPlane = 33 * 16;
+constexpr int bn_row_bytes(int threads, int planes, bool vec) { return planes * (vec ? 16 * threads : threads / 32 * kBnWarpPlane); }
+constexpr BnRing bn_ring(const BlockNormShape& s, int planes, bool vec, int feat, bool backward) {
   const int threads = s.threads_per_row * s.rows_per_block;
   BnRing r{kBnRows, 1, bn_shared_params(feat, backward) * 32 * s.threads_per_row + bn_own_params(feat, backward) * 32 * threads};
-  const int room = kBnSmemBytes - r.params_bytes, row = planes * 16 * threads;
+  const int room = kBnSmemBytes - r.params_bytes, row = bn_row_bytes(threads, planes, vec);
   if (room / (row * r.per) < 2) r.per = 1;
   r.batches = room / (row * r.per);
   if (r.batches > kBnMaxBatches) r.batches = kBnMaxBatches;

@@ -14,8 +14,8 @@
 // Measured (of 6.8 TB/s that a copy reaches): N = 65536, D = 4096 bf16, two RMS norms, forward 355 us (6.0
 // TB/s), backward 485 us (6.6). N = 16384, D = 2304 bf16 with an fp32 residual, layer norms, 16 gate
 // rows: 106 us (4.3), 198 us (3.4): latency and instructions, not memory. Rows shared by
-// clusters, D = 16384: 394 us, 590 us (16384 rows, 5.5). Unaligned rows, D = 4095: bf16 1.6 TB/s (no
-// asynchronous copies of two bytes), fp32 3.1 to 3.6.
+// clusters, D = 16384: 394 us, 590 us (16384 rows, 5.5). Unaligned rows, D = 4095: bf16 2.6 and 2.2
+// TB/s, fp32 4.0 and 3.0 (bound by instructions: 600 and 1000 for a warp's 256 columns).
 #pragma once
 
 #include <math_constants.h>
@@ -31,54 +31,105 @@
 namespace flce {
 namespace {
 
-// Rows are copied to shared memory (cp.async) some batches of kBnRows rows ahead. A thread
-// copies and reads only its own eight columns, so a batch is ready for it when its own copies
-// are: no barrier. A batch has, for each of its rows and tensors, planes of 16 bytes a thread.
-// Slots whose tensor or columns are not there are zeroed once and never copied to.
-struct RowRing {
+// Rows are copied to shared memory (cp.async) some batches of kBnRows rows ahead. A batch has,
+// for each of its rows and tensors, planes of 16 bytes a thread. Slots whose tensor or columns are
+// not there are zeroed once and never copied to.
+//
+// VEC: a thread copies and reads only its own eight columns, so a batch is ready for it when its
+// own copies are: no barrier. Else the rows start anywhere in 16 bytes, which wide copies do not,
+// and warps copy together. fp32 elements go to their thread's place one by one. Of 16-bit ones, for
+// which there are no asynchronous copies of their own, the 33 aligned pieces that the warp's 256
+// columns touch are copied (a plane has 33), and when they have landed each thread shifts its
+// own columns into its place (take and land; N = 32768, D = 4095 bf16, two RMS norms: forward 683 to
+// 421 us, backward 1030 to 730 us against loads of single elements).
+template <bool VEC> struct RowRing {
   uint32_t first, end;       // this thread's first plane of the ring's first batch, and past its last
-  int plane;                 // bytes of a plane (16 a thread)
+  int plane;                 // bytes from a plane of the thread to the next
   int row_bytes;             // from a batch's row to its next; 0 where it has one, which is read in the next one's place
   uint32_t batch_bytes;
 
   __device__ __forceinline__ void init(char* smem, int planes, int batches, int rows) {
-    plane = 16 * int(blockDim.x);
-    row_bytes = rows > 1 ? planes * plane : 0;
-    batch_bytes = uint32_t(rows * planes * plane);
-    first = smem_addr(smem) + 16u * threadIdx.x;
+    const int warps = int(blockDim.x) / 32, warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
+    plane = VEC ? 16 * int(blockDim.x) : kBnWarpPlane;
+    const int row = VEC ? planes * plane : warps * planes * plane;
+    row_bytes = rows > 1 ? row : 0;
+    batch_bytes = uint32_t(rows * row);
+    first = smem_addr(smem) + 16u * uint32_t(VEC ? int(threadIdx.x) : lane) + uint32_t(VEC ? 0 : warp * planes * plane);
     end = first + uint32_t(batches) * batch_bytes;
-    for (uint32_t at = first; at < end; at += uint32_t(plane))
-      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+    for (uint32_t at = first; at < end; at += uint32_t(row))
+      for (int i = 0; i < planes; ++i)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at + uint32_t(i * plane)), "r"(0) : "memory");
+    if (!VEC) __syncwarp();
   }
   __device__ __forceinline__ uint32_t after(uint32_t batch) const {
     return batch + batch_bytes == end ? first : batch + batch_bytes;
   }
-  // A thread's columns of a row into their planes. What cannot be copied asynchronously, 16-bit
-  // elements at odd places, is returned, for land(): all are on their way before the first is
-  // waited for.
-  template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> copy(uint32_t to, int planes, const T* row, const Cols& cs) const {
-    Raw8<T> v{};
+  // Not VEC: the columns before a warp's first thread's, and where they are in memory.
+  __device__ __forceinline__ static int warp_col(const Cols& cs) { return cs.col - 8 * (int(threadIdx.x) % 32); }
+  // A row's columns into their planes; base: the tensor, whose first row may start within 16 bytes.
+  // Not VEC: by the whole warp, if any of its columns are in the row.
+  template <typename T> __device__ __forceinline__ void copy(uint32_t to, int planes, const void* base, const T* row, const Cols& cs) const {
+    constexpr int kPieces = int(sizeof(T)) / 2;
     if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < int(sizeof(T)) / 2; ++i)
+      for (int i = 0; i < kPieces; ++i)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + uint32_t((planes + i) * plane)),
                      "l"(reinterpret_cast<const char*>(row + cs.col) + 16 * i)
                      : "memory");
     } else if constexpr (sizeof(T) == 4) {
-      const Cols c = cs.afresh();
+      // each element to its thread's place: neighbouring lanes copy neighbouring columns
+      const int lane = int(threadIdx.x) % 32, c = warp_col(cs) + lane;
+      to += uint32_t((planes + lane % 8 / 4) * plane + 16 * (lane / 8) + 4 * (lane % 4) - 16 * lane);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c.at(i) < c.D)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + uint32_t((planes + i / 4) * plane + i % 4 * 4)),
-                       "l"(row + c.at(i))
-                       : "memory");
+        if (c + 32 * i < cs.D)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 64u * i), "l"(row + c + 32 * i) : "memory");
     } else {
-      v = load8<T, false>(row, cs);
+      const int lane = int(threadIdx.x) % 32;
+      const char* at = reinterpret_cast<const char*>(row + warp_col(cs));
+      const int s = int(reinterpret_cast<uintptr_t>(at) & 15);
+      const int columns = cs.D - warp_col(cs) < 256 ? cs.D - warp_col(cs) : 256;
+      const int bytes = s + columns * int(sizeof(T)) - 16 * lane;  // from the lane's piece on
+      at += 16 * lane - s;
+      to += uint32_t(planes * plane);
+      if (bytes > 0 && at < static_cast<const char*>(base)) {  // nothing before the tensor is read
+        for (int e = s; e < (bytes < 16 ? bytes : 16); e += int(sizeof(T)))
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + uint32_t(e)), "h"(*reinterpret_cast<const uint16_t*>(at + e)) : "memory");
+      } else if (bytes > 0) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(at), "r"(bytes < 16 ? bytes : 16) : "memory");
+      }
+      if (lane == 0 && bytes > 512)  // the 33rd
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 512u), "l"(at + 512), "r"(bytes - 512 < 16 ? bytes - 512 : 16)
+                     : "memory");
+    }
+  }
+  // Not VEC: the thread's own columns of a row of 16-bit elements that has landed; row: where it came
+  // from. All lanes take before any puts them into its own place.
+  template <typename T> __device__ __forceinline__ Raw8<T> take(uint32_t to, int planes, const T* row, const Cols& cs) const {
+    Raw8<T> v = raw_zero<T>();
+    if constexpr (sizeof(T) == 2) {
+      const int s = int(reinterpret_cast<uintptr_t>(row + warp_col(cs)) & 15);
+      const uint32_t at = to + uint32_t(planes * plane);
+      uint32_t w[8], q[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                     : "r"(at + 16u * i));
+      words_from<T>(s / 4, w, s & 2, q);
+      if (cs.D - warp_col(cs) < 256) {  // the row's last warp: nothing past the row
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int left = cs.D - cs.col - 2 * i;  // columns of the row from this word on
+          q[i] = left <= 0 ? 0 : left == 1 ? q[i] & 0xffffu : q[i];
+        }
+      }
+      v.v[0] = make_uint4(q[0], q[1], q[2], q[3]);
     }
     return v;
   }
-  template <typename T, bool VEC> __device__ __forceinline__ void land(uint32_t to, int planes, const Raw8<T>& v) const {
-    if constexpr (!VEC && sizeof(T) == 2)
+  template <typename T> __device__ __forceinline__ void land(uint32_t to, int planes, const Raw8<T>& v) const {
+    if constexpr (sizeof(T) == 2)
       asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + uint32_t(planes * plane)), "r"(v.v[0].x), "r"(v.v[0].y),
                    "r"(v.v[0].z), "r"(v.v[0].w)
                    : "memory");
@@ -122,7 +173,7 @@ template <typename T> __device__ __forceinline__ T* row_at(void* base, int64_t r
 // sum is enough: a buffer is written again only after the barrier of the sum between. Words
 // of warps that are not there stay zero.
 // CLUSTER: blocks share rows; code apart, for its registers.
-template <bool CLUSTER, bool VEC> struct RowSum {
+template <bool CLUSTER> struct RowSum {
   float* buf;      // [2][kMaxValues * nw] of this row group
   float* clus;     // [2][kBnMaxCluster][4] of this block
   int nw, warp, lane, bar, threads, turn;
@@ -232,8 +283,8 @@ template <bool CLUSTER, bool VEC> struct RowSum {
         }
       };
 #pragma unroll 3
-      for (int w = 0; w < (VEC ? full : nw); ++w) add(w, VEC ? 256.f : columns[w].x, VEC ? 1.f / 256.f : columns[w].y);
-      if (VEC && part > 0) add(full, float(part), part_inv);
+      for (int w = 0; w < full; ++w) add(w, 256.f, 1.f / 256.f);
+      if (part > 0) add(full, float(part), part_inv);
       const float n = CLUSTER ? block_columns(int(cluster_ctarank())) : float(D), inv_n = CLUSTER ? (n > 0.f ? 1.f / n : 0.f) : inv_d;
 #pragma unroll
       for (int i = 0; i < NR / 2; ++i) {
@@ -327,13 +378,10 @@ template <bool CLUSTER, bool VEC> struct RowSum {
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] += c[kMaxValues * r + i];
   }
-  // Columns of the block's warps. VEC: `full` warps have 256 and the next one has `part`; else a
-  // table has each warp's and one over it.
+  // Columns of the block's warps: `full` warps have 256 and the next one has `part`.
   int full, part;
   float part_inv;
-  const float2* columns;
   __device__ __forceinline__ float inv_columns(int w) const {
-    if constexpr (!VEC) return columns[w].y;
     return w < full ? 1.f / 256.f : w == full ? part_inv : 0.f;
   }
 };
@@ -397,7 +445,7 @@ __device__ __forceinline__ void load_weight(const void* w, int dt, float off, co
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     f[i] = VEC ? make_float2(f[i].x + off, f[i].y + off)
-               : make_float2(cs.at(2 * i) < cs.D ? f[i].x + off : 0.f, cs.at(2 * i + 1) < cs.D ? f[i].y + off : 0.f);
+               : make_float2(cs.col + 2 * i < cs.D ? f[i].x + off : 0.f, cs.col + 2 * i + 1 < cs.D ? f[i].y + off : 0.f);
 }
 
 // Eight values in shared memory, in two planes: a parameter's for a thread of a row, in the
@@ -431,40 +479,30 @@ template <bool VEC> __device__ __forceinline__ void cut8(float2 (&v)[4], const C
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(live));
   } else {
-    const Cols c = cs.afresh();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = make_float2(c.at(2 * i) < c.D ? v[i].x : 0.f, c.at(2 * i + 1) < c.D ? v[i].y : 0.f);
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_float2(cs.col + 2 * i < cs.D ? v[i].x : 0.f, cs.col + 2 * i + 1 < cs.D ? v[i].y : 0.f);
   }
 }
 
 // Scratch of the sums: two barriers and two buffers of a cluster's sums, two buffers of all
-// warps' sums, two words a warp of its columns.
-constexpr int kClusterWords = 4 + 2 * RowSum<false, true>::kMaxValues * kBnMaxCluster;
-constexpr int kRowSumWords = kClusterWords + (2 * RowSum<false, true>::kMaxValues + 2) * kBnMaxThreads / 32;
+// warps' sums.
+constexpr int kClusterWords = 4 + 2 * RowSum<false>::kMaxValues * kBnMaxCluster;
+constexpr int kRowSumWords = kClusterWords + 2 * RowSum<false>::kMaxValues * kBnMaxThreads / 32;
 
-template <bool CLUSTER, bool VEC>
-__device__ __forceinline__ RowSum<CLUSTER, VEC> row_sum(float* scratch, const RowThread& r, int threads_per_row, int cluster, int D) {
-  RowSum<CLUSTER, VEC> rs;
+template <bool CLUSTER>
+__device__ __forceinline__ RowSum<CLUSTER> row_sum(float* scratch, const RowThread& r, int threads_per_row, int cluster, int D) {
+  RowSum<CLUSTER> rs;
   rs.D = D;
   const int cols = D - (r.col - 8 * r.t), most = 8 * threads_per_row;  // columns from this block's first on
   rs.full = (cols < 0 ? 0 : cols < most ? cols : most) / 256;
   rs.part = cols < 0 || cols >= most ? 0 : cols % 256;
   rs.part_inv = rs.part > 0 ? 1.f / float(rs.part) : 0.f;
-  rs.columns = reinterpret_cast<const float2*>(scratch + kRowSumWords - 2 * kBnMaxThreads / 32);
   rs.clus = scratch + 4;  // behind the cluster's two barriers
   rs.nw = threads_per_row / 32;
-  rs.buf = scratch + kClusterWords + r.group * 2 * RowSum<false, true>::kMaxValues * rs.nw;
+  rs.buf = scratch + kClusterWords + r.group * 2 * RowSum<false>::kMaxValues * rs.nw;
   for (int i = int(threadIdx.x); i < kRowSumWords; i += int(blockDim.x)) scratch[i] = 0.f;
   __syncthreads();
-  if (!VEC && int(threadIdx.x) < rs.nw) {
-    float n = 0.f;  // of columns t + i threads_per_row, i = 0 ... 7, of warp threadIdx.x
-    for (int i = 0; i < 8; ++i) {
-      const int left = cols - i * threads_per_row - 32 * int(threadIdx.x);
-      n += float(left < 0 ? 0 : left < 32 ? left : 32);
-    }
-    const_cast<float2*>(rs.columns)[threadIdx.x] = make_float2(n, n > 0.f ? 1.f / n : 0.f);
-  }
-  if (!VEC) __syncthreads();
   if (CLUSTER && threadIdx.x == 0) {
     mbar_init(reinterpret_cast<uint64_t*>(scratch), 1);
     mbar_init(reinterpret_cast<uint64_t*>(scratch) + 1, 1);
@@ -536,39 +574,53 @@ __global__ void __launch_bounds__(bn_max_threads(FEAT, VEC, CLUSTER), 1)
   constexpr int kX = 0, kR = sizeof(TX) / 2, kG = kR + sizeof(TR) / 2;  // planes of x, residual and full gate
   constexpr int kParams = bn_shared_params(FEAT, false);
   const RowThread r0 = row_thread(threads_per_row, cluster);
-  RowSum<CLUSTER, VEC> rs = row_sum<CLUSTER, VEC>(scratch, r0, threads_per_row, cluster, p.D);
-  const int col = VEC ? r0.col : r0.col - 7 * r0.t, D = p.D;  // VEC or not, a block has 8 columns a thread
-  const Cols cs{col, VEC ? 1 : threads_per_row, D, true};
-  const bool live = col < D;  // else a thread past the row, whose values are zero
+  RowSum<CLUSTER> rs = row_sum<CLUSTER>(scratch, r0, threads_per_row, cluster, p.D);
+  const int col = r0.col, D = p.D;
+  const Cols cs{col, D};
+  // else a thread (or, where warps copy together, a warp) past the row, whose values are zero
+  const bool copies = (VEC ? col : RowRing<VEC>::warp_col(cs)) < D;
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
   constexpr bool gate_full = GATE && (FEAT & BN_GATE_ROWS) != 0;  // a gate for each row, else for groups of rows
   const int lo = int(r0.worker * p.chunk_rows < p.N ? r0.worker * p.chunk_rows : p.N);
   const int hi = int(lo + p.chunk_rows < p.N ? lo + p.chunk_rows : p.N);
-  RowRing ring{};
+  RowRing<VEC> ring{};
   int next = lo;  // the row that is copied next
   auto fetch = [&](uint32_t at) FLCE_INLINE {
-    Raw8<TX> x[R], gx[R];
-    Raw8<TR> res[R], gr[R];
+    if (!VEC) __syncwarp();  // the warp has read what was there
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (!live || r >= per || next + r >= hi) continue;
+      if (!copies || r >= per || next + r >= hi) continue;
       const uint32_t to = at + uint32_t(r * ring.row_bytes);
-      x[r] = ring.copy<TX, VEC>(to, kX, row_at<TX>(p.x, next + r, p.ld_x), cs);
-      if (p.residual != nullptr) res[r] = ring.copy<TR, VEC>(to, kR, row_at<TR>(p.residual, next + r, p.ld_residual), cs);
-      if (gate_full && p.gate_res_type) gr[r] = ring.copy<TR, VEC>(to, kG, row_at<TR>(p.gate, next + r, p.ld_gate), cs);
-      if (gate_full && !p.gate_res_type) gx[r] = ring.copy<TX, VEC>(to, kG, row_at<TX>(p.gate, next + r, p.ld_gate), cs);
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (!live || r >= per || next + r >= hi) continue;
-      const uint32_t to = at + uint32_t(r * ring.row_bytes);
-      ring.land<TX, VEC>(to, kX, x[r]);
-      if (p.residual != nullptr) ring.land<TR, VEC>(to, kR, res[r]);
-      if (gate_full && p.gate_res_type) ring.land<TR, VEC>(to, kG, gr[r]);
-      if (gate_full && !p.gate_res_type) ring.land<TX, VEC>(to, kG, gx[r]);
+      ring.copy(to, kX, p.x, row_at<TX>(p.x, next + r, p.ld_x), cs);
+      if (p.residual != nullptr) ring.copy(to, kR, p.residual, row_at<TR>(p.residual, next + r, p.ld_residual), cs);
+      if (gate_full && p.gate_res_type) ring.copy(to, kG, p.gate, row_at<TR>(p.gate, next + r, p.ld_gate), cs);
+      if (gate_full && !p.gate_res_type) ring.copy(to, kG, p.gate, row_at<TX>(p.gate, next + r, p.ld_gate), cs);
     }
     next += per;
     ring.commit();
+  };
+  // Waits for the batch in slot `at`, whose first row is `row`.
+  auto arrive = [&](uint32_t at, int row) FLCE_INLINE {
+    ring.wait(batches - 1);
+    if constexpr (!VEC) {
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (!copies || r >= per || row + r >= hi) continue;
+        const uint32_t to = at + uint32_t(r * ring.row_bytes);
+        Raw8<TR> res = raw_zero<TR>(), gr = raw_zero<TR>();
+        Raw8<TX> gx = raw_zero<TX>();
+        const Raw8<TX> x = ring.take(to, kX, row_at<TX>(p.x, row + r, p.ld_x), cs);
+        if (p.residual != nullptr) res = ring.take(to, kR, row_at<TR>(p.residual, row + r, p.ld_residual), cs);
+        if (gate_full && p.gate_res_type) gr = ring.take(to, kG, row_at<TR>(p.gate, row + r, p.ld_gate), cs);
+        if (gate_full && !p.gate_res_type) gx = ring.take(to, kG, row_at<TX>(p.gate, row + r, p.ld_gate), cs);
+        __syncwarp();
+        ring.land(to, kX, x);
+        if (p.residual != nullptr) ring.land(to, kR, res);
+        if (gate_full && p.gate_res_type) ring.land(to, kG, gr);
+        if (gate_full && !p.gate_res_type) ring.land(to, kG, gx);
+      }
+    }
   };
   ring.init(ring_smem + (FULL ? kParams * 32 * threads_per_row : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
   for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
@@ -614,8 +666,8 @@ __global__ void __launch_bounds__(bn_max_threads(FEAT, VEC, CLUSTER), 1)
 #pragma unroll
   for (int r = 0; r < R; ++r) m1[r] = 0.f, r1[r] = 1.f;
   if (lo < hi) {
-    ring.wait(batches - 1);
-    if (post) row_stats<R, VEC, FULL, RowSum<CLUSTER, VEC>>([&](int r, float2 (&v)[4]) { ring.get<TX>(batch, r, kX, v); }, cs, p.layer, p.eps, inv_d, rs, m1, r1);
+    arrive(batch, lo);
+    if (post) row_stats<R, VEC, FULL, RowSum<CLUSTER>>([&](int r, float2 (&v)[4]) { ring.template get<TX>(batch, r, kX, v); }, cs, p.layer, p.eps, inv_d, rs, m1, r1);
   }
   for (int row = lo; row < hi; row += per) {
     const bool second = per > 1 && row + 1 < hi;  // the last batch may have one row
@@ -630,9 +682,9 @@ __global__ void __launch_bounds__(bn_max_threads(FEAT, VEC, CLUSTER), 1)
       if (gate_full) {
         float2 a[4];
         if (p.gate_res_type)
-          ring.get<TR>(batch, r, kG, a);
+          ring.template get<TR>(batch, r, kG, a);
         else
-          ring.get<TX>(batch, r, kG, a);
+          ring.template get<TX>(batch, r, kG, a);
         activate8(a, p.act);
         set_gate(a);
       } else if (gate && row + r >= gate_end) {
@@ -643,8 +695,8 @@ __global__ void __launch_bounds__(bn_max_threads(FEAT, VEC, CLUSTER), 1)
         gate_end = int((g + 1) * p.gate_group);
       }
       float2 u[4];
-      ring.get<TX>(batch, r, kX, u);
-      ring.get<TR>(batch, r, kR, h[r]);
+      ring.template get<TX>(batch, r, kX, u);
+      ring.template get<TR>(batch, r, kR, h[r]);
       if (FULL) {
         float2 w[4], b[4];
         param(kW1, w);
@@ -668,19 +720,19 @@ __global__ void __launch_bounds__(bn_max_threads(FEAT, VEC, CLUSTER), 1)
     for (int r = 0; r < R; ++r) m2[r] = r2[r] = n1[r] = 0.f, k1[r] = 1.f;
     fetch(batch);
     batch = ring.after(batch);
-    ring.wait(batches - 1);
+    arrive(batch, row + per);
     auto get_h = [&](int r, float2 (&v)[4]) FLCE_INLINE {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = h[r][i];
     };
     if (post && pre) {
       float mean[2 * R], rstd[2 * R];
-      row_stats<2 * R, VEC, FULL, RowSum<CLUSTER, VEC>>(
+      row_stats<2 * R, VEC, FULL, RowSum<CLUSTER>>(
           [&](int r, float2 (&v)[4]) {
             if (r < R)
               get_h(r, v);
             else
-              ring.get<TX>(batch, r - R, kX, v);
+              ring.template get<TX>(batch, r - R, kX, v);
           },
           cs, p.layer, p.eps, inv_d, rs, mean, rstd);
 #pragma unroll
@@ -691,9 +743,9 @@ __global__ void __launch_bounds__(bn_max_threads(FEAT, VEC, CLUSTER), 1)
         k1[r] = rstd[R + r];
       }
     } else if (pre) {
-      row_stats<R, VEC, FULL, RowSum<CLUSTER, VEC>>(get_h, cs, p.layer, p.eps, inv_d, rs, m2, r2);
+      row_stats<R, VEC, FULL, RowSum<CLUSTER>>(get_h, cs, p.layer, p.eps, inv_d, rs, m2, r2);
     } else if (post) {
-      row_stats<R, VEC, FULL, RowSum<CLUSTER, VEC>>([&](int r, float2 (&v)[4]) { ring.get<TX>(batch, r, kX, v); }, cs, p.layer, p.eps, inv_d, rs, n1, k1);
+      row_stats<R, VEC, FULL, RowSum<CLUSTER>>([&](int r, float2 (&v)[4]) { ring.template get<TX>(batch, r, kX, v); }, cs, p.layer, p.eps, inv_d, rs, n1, k1);
     }
     if (pre) {
       float2 b2[4];
@@ -745,13 +797,14 @@ __global__ void __launch_bounds__(kBnThreads, 1)
   // in shared memory: a bias's sum, and with a gate that and both biases' sums
   constexpr bool OWN_B = POST && FULL, OWN_A = POST && GATE && FULL;
   const RowThread r0 = row_thread(threads_per_row, cluster);
-  RowSum<CLUSTER, VEC> rs = row_sum<CLUSTER, VEC>(scratch, r0, threads_per_row, cluster, p.D);
-  const int col = VEC ? r0.col : r0.col - 7 * r0.t, D = p.D;  // VEC or not, a block has 8 columns a thread
-  const Cols cs{col, VEC ? 1 : threads_per_row, D, false};
+  RowSum<CLUSTER> rs = row_sum<CLUSTER>(scratch, r0, threads_per_row, cluster, p.D);
+  const int col = r0.col, D = p.D;
+  const Cols cs{col, D};
   const bool post = POST && p.w1 != nullptr, pre = p.w2 != nullptr, gate = GATE && p.gate != nullptr;
   constexpr bool gate_full = GATE && (FEAT & BN_GATE_ROWS) != 0;  // a gate for each row, else for groups of rows
   const int workers = int(gridDim.x) / cluster * (int(blockDim.x) / threads_per_row);
   const bool live_col = col < D;
+  const bool copies = (VEC ? col : RowRing<VEC>::warp_col(cs)) < D;
   // the worker's rows: chunk after chunk, once for the copies and once, behind them, for the work
   struct Rows {
     int chunk, row, hi;
@@ -763,7 +816,7 @@ __global__ void __launch_bounds__(kBnThreads, 1)
     w.row = first + (w.chunk - group * int(p.chunks_per_group)) * int(p.chunk_rows);
     w.hi = end - w.row < int(p.chunk_rows) ? end : w.row + int(p.chunk_rows);
   };
-  RowRing ring{};
+  RowRing<VEC> ring{};
   Rows ahead{int(r0.worker), 0, 0};
   open(ahead);
   // a batch's statistics: copied by the first lanes of each warp for the warp alone
@@ -779,28 +832,18 @@ __global__ void __launch_bounds__(kBnThreads, 1)
                      "l"(stats + row)
                      : "memory");
       }
-      if (live_col) {
+      if (copies) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           if (r > 0 && (r >= per || ahead.row + r >= ahead.hi)) continue;
           const uint32_t to = at + uint32_t(r * ring.row_bytes);
           const int row = ahead.row + r;
-          const Raw8<TX> x = ring.copy<TX, VEC>(to, kX, row_at<TX>(p.x, row, p.ld_x), cs);
-          Raw8<TR> h = raw_zero<TR>(), dh = raw_zero<TR>();
-          Raw8<TX> dy = raw_zero<TX>();
-          if (pre) h = ring.copy<TR, VEC>(to, kH, row_at<TR>(p.h_in, row, D), cs);
-          if (p.dh != nullptr) dh = ring.copy<TR, VEC>(to, kDh, row_at<TR>(p.dh, row, p.ld_dh), cs);
-          if (pre && p.dy != nullptr) dy = ring.copy<TX, VEC>(to, kY, row_at<TX>(p.dy, row, p.ld_dy), cs);
-          if (gate_full) {
-            if (p.gate_res_type)
-              ring.land<TR, VEC>(to, kG, ring.copy<TR, VEC>(to, kG, row_at<TR>(p.gate, row, p.ld_gate), cs));
-            else
-              ring.land<TX, VEC>(to, kG, ring.copy<TX, VEC>(to, kG, row_at<TX>(p.gate, row, p.ld_gate), cs));
-          }
-          ring.land<TX, VEC>(to, kX, x);
-          ring.land<TR, VEC>(to, kH, h);
-          ring.land<TR, VEC>(to, kDh, dh);
-          ring.land<TX, VEC>(to, kY, dy);
+          ring.copy(to, kX, p.x, row_at<TX>(p.x, row, p.ld_x), cs);
+          if (pre) ring.copy(to, kH, p.h_in, row_at<TR>(p.h_in, row, D), cs);
+          if (p.dh != nullptr) ring.copy(to, kDh, p.dh, row_at<TR>(p.dh, row, p.ld_dh), cs);
+          if (pre && p.dy != nullptr) ring.copy(to, kY, p.dy, row_at<TX>(p.dy, row, p.ld_dy), cs);
+          if (gate_full && p.gate_res_type) ring.copy(to, kG, p.gate, row_at<TR>(p.gate, row, p.ld_gate), cs);
+          if (gate_full && !p.gate_res_type) ring.copy(to, kG, p.gate, row_at<TX>(p.gate, row, p.ld_gate), cs);
         }
       }
       ahead.row += per;
@@ -811,6 +854,43 @@ __global__ void __launch_bounds__(kBnThreads, 1)
     }
     ring.commit();
     stat_slot = stat_slot + 1 == batches ? 0 : stat_slot + 1;
+  };
+  // Waits until all but the newest `left` batches have landed, the last of them in slot `at`, rows w.
+  auto arrive = [&](int left, uint32_t at, const Rows& w) FLCE_INLINE {
+    ring.wait(left);
+    __syncwarp();
+    if constexpr (!VEC) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (!copies || (r > 0 && (r >= per || w.row + r >= w.hi))) continue;
+        const uint32_t to = at + uint32_t(r * ring.row_bytes);
+        const int row = w.row + r;
+        {
+          Raw8<TR> h = raw_zero<TR>();
+          const Raw8<TX> x = ring.take(to, kX, row_at<TX>(p.x, row, p.ld_x), cs);
+          if (pre) h = ring.take(to, kH, row_at<TR>(p.h_in, row, D), cs);
+          __syncwarp();
+          ring.land(to, kX, x);
+          ring.land(to, kH, h);
+        }
+        Raw8<TR> dh = raw_zero<TR>();
+        Raw8<TX> dy = raw_zero<TX>();
+        if (p.dh != nullptr) dh = ring.take(to, kDh, row_at<TR>(p.dh, row, p.ld_dh), cs);
+        if (pre && p.dy != nullptr) dy = ring.take(to, kY, row_at<TX>(p.dy, row, p.ld_dy), cs);
+        __syncwarp();
+        ring.land(to, kDh, dh);
+        ring.land(to, kY, dy);
+        if (gate_full && p.gate_res_type) {
+          const Raw8<TR> g = ring.take(to, kG, row_at<TR>(p.gate, row, p.ld_gate), cs);
+          __syncwarp();
+          ring.land(to, kG, g);
+        } else if (gate_full) {
+          const Raw8<TX> g = ring.take(to, kG, row_at<TX>(p.gate, row, p.ld_gate), cs);
+          __syncwarp();
+          ring.land(to, kG, g);
+        }
+      }
+    }
   };
   ring.init(ring_smem + kParams * 32 * threads_per_row + bn_own_params(FEAT, true) * 32 * int(blockDim.x),
             kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
@@ -849,14 +929,14 @@ __global__ void __launch_bounds__(kBnThreads, 1)
   const float live = live_col ? 1.f : 0.f;  // threads past the row: their values stay zero
   // values of row r of the batch in slot `at`
   auto get_x = [&](uint32_t at, int r, float m1, float2 (&v)[4]) FLCE_INLINE {
-    ring.get<TX>(at, r, kX, v);
+    ring.template get<TX>(at, r, kX, v);
     if (FULL && POST) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = add2(v[i], both(-m1));
     }
   };
   auto get_h = [&](uint32_t at, int r, float m2, float2 (&v)[4]) FLCE_INLINE {
-    ring.get<TR>(at, r, kH, v);
+    ring.template get<TR>(at, r, kH, v);
     if (FULL) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = add2(v[i], both(-m2));
@@ -885,7 +965,7 @@ __global__ void __launch_bounds__(kBnThreads, 1)
       const float4 st = get_stats(slot, r);
       float2 n[4], g[4];
       get_h(at, r, st.z, n);
-      ring.get<TX>(at, r, kY, g);
+      ring.template get<TX>(at, r, kY, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], w2[i]);
       s1[r] = dot8(g, n);
@@ -928,8 +1008,7 @@ __global__ void __launch_bounds__(kBnThreads, 1)
 #pragma unroll
   for (int r = 0; r < R; ++r) s1[r] = s0[r] = t1[r] = t0[r] = 0.f;
   if (now.chunk < p.chunks && pre) {
-    ring.wait(batches - 1);
-    __syncwarp();
+    arrive(batches - 1, batch, now);
     second_norm(batch, slot, now, s1, s0);
     total(t1, t0, s1, s0);
   }
@@ -938,10 +1017,7 @@ __global__ void __launch_bounds__(kBnThreads, 1)
     const bool second = per > 1 && row + 1 < now.hi;  // a chunk's last batch may have one row
     Rows next = now;
     step(next);
-    if (!pre) {
-      ring.wait(batches - 1);
-      __syncwarp();
-    }
+    if (!pre) arrive(batches - 1, batch, now);
     float2 d[R][4];  // the gradient of h, then what the first norm's gradient is taken of
     if (FULL && POST) param(kW1, w1);
 #pragma unroll
@@ -949,11 +1025,11 @@ __global__ void __launch_bounds__(kBnThreads, 1)
       t1[r] = t0[r] = 0.f;
       if (r > 0 && !second) continue;
       const float4 st = get_stats(slot, r);
-      ring.get<TR>(batch, r, kDh, d[r]);
+      ring.template get<TR>(batch, r, kDh, d[r]);
       if (pre) {
         float2 n[4], g[4];
         get_h(batch, r, st.z, n);
-        ring.get<TX>(batch, r, kY, g);
+        ring.template get<TX>(batch, r, kY, g);
         if (FULL) param(kW2, w2);
         if (FULL) {
           if (OWN_A) own(kDb2, db2);
@@ -977,9 +1053,9 @@ __global__ void __launch_bounds__(kBnThreads, 1)
       if (POST || GATE) get_x(batch, r, st.x, x);
       if (gate_full) {
         if (p.gate_res_type)
-          ring.get<TR>(batch, r, kG, a);
+          ring.template get<TR>(batch, r, kG, a);
         else
-          ring.get<TX>(batch, r, kG, a);
+          ring.template get<TX>(batch, r, kG, a);
         activate8(a, p.act);
         if (p.dgate != nullptr) {  // d u scale act', u = (x - m) r w1 + b1, or x
           float2 e[4], da[4];
@@ -1026,8 +1102,7 @@ __global__ void __launch_bounds__(kBnThreads, 1)
     const uint32_t batch_next = ring.after(batch);
     const int slot_next = slot + 1 == batches ? 0 : slot + 1;
     if (pre && next.chunk < p.chunks) {
-      ring.wait(batches - 2);
-      __syncwarp();
+      arrive(batches - 2, batch_next, next);
       second_norm(batch_next, slot_next, next, s1, s0);
     }
     if (pre || post) total(t1, t0, s1, s0);
@@ -1148,11 +1223,11 @@ __global__ void __launch_bounds__(kBnThreads, 1)
 }
 
 template <typename K>
-cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& s, unsigned blocks, int planes, int feat,
+cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& s, unsigned blocks, int planes, bool vec, int feat,
                       bool backward, cudaStream_t stream) {
   const int threads = s.threads_per_row * s.rows_per_block;
-  const BnRing r = bn_ring(s, planes, feat, backward);
-  size_t smem = size_t(r.params_bytes) + size_t(planes) * 16 * threads * r.per * r.batches;
+  const BnRing r = bn_ring(s, planes, vec, feat, backward);
+  size_t smem = size_t(r.params_bytes) + size_t(bn_row_bytes(threads, planes, vec)) * r.per * r.batches;
   if (smem < size_t(threads) * 32) smem = size_t(threads) * 32;  // row groups add up their sums in it
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmemBytes);
   if (e != cudaSuccess) return e;
@@ -1174,7 +1249,7 @@ cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& 
 
 // The kernel of a feature set (as bn_kernel_features gives it); the argument: more of one row a block.
 #define FLCE_BN_CASE(VEC, CLUSTER, FEAT) \
-  case FEAT: return bn_launch(KERNEL<TX, TR, VEC, CLUSTER, FEAT>, p, s, blocks, planes, FEAT, BACKWARD, stream)
+  case FEAT: return bn_launch(KERNEL<TX, TR, VEC, CLUSTER, FEAT>, p, s, blocks, planes, VEC, FEAT, BACKWARD, stream)
 #define FLCE_BN_WIDE_CASES FLCE_BN_CASE(true, false, 23); FLCE_BN_CASE(true, false, 31)
 #define FLCE_BN_DISPATCH(...)                                                               \
   const int planes = bn_planes(int(sizeof(TX)), int(sizeof(TR)), p.gate_full, BACKWARD);    \

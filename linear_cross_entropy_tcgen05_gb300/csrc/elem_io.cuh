@@ -179,20 +179,11 @@ template <typename T> __device__ __forceinline__ Raw8<T> pack8(const float2 (&f)
   return pack8<T>(g);
 }
 
-// A thread's eight columns of a row of D: col, col + 1, ... where rows are aligned to eight elements
-// and D is a multiple of eight (VEC: one access), else col, col + step, ... with neighbouring
-// threads on neighbouring columns. Columns past the row read as zero and are not written.
+// A thread's eight columns of a row of D. VEC: rows are aligned to eight elements and D is a multiple
+// of eight, so they are one access and all in the row or all past it. Columns past the row read as
+// zero and are not written.
 struct Cols {
-  int col, step, D;
-  bool kept;  // a kernel with registers to spare keeps the offsets
-  __device__ __forceinline__ int at(int i) const { return col + i * step; }
-  // The same columns, to the compiler others: kept from one tensor to the next, their eight
-  // offsets and addresses cost the registers that the sums need.
-  __device__ __forceinline__ Cols afresh() const {
-    Cols c = *this;
-    if (!kept) asm("" : "+r"(c.col), "+r"(c.step));
-    return c;
-  }
+  int col, D;
 };
 
 template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> load8(const T* row, const Cols& c) {
@@ -200,22 +191,87 @@ template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> load8(const T
     return c.col < c.D ? raw_load(row + c.col) : raw_zero<T>();
   } else {
     float f[8];
-    const Cols d = c.afresh();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = d.at(i) < d.D ? to_f32(row[d.at(i)]) : 0.f;
+    for (int i = 0; i < 8; ++i) f[i] = c.col + i < c.D ? to_f32(row[c.col + i]) : 0.f;
     return pack8<T>(f);
   }
 }
 
-template <typename T, bool VEC> __device__ __forceinline__ void store8(T* row, const Cols& c, const float2 (&f)[4]) {
-  if constexpr (VEC) {
-    if (c.col < c.D) raw_store(row + c.col, pack8<T>(f));
-  } else {
-    const float g[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
-    const Cols d = c.afresh();
+// out = the words that begin 4 by + half bytes (half: 0 or 2) after w's first; what is past w is zero.
+// `by` is the same for a whole warp, so it chooses between copies of the code that name the
+// words, instead of choosing between words.
+template <int BY, typename T, int N, int M>
+__device__ __forceinline__ void words_from(const uint32_t (&w)[N], int half, uint32_t (&out)[M]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (d.at(i) < d.D) row[d.at(i)] = from_f32<T>(g[i]);
+  for (int i = 0; i < M; ++i) {
+    const uint32_t a = i + BY < N ? w[i + BY < N ? i + BY : 0] : 0u, b = i + BY + 1 < N ? w[i + BY + 1 < N ? i + BY + 1 : 0] : 0u;
+    out[i] = sizeof(T) == 4 ? a : __funnelshift_r(a, b, 8 * half);
+  }
+}
+template <typename T, int N, int M>
+__device__ __forceinline__ void words_from(int by, const uint32_t (&w)[N], int half, uint32_t (&out)[M]) {
+  switch (by) {
+    case 0: words_from<0, T>(w, half, out); break;
+    case 1: words_from<1, T>(w, half, out); break;
+    case 2: words_from<2, T>(w, half, out); break;
+    case 3: words_from<3, T>(w, half, out); break;
+    default: words_from<4, T>(w, half, out); break;
+  }
+}
+
+// Bytes first ... end - 1 of an aligned 16 that are in w.
+template <typename T> __device__ __forceinline__ void store_part(char* at, const uint32_t* w, int first, int end) {
+#pragma unroll
+  for (int i = 0; i < 16 / int(sizeof(T)); ++i) {
+    const int b = i * int(sizeof(T));
+    if (b < first || b >= end) continue;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<uint32_t*>(at + b) = w[i];
+    else
+      *reinterpret_cast<uint16_t*>(at + b) = uint16_t(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+  }
+}
+
+// Eight columns of a thread, neighbouring threads with neighbouring ones. Not VEC: called by whole
+// warps. The row's start is anywhere in 16 bytes, so a thread writes the aligned pieces that end in
+// its own, with what it lacks of the first from the thread before it.
+template <typename T, bool VEC> __device__ __forceinline__ void store8(T* row, const Cols& c, const float2 (&f)[4]) {
+  const Raw8<T> raw = pack8<T>(f);
+  if constexpr (VEC) {
+    if (c.col < c.D) raw_store(row + c.col, raw);
+  } else {
+    constexpr int kPieces = int(sizeof(T)) / 2, kWords = 4 * kPieces;
+    const int lane = int(threadIdx.x) % 32;
+    char* at = reinterpret_cast<char*>(row + c.col);
+    const int s = int(reinterpret_cast<uintptr_t>(at) & 15);
+    at -= s;
+    uint32_t w[kWords + 4], out[kWords + 4];  // the 16 bytes before the thread's own, and its own
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      w[4 + 4 * i] = raw.v[i].x;
+      w[5 + 4 * i] = raw.v[i].y;
+      w[6 + 4 * i] = raw.v[i].z;
+      w[7 + 4 * i] = raw.v[i].w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, w[kWords + i], 1);
+    words_from<T>((16 - s) / 4, w, s & 2, out);
+    // bytes of the thread's pieces that are in the row, from the first piece on
+    const int end = (c.D - c.col) * int(sizeof(T)) + s;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (end - 16 * i >= 16 && (i > 0 || lane > 0 || s == 0))
+        *reinterpret_cast<uint4*>(at + 16 * i) = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+    // pieces that are not whole: the warp's first, its last (up to the next warp's first), the row's last
+    if (lane == 0 && s > 0 && end > s) store_part<T>(at, out, s, end);
+    const int left = end - 16 * kPieces;
+    if (lane == 31 && s > 0 && left > 0) {
+      store_part<T>(at + 16 * kPieces, out + kWords, 0, left < s ? left : s);
+    } else if (left < 0 && end > 0) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        if (end - 16 * i > 0 && end - 16 * i < 16 && (i > 0 || lane > 0 || s == 0)) store_part<T>(at + 16 * i, out + 4 * i, 0, end - 16 * i);
+    }
   }
 }
 

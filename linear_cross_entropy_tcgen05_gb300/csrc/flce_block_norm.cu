@@ -50,7 +50,7 @@ struct BnKernel {
 };
 BnKernel bn_pick(const flce_block_norm_desc* d, bool vec, int feat, bool backward) {
   const int planes = bn_planes(elem_bytes(d->x_dtype), elem_bytes(d->residual_dtype), d->gate && d->gate_rows == d->N, backward);
-  auto fits = [&](const BlockNormShape& s, int f) { return bn_ring(s, planes, f, backward).batches >= 2; };
+  auto fits = [&](const BlockNormShape& s, int f) { return bn_ring(s, planes, vec, f, backward).batches >= 2; };
   const BlockNormShape s = bn_shape(d->D, kBnThreads);
   if (!backward && vec) {
     const BlockNormShape w = bn_shape(d->D, kBnMaxThreads);

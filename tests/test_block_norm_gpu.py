@@ -128,6 +128,36 @@ def test_wide_blocks(gpu_lib, case):
     test_against_the_formulas(gpu_lib, case)
 
 
+@pytest.mark.parametrize("x,res", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+def test_unaligned_widths(gpu_lib, x, res):
+    """Rows that start and end anywhere in 16 bytes, within one warp's columns and over several."""
+    for D in (2, 3, 5, 9, 12, 15, 17, 31, 33, 63, 249, 255, 257, 260, 263, 511, 513, 770, 2047, 2049):
+        test_against_the_formulas(gpu_lib, (5, D, x, res, "layer" if D % 2 else "rms", D % 3 > 0, (0, 1, -1)[D % 3],
+                                            "tanh", D % 2 > 0))
+
+
+@pytest.mark.parametrize("offset", range(1, 8))
+def test_unaligned_bases(gpu_lib, offset):
+    """Tensors that start anywhere in 16 bytes, with what is around their rows left as it is."""
+    N, D = 7, 264
+    g = torch.Generator(device=DEV).manual_seed(offset)
+    wide = torch.empty(N * (D + 3) + 16, device=DEV).normal_(generator=g).to(torch.bfloat16)
+    x = wide[offset:offset + N * (D + 3)].view(N, D + 3)[:, :D]
+    w = torch.empty(D, device=DEV).normal_(1.0, 0.2, generator=g)
+    h, y = flce.block_norm(x, None, w, post_weight=w)
+    h2, y2 = flce.block_norm(x.contiguous(), None, w, post_weight=w)
+    # sums are grouped alike; the aligned kernel of RMS norms multiplies in another order
+    assert ((h.float() - h2.float()).abs() <= 2.0 ** -8 * h2.float().abs() * 2).all()
+    assert ((y.float() - y2.float()).abs() <= 2.0 ** -8 * y2.float().abs() * 3).all()
+    buf = torch.full((N * D + 32,), 3.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[offset:offset + N * D].view(N, D)
+    d = flce.FlceBlockNormDesc(N=N, D=D, x=x.data_ptr(), post_weight=w.data_ptr(), weight=w.data_ptr(), ld_x=D + 3,
+                               post_weight_dtype=2, weight_dtype=2, eps=1e-6, scale=1.0)
+    flce.flce_block_norm_forward(d, out, y2)
+    assert torch.equal(out, h) and torch.equal(y2, y)
+    assert bool((buf[:offset] == 3).all()) and bool((buf[offset + N * D:] == 3).all())
+
+
 def test_without_a_weight(gpu_lib):
     case = (50, 384, "bf16", "f32", "rms", True, 1, "tanh", False)
     t, dh, _ = make(case)
