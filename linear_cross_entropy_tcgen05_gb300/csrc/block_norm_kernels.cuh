@@ -36,12 +36,14 @@ namespace {
 // not there are zeroed once and never copied to.
 //
 // VEC: a thread copies and reads only its own eight columns, so a batch is ready for it when its
-// own copies are: no barrier. Else the rows start anywhere in 16 bytes, which wide copies do not,
-// and warps copy together. fp32 elements go to their thread's place one by one. Of 16-bit ones, for
-// which there are no asynchronous copies of their own, the 33 aligned pieces that the warp's 256
-// columns touch are copied (a plane has 33), and when they have landed each thread shifts its
-// own columns into its place (take and land; N = 32768, D = 4095 bf16, two RMS norms: forward 683 to
-// 421 us, backward 1030 to 730 us against loads of single elements).
+// own copies are: no barrier. (Neighbouring lanes copying neighbouring 16 bytes of fp32 rows, to
+// one another's places, measured slower: N = 65536, D = 4096, forward 952 us against 896.) Else the
+// rows start anywhere in 16 bytes, which wide copies do not, and a warp copies its 256 columns
+// together. fp32 elements go to their thread's place one by one. Of 16-bit ones, which are too
+// small for that, the 33 aligned pieces that the columns touch are copied (a plane has 33),
+// and when they have landed each thread shifts its own columns into its place (take and land; N =
+// 32768, D = 4095 bf16, two RMS norms: forward 683 to 410 us, backward 1030 to 725 us against loads of
+// single elements).
 template <bool VEC> struct RowRing {
   uint32_t first, end;       // this thread's first plane of the ring's first batch, and past its last
   int plane;                 // bytes from a plane of the thread to the next
@@ -64,15 +66,14 @@ template <bool VEC> struct RowRing {
   __device__ __forceinline__ uint32_t after(uint32_t batch) const {
     return batch + batch_bytes == end ? first : batch + batch_bytes;
   }
-  // Not VEC: the columns before a warp's first thread's, and where they are in memory.
+  // The first column of the warp's first thread.
   __device__ __forceinline__ static int warp_col(const Cols& cs) { return cs.col - 8 * (int(threadIdx.x) % 32); }
   // A row's columns into their planes; base: the tensor, whose first row may start within 16 bytes.
-  // Not VEC: by the whole warp, if any of its columns are in the row.
+  // VEC: by threads whose columns are in the row, else by warps of which some are.
   template <typename T> __device__ __forceinline__ void copy(uint32_t to, int planes, const void* base, const T* row, const Cols& cs) const {
-    constexpr int kPieces = int(sizeof(T)) / 2;
     if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)
+      for (int i = 0; i < int(sizeof(T)) / 2; ++i)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + uint32_t((planes + i) * plane)),
                      "l"(reinterpret_cast<const char*>(row + cs.col) + 16 * i)
                      : "memory");
@@ -402,18 +403,26 @@ __device__ __forceinline__ RowThread row_thread(int threads_per_row, int cluster
   return r;
 }
 
-__device__ __forceinline__ float activate(float g, int act) {
-  return act == 1 ? 1.f / (1.f + expf(-g)) : tanhf(g);
+// QUICK: the sigmoid's reciprocal is the instruction's, off by one step at most. With a gate for each
+// row the forward's divisions were a quarter of its time (N = 32768, D = 4096 bf16, layer norms: 427
+// to 312 us); the backward has no registers for eight of these at once (740 to 855 us).
+template <bool QUICK> __device__ __forceinline__ float activate(float g, int act) {
+  if (act != 1) return tanhf(g);
+  const float d = 1.f + expf(-g);
+  if (!QUICK) return 1.f / d;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
 }
 // derivative of the activation, from its value
 __device__ __forceinline__ float activate_d(float a, int act) {
   return act == 0 ? 1.f : act == 1 ? a * (1.f - a) : 1.f - a * a;
 }
 
-__device__ __forceinline__ void activate8(float2 (&a)[4], int act) {
+template <bool QUICK> __device__ __forceinline__ void activate8(float2 (&a)[4], int act) {
   if (act == 0) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = make_float2(activate(a[i].x, act), activate(a[i].y, act));
+  for (int i = 0; i < 4; ++i) a[i] = make_float2(activate<QUICK>(a[i].x, act), activate<QUICK>(a[i].y, act));
 }
 // derivatives of the activation, from its values
 __device__ __forceinline__ void derive8(const float2 (&a)[4], int act, float2 (&da)[4]) {
@@ -421,13 +430,13 @@ __device__ __forceinline__ void derive8(const float2 (&a)[4], int act, float2 (&
   for (int i = 0; i < 4; ++i) da[i] = make_float2(activate_d(a[i].x, act), activate_d(a[i].y, act));
 }
 
-template <typename TX, typename TR, bool VEC>
+template <typename TX, typename TR, bool VEC, bool QUICK>
 __device__ __forceinline__ void load_gate(const BlockNormParams& p, int64_t grow, const Cols& cs, float2 (&a)[4]) {
   if (p.gate_res_type)
     unpack8(load8<TR, VEC>(static_cast<const TR*>(p.gate) + grow * p.ld_gate, cs), a);
   else
     unpack8(load8<TX, VEC>(static_cast<const TX*>(p.gate) + grow * p.ld_gate, cs), a);
-  activate8(a, p.act);
+  activate8<QUICK>(a, p.act);
 }
 
 // Parameters (zero past the row and where there are none), w + off; read once a block.
@@ -685,12 +694,12 @@ __global__ void __launch_bounds__(bn_max_threads(FEAT, VEC, CLUSTER), 1)
           ring.template get<TR>(batch, r, kG, a);
         else
           ring.template get<TX>(batch, r, kG, a);
-        activate8(a, p.act);
+        activate8<true>(a, p.act);
         set_gate(a);
       } else if (gate && row + r >= gate_end) {
         const int g = (row + r) / int(p.gate_group);
         float2 a[4];
-        load_gate<TX, TR, VEC>(p, g, cs, a);
+        load_gate<TX, TR, VEC, true>(p, g, cs, a);
         set_gate(a);
         gate_end = int((g + 1) * p.gate_group);
       }
@@ -999,7 +1008,7 @@ __global__ void __launch_bounds__(kBnThreads, 1)
   int slot = 0;
   auto enter = [&](int chunk) FLCE_INLINE {  // a chunk has one gate row
     if (gate && !gate_full && chunk < p.chunks) {
-      load_gate<TX, TR, VEC>(p, chunk / int(p.chunks_per_group), cs, a);
+      load_gate<TX, TR, VEC, false>(p, chunk / int(p.chunks_per_group), cs, a);
       if (OWN_A) set_own(kA, a);
     }
   };
@@ -1056,7 +1065,7 @@ __global__ void __launch_bounds__(kBnThreads, 1)
           ring.template get<TR>(batch, r, kG, a);
         else
           ring.template get<TX>(batch, r, kG, a);
-        activate8(a, p.act);
+        activate8<false>(a, p.act);
         if (p.dgate != nullptr) {  // d u scale act', u = (x - m) r w1 + b1, or x
           float2 e[4], da[4];
           derive8(a, p.act, da);
