@@ -226,11 +226,19 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
     const int l = i / p.pieces, k = s_beam[l];
     return s_base32[k] + stat[k * p.pieces + (i - l * p.pieces)].x;
   };
-  // Each thread's set: some of these, or where they are few, tokens.
+  // Each thread's set: some of these, or where they are few, tokens. Sets of neighbouring lanes are
+  // joined to about twice as many as candidates wanted: about 1.4 M random values reach the M-th
+  // largest of 2 M maxima. Each has pieces of every beam: a beam that is far ahead of the others has
+  // all the candidates, and with its pieces in a few sets the threshold would be another's
+  // (16 requests of 8 beams, 128256 random logits, scores of deviation 1: 1.2 ms).
   float best = -CUDART_INF_F, size = 0.f;
   const bool by_piece = all >= 4 * p.M;
+  const int values = by_piece ? all : p.V, active = values < kJoinThreads ? values : kJoinThreads;
+  int lanes = 1;
+  while (active / lanes >= 4 * p.M && lanes < 32) lanes *= 2;
+  const int sets = kJoinThreads / lanes, first_piece = tid % lanes * sets + tid / lanes;
   if (by_piece) {
-    for (int i = tid; i < all; i += kJoinThreads) best = fmaxf(best, piece_best(i));
+    for (int i = first_piece; i < all; i += kJoinThreads) best = fmaxf(best, piece_best(i));
   } else {
     if (tid < s_n_done) best = piece_best(live_pieces + tid);
     for (int l = 0; l < s_n_live; ++l) {
@@ -243,11 +251,6 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
   }
   for (int k = lane; k < p.K; k += 32)
     if (s_state[k] != BEAM_NONE) size = fmaxf(size, fabsf(s_base32[k]));
-  // Sets of neighbouring lanes are joined to about twice as many as candidates wanted: about 1.4 M
-  // random values reach the M-th largest of 2 M maxima.
-  const int values = by_piece ? all : p.V, active = values < kJoinThreads ? values : kJoinThreads;
-  int lanes = 1;
-  while (active / lanes >= 4 * p.M && lanes < 32) lanes *= 2;
   if (lanes == 1) s_set[tid] = best;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -256,7 +259,6 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
     if (lanes == 2 * o && tid % lanes == 0) s_set[tid / lanes] = best;
   }
   __syncthreads();
-  const int sets = kJoinThreads / lanes;
   if (tid < sets) {
     const float mine = s_set[tid];
     int above = 0;
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
     // leaves fewer than M tokens, say). With the threshold in 64 bits, those above it first.
     double top = -CUDART_INF;
     if (by_piece) {
-      for (int i = tid; i < all; i += kJoinThreads) {
+      for (int i = first_piece; i < all; i += kJoinThreads) {
         const int l = i / p.pieces, k = i < live_pieces ? s_beam[l] : s_beam[s_n_live + i - live_pieces];
         top = fmax(top, s_base[k] + (i < live_pieces ? double(stat[k * p.pieces + (i - l * p.pieces)].x) : 0.0));
       }

@@ -123,6 +123,16 @@ def test_masked_tokens(gpu_lib, dtype):
     check(z, s, 64)
 
 
+@pytest.mark.parametrize("B,K,V,M", [(16, 8, 128256, 8), (2, 16, 4000, 32), (3, 5, 8000, 64), (1, 32, 70001, 64)])
+def test_one_beam_far_ahead(gpu_lib, B, K, V, M):
+    """All candidates are one beam's, whichever it is."""
+    for ahead in (0, K // 2, K - 1):
+        z, s = make(B, K, V, "bf16", seed=ahead, std=1.0)
+        s[:, ahead] += 12.0
+        got = check(z, s, M)
+        assert bool((got[1] == ahead).all())
+
+
 def test_scores_below_the_range_still_fill(gpu_lib):
     """Masks of the lowest value on tokens and on a beam: sums that fp32 does not have come last."""
     low = torch.finfo(torch.float32).min
