@@ -29,6 +29,7 @@ namespace {
 constexpr int kBeamThreads = 256, kJoinThreads = 512;
 constexpr int kMaxBeams = 32, kMaxSelect = 64;
 constexpr int kListCap = 2048;   // candidates that are ranked against one another
+constexpr int kBorderList = 512;  // of them, where there are more, those that a threshold is taken from
 constexpr int kPiecesCap = 2048;  // pieces that may have some
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -138,8 +139,9 @@ enum BeamState : int { BEAM_LIVE = 0, BEAM_NONE = 1, BEAM_FINISHED = 2 };
 // it, from the few pieces whose maximum does; and their ranks among one another. The threshold
 // and the test against it are in 32 bits with a margin, the scores and the order in 64. All of it
 // is latency: 8 us for one request of four beams, 20 us for 16 beams of 256000 tokens and 32
-// candidates (512 threads; 33 us with 256). More equal or sorted logits than the list holds take the
-// slower ways at the end (8 rows of 128256 equal logits 0.3 ms, sorted ones 6 ms).
+// candidates (512 threads; 33 us with 256). More equal or sorted logits than the list holds take
+// some passes more over the pieces that have them (4 requests of 8 beams of 128256 equal ones: 95 us
+// with the pass over the logits).
 template <typename T, int NV>
 __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const SelectParams p) {
   constexpr int kWarps = kJoinThreads / 32;
@@ -306,71 +308,55 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
         if (wanted(base32 + v[e])) f(s_base[k] + double(v[e]), k, z.e0 + j * 256 + e);
     }
   };
+  // more candidates than the list holds: which ones it has does not matter then
+  auto full = [&]() { return *reinterpret_cast<volatile int*>(&s_count) > kListCap; };
   const int n_pieces = s_n_pieces;
-  if (n_pieces <= kPiecesCap)
-    for (int i = warp; i < n_pieces; i += kWarps) scan(s_pieces[i], add);
+  if (n_pieces <= kPiecesCap) {
+    for (int i = warp; i < n_pieces && !full(); i += kWarps) scan(s_pieces[i], add);
+  } else {
+    for (int i = warp; i < live_pieces && !full(); i += kWarps)
+      if (wanted(piece_best(i))) scan(i, add);
+  }
   __syncthreads();
-  const int count = s_count;
+  int count = s_count;
   const int64_t out = int64_t(b) * p.M;
   auto put = [&](int n, uint64_t score, uint64_t place) {
     p.out_scores[out + n] = float(unordered64(score));
     p.out_parents[out + n] = int32_t(place >> 32);
     p.out_tokens[out + n] = int32_t(uint32_t(place));
   };
-  // the best of the list's n candidates, by rank
-  auto rank = [&](int n) {
-    // four threads count those above a candidate, a quarter of the list each
-    const int part = tid % 4, quarter = (n + 3) / 4;
+  // f(i, those above it) for each of the list's n candidates
+  auto each_rank = [&](int n, auto&& f) {
+    // four threads count those above a candidate, every fourth of the list each
+    const int part = tid % 4;
     for (int i = tid / 4; i < (n + 7) / 8 * 8; i += kJoinThreads / 4) {  // whole warps: they shuffle
       const uint64_t score = i < n ? s_score[i] : ~uint64_t(0), place = i < n ? s_place[i] : 0;
-      const int end = (part + 1) * quarter < n ? (part + 1) * quarter : n;
       int above = 0;
 #pragma unroll 4
-      for (int j = part * quarter; j < end; ++j)
+      for (int j = part; j < n; j += 4)
         above += int(s_score[j] > score) + int(s_score[j] == score && s_place[j] < place);
       above += __shfl_xor_sync(0xffffffffu, above, 1);
       above += __shfl_xor_sync(0xffffffffu, above, 2);
-      if (part == 0 && i < n && above < p.M) put(above, score, place);
+      if (part == 0 && i < n) f(i, above);
     }
   };
-  const bool fits = n_pieces <= kPiecesCap && count <= kListCap;
-  int strictly = 0;
+  // Thousands reach the threshold (a mask of the type's lowest value that leaves few tokens, sorted or
+  // equal logits, a beam of few pieces far ahead). The M-th best of some in the list, whichever these
+  // are, is a threshold too; those above it are listed, until they fit. At least the others that
+  // it was taken from are not above it, so this ends.
+  bool border_set = false;
   double border = 0.0;
-  if (fits) {
-    rank(count);
-  } else {
-    // Thousands reach the threshold, most of them equal (a mask of the type's lowest value that
-    // leaves fewer than M tokens, say). With the threshold in 64 bits, those above it first.
-    double top = -CUDART_INF;
-    if (by_piece) {
-      for (int i = first_piece; i < all; i += kJoinThreads) {
-        const int l = i / p.pieces, k = i < live_pieces ? s_beam[l] : s_beam[s_n_live + i - live_pieces];
-        top = fmax(top, s_base[k] + (i < live_pieces ? double(stat[k * p.pieces + (i - l * p.pieces)].x) : 0.0));
-      }
-    } else {
-      if (tid < s_n_done) top = s_base[s_beam[s_n_live + tid]];
-      for (int l = 0; l < s_n_live; ++l) {
-        const int k = s_beam[l];
-        const T* z = row_of<T>(p, b, k);
-        for (int v = tid; v < p.V; v += kJoinThreads) top = fmax(top, s_base[k] + double(to_f32(z[v])));
-      }
-    }
-    for (int o = 1; o < lanes; o <<= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-    __syncthreads();  // the list is used again
-    double* set64 = reinterpret_cast<double*>(s_score);
-    if (tid % lanes == 0) set64[tid / lanes] = top;
-    if (tid == 0) s_count = 0;
-    __syncthreads();
-    if (tid < sets) {
-      const double mine = set64[tid];
-      int above = 0;
-      for (int j = 0; j < sets; ++j) above += int(set64[j] > mine || (set64[j] == mine && j < tid));
-      if (above == p.M - 1) s_border = mine;
-    }
+  while (count > kListCap) {
+    each_rank(kBorderList, [&](int i, int above) {
+      if (above == p.M - 1) s_border = unordered64(s_score[i]);
+    });
     __syncthreads();
     border = s_border;
+    border_set = true;
+    if (tid == 0) s_count = 0;
+    __syncthreads();
     if (tid < p.K && s_state[tid] == BEAM_FINISHED && s_base[tid] > border) add(s_base[tid], tid, p.pad_token);
-    for (int i = warp; i < live_pieces; i += kWarps) {
+    for (int i = warp; i < live_pieces && !full(); i += kWarps) {
       const int l = i / p.pieces, k = s_beam[l];
       if (s_base[k] + double(stat[k * p.pieces + (i - l * p.pieces)].x) <= border) continue;
       scan(i, [&](double score, int beam, int token) {
@@ -378,13 +364,15 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
       });
     }
     __syncthreads();
-    strictly = s_count;
-    if (strictly <= kListCap) rank(strictly);
+    count = s_count;
   }
-  if (!fits && strictly <= kListCap) {
-    // then as many at the threshold as are wanted, lowest index first
-    if (warp != 0) return;
-    int have = strictly;
+  each_rank(count, [&](int i, int above) {
+    if (above < p.M) put(above, s_score[i], s_place[i]);
+  });
+  if (warp != 0 || count >= p.M) return;
+  int have = count;
+  if (border_set) {
+    // as many at the threshold as are wanted, lowest index first
     auto take = [&](uint32_t mine, int k, int token) {  // bits of a lane's eight tokens from `token` on
       int before = __popc(mine), total = before;
 #pragma unroll
@@ -424,42 +412,9 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
     }
     return;
   }
-  if (!fits) {
-    // Thousands of different ones, all in a few places (sorted logits): the M best one after the other.
-    uint64_t last_score = ~uint64_t(0), last_place = 0;
-    for (int n = 0; n < p.M; ++n) {
-      uint64_t score = 0, place = ~uint64_t(0);
-      auto offer = [&](double v, int k, int token) {
-        const uint64_t s = ordered64(v), at = uint64_t(k) << 32 | uint32_t(token);
-        if (s > last_score || (s == last_score && at <= last_place)) return;
-        if (s > score || (s == score && at < place)) score = s, place = at;
-      };
-      if (tid < p.K && s_state[tid] == BEAM_FINISHED) offer(s_base[tid], tid, p.pad_token);
-      for (int i = warp; i < live_pieces; i += kWarps)
-        if (wanted(piece_best(i))) scan(i, offer);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t s = __shfl_xor_sync(0xffffffffu, score, o), at = __shfl_xor_sync(0xffffffffu, place, o);
-        if (s > score || (s == score && at < place)) score = s, place = at;
-      }
-      __syncthreads();
-      if (lane == 0) {
-        s_score[warp] = score;
-        s_place[warp] = place;
-      }
-      __syncthreads();
-      for (int w = 0; w < kWarps; ++w)
-        if (s_score[w] > score || (s_score[w] == score && s_place[w] < place)) score = s_score[w], place = s_place[w];
-      if (tid == 0) put(n, score, place);
-      last_score = score;
-      last_place = place;
-    }
-  }
   // What is no candidate fills the rest, lowest index first: all tokens of a beam without any, all but
   // the padding of a finished one, the masked ones of a live one (with scores of -inf, or, under
   // two masks of the type's lowest value, of less than fp32 has).
-  if (warp != 0 || !fits || count >= p.M) return;
-  int have = count;
   for (int k = 0; k < p.K && have < p.M; ++k) {
     const T* z = row_of<T>(p, b, k);
     for (int v0 = 0; v0 < p.V && have < p.M; v0 += 32) {
