@@ -424,7 +424,9 @@ flce_status flce_clip_grad_norm(const flce_grad_tensor* tensors, int64_t count, 
  * strides ld_batch and ld_beam, unit stride along V. A beam with finished[b, k] != 0 (NULL:
  * none) has the one candidate (pad_token, scores[b, k]). A beam whose score or lse is not
  * finite has none. What is no candidate has a score of -inf and comes last, lowest index
- * first. Scores are compared in 64 bits. K <= 32, M <= 64, B K <= 65535. */
+ * first. Scores are formed as (logit - row maximum) + (score - log of the sum of exponentials), so that
+ * a row whose logits are all one value, the type's lowest for example, is uniform, and compared in 64
+ * bits. K <= 32, M <= 64, B K <= 65535. */
 size_t flce_beam_select_workspace_size(int64_t B, int64_t K, int64_t V, int64_t M);
 
 flce_status flce_beam_select(const void* logits, int32_t dtype, int64_t B, int64_t K, int64_t V, int64_t ld_batch,

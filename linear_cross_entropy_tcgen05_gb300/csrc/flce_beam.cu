@@ -2,7 +2,9 @@
 // the reordering of the states that go with the beams.
 //
 // Selection: s[b, k, v] = score[b, k] + z[b, k, v] - lse_v z[b, k, :], the M best of K V, the
-// lowest flat index first where they are equal. Bound by reading the logits once, so that pass
+// lowest flat index first where they are equal. With m the row's maximum and S = sum exp(z - m) it is
+// formed as (z - m) + (score - log S): m + log S would lose log S, and the score with it, in a row whose
+// logits are all masked with the type's lowest value (or near any other large one). Bound by reading the logits once, so that pass
 // selects nothing: it leaves the maximum and the sum of exponentials of every piece of a row. One
 // block a request then finds from the maxima a threshold that M candidates reach, and looks for
 // them in the few pieces that can have any (from L2). The order between beams depends on their
@@ -147,8 +149,8 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
   constexpr int kWarps = kJoinThreads / 32;
   __shared__ float s_part_max[kMaxBeams];  // at least as many as warps
   __shared__ double s_part_sum[kMaxBeams];
-  __shared__ double s_base[kMaxBeams];  // score - lse, or a finished beam's score
-  __shared__ float s_base32[kMaxBeams];
+  __shared__ double s_base[kMaxBeams];  // score - log S, or a finished beam's score
+  __shared__ float s_base32[kMaxBeams], s_top[kMaxBeams];  // and the row's maximum
   __shared__ int s_state[kMaxBeams], s_beam[kMaxBeams], s_n_live, s_n_done;
   __shared__ __align__(16) float s_set[kJoinThreads];
   __shared__ float s_least;
@@ -198,9 +200,10 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
           const float x = s_part_max[k * per_beam + w];
           sum += x == -CUDART_INF_F ? s_part_sum[k * per_beam + w] : s_part_sum[k * per_beam + w] * double(ex2((x - m) * kLog2e));
         }
-        const double lse = double(m) + log(sum);
-        base -= lse;
-        if (isfinite(score) && isfinite(lse)) state = BEAM_LIVE;
+        const double log_sum = log(sum);
+        base -= log_sum;
+        s_top[k] = m;
+        if (isfinite(score) && isfinite(m) && isfinite(log_sum)) state = BEAM_LIVE;
       } else if (isfinite(score)) {
         state = BEAM_FINISHED;
       }
@@ -220,13 +223,16 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
   }
   if (tid == 0) s_n_pieces = s_count = 0;
   __syncthreads();
+  // a live beam's candidate of logit z
+  auto value32 = [&](int k, float z) { return s_base32[k] + (z - s_top[k]); };
+  auto value64 = [&](int k, float z) { return s_base[k] + (double(z) - double(s_top[k])); };
   // What the maxima are known of: the live beams' pieces, then the finished beams. (Beams without a
   // candidate are not among them: at a request's first step all but one are.)
   const int live_pieces = s_n_live * p.pieces, all = live_pieces + s_n_done;
   auto piece_best = [&](int i) {
     if (i >= live_pieces) return s_base32[s_beam[s_n_live + i - live_pieces]];
     const int l = i / p.pieces, k = s_beam[l];
-    return s_base32[k] + stat[k * p.pieces + (i - l * p.pieces)].x;
+    return value32(k, stat[k * p.pieces + (i - l * p.pieces)].x);
   };
   // Each thread's set: some of these, or where they are few, tokens. Sets of neighbouring lanes are
   // joined to about twice as many as candidates wanted: about 1.4 M random values reach the M-th
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
       const T* z = row_of<T>(p, b, k);
       float m = -CUDART_INF_F;
       for (int v = tid; v < p.V; v += kJoinThreads) m = fmaxf(m, to_f32(z[v]));
-      best = fmaxf(best, s_base32[k] + m);
+      best = fmaxf(best, value32(k, m));
     }
   }
   for (int k = lane; k < p.K; k += 32)
@@ -271,7 +277,8 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
                int(q.z > mine || (q.z == mine && j + 2 < tid)) + int(q.w > mine || (q.w == mine && j + 3 < tid));
     }
     if (above == p.M - 1) {
-      // base, logit and their sum are rounded once each: 4 steps of the largest of them are ample
+      // base, difference and their sum are rounded once each, and the difference is at most the sum
+      // and the base: 16 steps of these are ample
       const float v = mine - 16.f * 0x1p-24f * (fabsf(mine) + 2.f * size);
       s_least = v == v ? v : -CUDART_INF_F;
     }
@@ -296,7 +303,6 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
   // every candidate of a piece that is wanted, to f(score, beam, token); by one warp
   auto scan = [&](int i, auto&& f) {
     const int l = i / p.pieces, k = s_beam[l];
-    const float base32 = s_base32[k];
     Piece<T, NV> z;
     z.load(row_of<T>(p, b, k), p.V, i - l * p.pieces, lane);
 #pragma unroll
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
       unpack8(z.raw[j], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (wanted(base32 + v[e])) f(s_base[k] + double(v[e]), k, z.e0 + j * 256 + e);
+        if (wanted(value32(k, v[e]))) f(value64(k, v[e]), k, z.e0 + j * 256 + e);
     }
   };
   // more candidates than the list holds: which ones it has does not matter then
@@ -358,7 +364,7 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
     if (tid < p.K && s_state[tid] == BEAM_FINISHED && s_base[tid] > border) add(s_base[tid], tid, p.pad_token);
     for (int i = warp; i < live_pieces && !full(); i += kWarps) {
       const int l = i / p.pieces, k = s_beam[l];
-      if (s_base[k] + double(stat[k * p.pieces + (i - l * p.pieces)].x) <= border) continue;
+      if (value64(k, stat[k * p.pieces + (i - l * p.pieces)].x) <= border) continue;
       scan(i, [&](double score, int beam, int token) {
         if (score > border) add(score, beam, token);
       });
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
       if (s_state[k] != BEAM_LIVE) continue;
       for (int p0 = 0; p0 < p.pieces && have < p.M; p0 += 32) {
         const int piece = p0 + lane;
-        const bool has = piece < p.pieces && s_base[k] + double(stat[k * p.pieces + piece].x) >= border;
+        const bool has = piece < p.pieces && value64(k, stat[k * p.pieces + piece].x) >= border;
         for (uint32_t todo = __ballot_sync(0xffffffffu, has); todo != 0 && have < p.M; todo &= todo - 1) {
           Piece<T, NV> z;
           z.load(row_of<T>(p, b, k), p.V, p0 + __ffs(int(todo)) - 1, lane);
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
             uint32_t mine = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (v[e] > -CUDART_INF_F && s_base[k] + double(v[e]) == border) mine |= 1u << e;
+              if (v[e] > -CUDART_INF_F && value64(k, v[e]) == border) mine |= 1u << e;
             take(mine, k, z.e0 + j * 256);
           }
         }
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(kJoinThreads) flce_beam_join_kernel(const Sele
       const int v = v0 + lane;
       bool none = v < p.V;
       if (none && s_state[k] == BEAM_FINISHED) none = v != p.pad_token;
-      if (none && s_state[k] == BEAM_LIVE) none = !(s_base32[k] + to_f32(z[v]) > -CUDART_INF_F);
+      if (none && s_state[k] == BEAM_LIVE) none = !(value32(k, to_f32(z[v])) > -CUDART_INF_F);
       const uint32_t who = __ballot_sync(0xffffffffu, none);
       const int n = have + __popc(who & ((1u << lane) - 1));
       if (none && n < p.M) put(n, ordered64(-CUDART_INF), uint64_t(k) << 32 | uint32_t(v));
