@@ -426,7 +426,10 @@ flce_status flce_clip_grad_norm(const flce_grad_tensor* tensors, int64_t count, 
  * finite has none. What is no candidate has a score of -inf and comes last, lowest index
  * first. Scores are formed as (logit - row maximum) + (score - log of the sum of exponentials), so that
  * a row whose logits are all one value, the type's lowest for example, is uniform, and compared in 64
- * bits. K <= 32, M <= 64, B K <= 65535. */
+ * bits. The exponentials are in 32 bits (added in 64 from some hundreds on), so a beam's log of their sum is
+ * right to about 1e-7: candidates of different beams that are nearer than that may change places. Rows
+ * that are equal bit for bit have equal sums, wherever they are in memory, so that equal beams are exact
+ * ties. K <= 32, M <= 64, B K <= 65535. */
 size_t flce_beam_select_workspace_size(int64_t B, int64_t K, int64_t V, int64_t M);
 
 flce_status flce_beam_select(const void* logits, int32_t dtype, int64_t B, int64_t K, int64_t V, int64_t ld_batch,

@@ -75,7 +75,8 @@ def beam_select(logits, scores, num: int | None = None, finished=None, pad_token
 
     ``logits`` [B, K, V] (bf16, f16 or f32, unit stride along V) and the beams' ``scores`` [B, K]
     (float32, sums of log-probabilities) give every candidate ``scores[b, k] + log_softmax(logits[b,
-    k])[v]``; of equal ones the lowest ``k * V + v`` comes first. A beam marked in ``finished`` [B,
+    k])[v]``; of equal ones the lowest ``k * V + v`` comes first (equal rows at equal scores are exact ties; the
+    log of a row's sum of exponentials is right to about 1e-7). A beam marked in ``finished`` [B,
     K] (bool) goes on with ``pad_token`` alone, at its score. Masked tokens have a logit of -inf and
     so a score of -inf; a beam whose score or logsumexp is not finite (all tokens masked, a NaN) has
     no candidate. Candidates at -inf are returned, lowest index first, only where there are no

@@ -64,25 +64,93 @@ struct SelectParams {
   int32_t *out_parents, *out_tokens;
 };
 
-// A lane's vectors of a piece: NV of eight logits, 256 apart, from the row's last vector boundary in
-// memory before its first logit; -inf outside the row.
+// A lane's vectors of a piece: NV of eight logits, 256 apart; -inf past the row. Pieces and vectors are
+// counted from the row's first logit wherever it is in memory, so that equal rows have equal sums to
+// the last bit, and equal beams exact ties.
 template <typename T, int NV> struct Piece {
+  static constexpr int kPer = 16 / sizeof(T), kParts = 8 / kPer;  // logits of 16 bytes, and those of a vector
   Raw8<T> raw[NV];
   int e0;  // the first logit of the lane's first vector
-  __device__ __forceinline__ void load(const T* z, int V, int piece, int lane) {
-    const int mis = int((reinterpret_cast<uintptr_t>(z) & uintptr_t(8 * sizeof(T) - 1)) / sizeof(T));
-    e0 = piece * 256 * NV - mis + lane * 8;
+  // Whether 16-byte loads of the row are aligned from its first logit on.
+  __device__ __forceinline__ static bool aligned(const T* z) {
+    return (reinterpret_cast<uintptr_t>(z) & uintptr_t(8 * sizeof(T) - 1)) == 0;
+  }
+  __device__ __forceinline__ void load_aligned(const T* z, int V) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e = e0 + j * 256;
-      if (e >= 0 && e + 8 <= V) {
+      if (e + 8 <= V)
         raw[j] = raw_load(z + e);
-      } else {
+      else
+        load_each(z, V, j);
+    }
+  }
+  __device__ __forceinline__ void load_each(const T* z, int V, int j) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = e0 + j * 256 + i < V ? to_f32(z[e0 + j * 256 + i]) : -CUDART_INF_F;
+    raw[j] = pack8<T>(f);
+  }
+  // For a few pieces.
+  __device__ __forceinline__ void load(const T* z, int V, int piece, int lane) {
+    e0 = piece * 256 * NV + lane * 8;
+    if (aligned(z)) {
+      load_aligned(z, V);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) load_each(z, V, j);
+    }
+  }
+  // For all pieces of a row, by whole warps. The vectors of an unaligned row are shifted out of the
+  // aligned pieces of 16 bytes around them: a lane loads those that its first logits are in and has the
+  // last from the next lane, the last lane from the first one's next vector. (512 x 4 rows of 50257 bf16
+  // logits, with the join: 72 us; 62 with pieces that begin where memory's vectors do, whose sums
+  // differed in their last bits between equal rows, and so put equal beams in any order; 109 with bounds
+  // checked load by load.)
+  __device__ __forceinline__ void load_all(const T* z, int V, int piece, int lane) {
+    e0 = piece * 256 * NV + lane * 8;
+    if (aligned(z)) return load_aligned(z, V);
+    const int bytes = int(reinterpret_cast<uintptr_t>(z) & 15), ahead = bytes / int(sizeof(T));
+    uint4 v[NV * kParts + 1];
+    const T* at = z + e0 - ahead;
+    if (piece > 0 && (piece + 1) * 256 * NV + kPer <= V) {
+#pragma unroll
+      for (int i = 0; i < NV * kParts; ++i) v[i] = *reinterpret_cast<const uint4*>(at + i / kParts * 256 + i % kParts * kPer);
+      v[NV * kParts] = lane == 0 ? *reinterpret_cast<const uint4*>(at + NV * 256) : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+#pragma unroll
+      for (int i = 0; i <= NV * kParts; ++i) {
+        const int e = e0 - ahead + i / kParts * 256 + i % kParts * kPer;
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = e + i >= 0 && e + i < V ? to_f32(z[e + i]) : -CUDART_INF_F;
-        raw[j] = pack8<T>(f);
+        for (int k = 0; k < 8; ++k) f[k] = k < kPer && e + k >= 0 && e + k < V ? to_f32(z[e + k]) : -CUDART_INF_F;
+        v[i] = pack8<T>(f).v[0];
       }
+    }
+    switch (bytes / 4) {
+      case 0: shift<0>(v, lane, bytes & 2); break;
+      case 1: shift<1>(v, lane, bytes & 2); break;
+      case 2: shift<2>(v, lane, bytes & 2); break;
+      default: shift<3>(v, lane, bytes & 2); break;
+    }
+  }
+  template <int BY> __device__ __forceinline__ void shift(const uint4 (&v)[NV * kParts + 1], int lane, int half) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const uint4 &own = v[j * kParts], &next = v[(j + 1) * kParts];
+      const uint32_t give[4] = {lane == 0 ? next.x : own.x, lane == 0 ? next.y : own.y, lane == 0 ? next.z : own.z,
+                                lane == 0 ? next.w : own.w};
+      uint32_t w[4 * kParts + 4], q[4 * kParts];
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        const uint4& p = v[j * kParts + i];
+        w[4 * i] = p.x, w[4 * i + 1] = p.y, w[4 * i + 2] = p.z, w[4 * i + 3] = p.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[4 * kParts + i] = i <= BY ? __shfl_sync(0xffffffffu, give[i], (lane + 1) % 32) : 0u;
+      words_from<BY, T>(w, half, q);
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) raw[j].v[i] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
     }
   }
 };
@@ -103,7 +171,7 @@ __global__ void __launch_bounds__(kBeamThreads) flce_beam_rows_kernel(const Sele
   if (p.finished != nullptr && p.finished[row]) return;  // its only candidate needs no logits
   const int b = row / p.K;
   Piece<T, NV> z;
-  z.load(row_of<T>(p, b, row - b * p.K), p.V, piece, lane);
+  z.load_all(row_of<T>(p, b, row - b * p.K), p.V, piece, lane);
   float m = -CUDART_INF_F;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -446,7 +514,7 @@ int pick_vectors(int64_t rows, int64_t V) {
 
 int64_t select_pieces(int64_t rows, int64_t V) {
   const int64_t piece = 256 * pick_vectors(rows, V);
-  return (V + 7 + piece - 1) / piece;  // a misaligned row starts up to seven logits into its first vector
+  return (V + piece - 1) / piece;
 }
 
 template <typename T, int NV> cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {

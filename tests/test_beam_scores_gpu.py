@@ -55,3 +55,23 @@ def test_rows_with_few_tokens_left(gpu_lib, dtype):
         index = parents.long() * V + tokens.long()
         assert bool(((c.view(3, -1).gather(1, index) - best[:, :M]).abs()[fine] <= 2.0 ** -20).all())
         assert torch.equal(index[~fine], at[:, :M][~fine])  # what is no candidate, lowest index first
+
+
+@pytest.mark.parametrize("dtype", list(T))
+@pytest.mark.parametrize("V", [7, 1003, 4099, 50257, 128256 + 5])
+def test_beams_that_are_alike_come_in_order(gpu_lib, dtype, V):
+    """Equal rows at equal scores are exact ties, wherever their rows start in memory: the lower
+    beam first."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    for trial in range(4):
+        B, K, M = 2, 5, 9
+        row = torch.empty(B, 1, V, device=DEV).normal_(0, 2.5, generator=g).to(T[dtype])
+        z, s = row.expand(B, K, V).contiguous(), torch.full((B, K), -3.25, device=DEV)
+        want = torch.sort(z.double().view(B, -1), dim=1, descending=True, stable=True)[1][:, :M]
+        for left in (0, 1, 6):
+            room = torch.zeros(B, K, V + 11, dtype=T[dtype], device=DEV)
+            room[..., left:left + V] = z
+            scores, parents, tokens = flce.beam_select(room[..., left:left + V], s, M)
+            assert torch.equal(parents.long(), want // V) and torch.equal(tokens.long(), want % V)
+            # and the scores do not depend on the layout either
+            assert torch.equal(scores, flce.beam_select(z, s, M)[0])
