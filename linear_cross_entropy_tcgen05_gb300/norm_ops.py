@@ -8,6 +8,7 @@ import ctypes
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 __all__ = ["block_norm", "BlockNormFunction", "BlockNorm", "FlceBlockNormDesc", "FlceBlockNormGrads",
            "flce_block_norm_forward", "flce_block_norm_backward", "flce_block_norm_workspace_size", "DTYPES", "NORMS",
@@ -262,15 +263,23 @@ def block_norm(x, residual=None, weight=None, *, bias=None, post_weight=None, po
     ``gate_activation`` ("none", "sigmoid", "tanh"). ``norm`` is "rms" or "layer"; weights are
     used as ``weight + weight_offset``. D is at most 16384.
 
-    Differentiable in every tensor; a gradient has its input's type. With a 16-bit residual
+    Differentiable in every tensor (by backward passes; forward-mode inputs raise); a gradient has its
+    input's type. With a 16-bit residual
     stream the backward pass reads the rounded h.
     """
     args = (x, residual, weight, bias, post_weight, post_bias, gate)
-    if torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in args]):
+    if torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in args]) or _forward_mode(args):
         return BlockNormFunction.apply(*args, norm, eps, scale, gate_activation, weight_offset)
     desc = _describe(*args, norm, eps, scale, gate_activation, weight_offset)
     h, y, _ = _forward(desc, x, x.dtype if residual is None else residual.dtype, weight is not None, False)
     return h, y
+
+
+def _forward_mode(args) -> bool:
+    """Whether a tensor has a forward-mode tangent. BlockNormFunction refuses it; a call that does not go
+    through autograd would lose it."""
+    return forward_ad._current_level >= 0 and any([t is not None and forward_ad.unpack_dual(t).tangent is not None
+                                                   for t in args])
 
 
 class BlockNorm(torch.nn.Module):
