@@ -38,3 +38,15 @@ def test_vmap_is_refused(gpu_lib):
     t = make(6, 64)
     with pytest.raises((RuntimeError, NotImplementedError)):
         torch.vmap(lambda x: flce.block_norm(x, None, t["weight"]))(t["x"].unsqueeze(0))
+
+
+def test_tracing_is_refused(gpu_lib):
+    """A trace would keep empty outputs that nothing fills."""
+    t = make(6, 64)
+    z, s = torch.randn(1, 2, 50, device=DEV), torch.zeros(1, 2, device=DEV)
+    parents = torch.zeros(1, 2, dtype=torch.int32, device=DEV)
+    for f, args in [(lambda x: flce.block_norm(x, None, t["weight"])[1], (t["x"],)), (lambda v: flce.beam_select(v, s)[0], (z,)),
+                    (lambda v: flce.beam_reorder([v], parents)[0], (torch.zeros(2, 3, device=DEV),)),
+                    (lambda v: flce.clip_grad_norm([v], 1.0), (torch.ones(3, device=DEV),))]:
+        with pytest.raises(RuntimeError, match="traced"):
+            torch.jit.trace(f, args, check_trace=False)
