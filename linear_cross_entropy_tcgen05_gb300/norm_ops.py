@@ -90,6 +90,14 @@ def _rows(t, D: int, name: str):
     raise ValueError(f"{name} must have unit stride along its last dimension and one stride between its rows")
 
 
+def _has_rows(t, D: int) -> bool:
+    """Whether the kernels can read t as it is."""
+    try:
+        return _row_stride(_rows(t if t.dim() > 1 else t.unsqueeze(0), D, "")) >= D
+    except ValueError:
+        return False
+
+
 def _gate_rows(gate, x) -> int:
     """Rows of the gate: it is shared by all rows ([D]), by equal runs of rows ([G, D], or x's
     shape with ones between the leading dimensions and the last), or has one for each."""
@@ -208,10 +216,13 @@ class BlockNormFunction(torch.autograd.Function):
     def backward(ctx, dh, dy):
         if dh is None and dy is None:
             return (None,) * 12
+        # a saved-tensor hook may have brought them back elsewhere or with other strides: described anew
+        # (the residual may be gone, h stands in for its type), and copied where the kernels need it
         x, weight, bias, post_weight, post_bias, gate, h, stats = ctx.saved_tensors
         want, dev, D = ctx.needs_input_grad, x.device, x.shape[-1]
-        # described anew: the residual may be gone (h stands in for its type), and a saved-tensor hook
-        # may have brought the others back elsewhere or with other strides
+        x, gate = (t if t is None or t.is_contiguous() or _has_rows(t, D) else t.contiguous() for t in (x, gate))
+        weight, bias, post_weight, post_bias, h, stats = (t if t is None else t.contiguous() for t in (
+            weight, bias, post_weight, post_bias, h, stats))
         words, N, gate_rows = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
         out = [None] * 12
         at = [0] * 7

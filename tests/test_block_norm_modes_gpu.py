@@ -50,3 +50,23 @@ def test_tracing_is_refused(gpu_lib):
                     (lambda v: flce.clip_grad_norm([v], 1.0), (torch.ones(3, device=DEV),))]:
         with pytest.raises(RuntimeError, match="traced"):
             torch.jit.trace(f, args, check_trace=False)
+
+
+@pytest.mark.parametrize("r", [torch.bfloat16, torch.float32])
+def test_saved_tensors_with_other_strides(gpu_lib, r):
+    """Saved-tensor hooks that give back the same values in wider rows, parameters among them."""
+    t = make(6, 512, r=r)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    up = [torch.empty(6, 512, device=DEV, dtype=d).normal_(generator=g) for d in (r, torch.bfloat16)]
+    leaves = [v.requires_grad_() for v in t.values()]
+    want = torch.autograd.grad(call(t), leaves, up)
+
+    def wide(s):
+        room = torch.full((*s.shape, 2) if s.dim() == 1 else (s.shape[0], 2 * s.shape[1]), 7.0, dtype=s.dtype, device=DEV)
+        view = room[:, 0] if s.dim() == 1 else room[:, :s.shape[1]]
+        return view.copy_(s.detach())
+
+    with torch.autograd.graph.saved_tensors_hooks(lambda s: s, wide):
+        out = call(t)
+    got = torch.autograd.grad(out, leaves, up)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
