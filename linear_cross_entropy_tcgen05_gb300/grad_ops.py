@@ -8,6 +8,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd.graph import increment_version
 
 __all__ = ["clip_grad_norm", "clip_grad_norm_", "grad_norm", "flce_clip_grad_norm", "flce_clip_grad_norm_workspace_size"]
 
@@ -92,6 +93,8 @@ def _run(grads, max_norm, norm_type, eps, grad_scale, out):
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _call_on(dev, "flce_clip_grad_norm", lib.flce_clip_grad_norm, table.buffer_info()[0], len(grads), max_norm, norm_type,
              eps, grad_scale, total.data_ptr(), ws.data_ptr(), need)
+    if out is not None:
+        increment_version(out)  # a backward pass that saved one of them is refused
     return total
 
 
@@ -105,7 +108,7 @@ def clip_grad_norm(grads, max_norm: float, norm_type: float = 2.0, eps: float = 
     gradients' shapes that get the result, of any of the three types (None: in place). The
     sum of squares is held in 64 bits and does not overflow or underflow where the norm does not. As in
     torch, a NaN norm makes every gradient NaN, and an infinite one makes them 0 or NaN. A
-    tensor may not be listed twice.
+    tensor may not be listed twice. Runs as under ``no_grad``: the norm and the results carry no gradient.
     """
     grads = list(grads)
     if out is not None and len(out) != len(grads):
@@ -124,7 +127,7 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0, eps: fl
 
 
 def grad_norm(grads, norm_type: float = 2.0, grad_scale: float = 1.0):
-    """The norm of all ``grads`` together, which stay as they are."""
+    """The norm of all ``grads`` together, which stay as they are. It carries no gradient."""
     grads = list(grads)
     if not grads:
         return torch.zeros((), dtype=torch.float32)
