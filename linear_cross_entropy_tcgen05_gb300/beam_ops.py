@@ -8,6 +8,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd.graph import increment_version
 
 __all__ = ["beam_select", "beam_reorder", "flce_beam_select", "flce_beam_select_workspace_size", "flce_beam_reorder",
            "FlceBeamState"]
@@ -81,7 +82,7 @@ def beam_select(logits, scores, num: int | None = None, finished=None, pad_token
     so a score of -inf; a beam whose score or logsumexp is not finite (all tokens masked, a NaN) has
     no candidate. Candidates at -inf are returned, lowest index first, only where there are no
     others. Unused beams (all but the first at the first step) have a score of -inf. K is at most
-    32, num 64.
+    32, num 64. The scores carry no gradient.
     """
     if logits.dtype not in DTYPES:
         raise TypeError(f"logits must be bfloat16, float16 or float32, got {logits.dtype}")
@@ -152,7 +153,8 @@ def beam_reorder(states, parents, dims=0, out=None):
 
     States have any type and any strides that leave at most four outer dimensions: a cache's
     first ``length`` positions are reordered alone as ``cache[:, :, :length]``. A parent
-    outside [0, K) leaves the beam what it was. K is at most 32.
+    outside [0, K) leaves the beam what it was. K is at most 32. Not differentiable: what is written may not
+    require a gradient (but under ``no_grad``).
     """
     states = list(states)
     dst = states if out is None else list(out)
@@ -179,8 +181,12 @@ def beam_reorder(states, parents, dims=0, out=None):
             raise ValueError("an expanded tensor cannot be reordered into")
         if s.numel():
             table += _state(s, d, dim % s.dim())
+    if torch.is_grad_enabled() and any([d.requires_grad for d in dst]):
+        raise RuntimeError("a tensor that requires a gradient cannot be reordered into: its gradient would not know of the "
+                           "new order. Decode under torch.no_grad(), or detach the states")
     if table:
         words = array.array("q", table)
         _call_on(dev, "flce_beam_reorder", load_library().flce_beam_reorder, words.buffer_info()[0], len(words) // 17,
                  parents.data_ptr(), parents.stride(0) if B > 1 else K, B, K)
+        increment_version(dst)  # a backward pass that saved one of them is refused
     return dst

@@ -42,3 +42,34 @@ def test_clipped_parameters(gpu_lib):
     flce.clip_grad_norm_([p], 0.1)
     with pytest.raises(RuntimeError, match="inplace"):
         end.backward()
+
+
+def test_reordered_states(gpu_lib):
+    parents = torch.tensor([[1, 0, 2], [2, 2, 1]], dtype=torch.int32, device=DEV)
+    leaf, mid, end = saved(6)
+    with torch.no_grad():
+        flce.beam_reorder([mid], parents)
+    with pytest.raises(RuntimeError, match="inplace"):
+        end.backward()
+    leaf, mid, end = saved(6)
+    flce.beam_reorder([torch.zeros(6, 5, device=DEV)], parents, out=[mid.detach()])
+    with pytest.raises(RuntimeError, match="inplace"):
+        end.backward()
+    leaf, mid, end = saved(6)
+    out = flce.beam_reorder([mid], parents, out=[torch.empty(6, 5, device=DEV)])[0]  # what is only read
+    end.backward()
+    assert torch.equal(leaf.grad, 8 * leaf.detach()) and not out.requires_grad
+    with torch.inference_mode():
+        s = torch.arange(6.0, device=DEV)[:, None]
+        assert flce.beam_reorder([s], parents)[0].flatten().tolist() == [1, 0, 2, 5, 5, 4]
+
+
+def test_reordering_what_needs_a_gradient_is_refused(gpu_lib):
+    """Its gradient would not know of the new order."""
+    parents = torch.tensor([[1, 0, 2], [2, 2, 1]], dtype=torch.int32, device=DEV)
+    leaf, mid, _ = saved(6)
+    before = mid.detach().clone()
+    for states, out in (([mid], None), ([leaf], None), ([torch.zeros(6, 5, device=DEV)], [mid])):
+        with pytest.raises(RuntimeError, match="no_grad"):
+            flce.beam_reorder(states, parents, out=out)
+    assert torch.equal(mid, before)
