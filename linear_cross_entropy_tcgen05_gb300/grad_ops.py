@@ -4,6 +4,7 @@ tensors, ``clip_grad_norm_`` parameters; ``flce_clip_grad_norm`` marshals to the
 from __future__ import annotations
 
 import array
+import collections
 import ctypes
 import math
 
@@ -59,6 +60,18 @@ def _dense(t) -> bool:
     return True
 
 
+def _check_written(words) -> None:
+    """Refuses a table in which an entry writes what another one reads or writes."""
+    read, write = words[0::4], [o for o, n in zip(words[1::4], words[2::4]) if n]
+    if len(set(write)) != len(write):
+        raise ValueError("a tensor may not be listed twice")
+    if read != words[1::4]:
+        readers = collections.Counter(g for g, n in zip(read, words[2::4]) if n)
+        for g, o, n in zip(read, words[1::4], words[2::4]):
+            if n and readers[o] != (g == o):
+                raise ValueError("a tensor of out may not be another entry's gradient")
+
+
 def _run(grads, max_norm, norm_type, eps, grad_scale, out):
     first = grads[0]
     dev = first.device
@@ -87,6 +100,8 @@ def _run(grads, max_norm, norm_type, eps, grad_scale, out):
                                                          (g.is_contiguous() and o.is_contiguous())):
                 raise ValueError("out must have the gradients' shapes, strides and device")
             words += (p, o.data_ptr(), g.numel(), dt | odt << 32)
+    if out is not None:
+        _check_written(words)
     lib, table = load_library(), _table(words)
     total = torch.empty((), dtype=torch.float32, device=dev)
     need = lib.flce_clip_grad_norm_workspace_size(len(grads))
@@ -120,10 +135,11 @@ def clip_grad_norm(grads, max_norm: float, norm_type: float = 2.0, eps: float = 
 
 def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, grad_scale: float = 1.0):
     """``clip_grad_norm`` in place on the ``.grad`` of ``parameters`` (a tensor or an iterable);
-    those without one are passed over."""
+    those without one are passed over, and one that is listed again (tied weights) counts once."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
-    return clip_grad_norm([p.grad for p in parameters if p.grad is not None], max_norm, norm_type, eps, grad_scale)
+    unique = {id(p): p for p in parameters}.values()
+    return clip_grad_norm([p.grad for p in unique if p.grad is not None], max_norm, norm_type, eps, grad_scale)
 
 
 def grad_norm(grads, norm_type: float = 2.0, grad_scale: float = 1.0):
