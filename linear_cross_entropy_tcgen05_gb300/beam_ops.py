@@ -33,6 +33,7 @@ def declare(lib) -> None:
 
 
 from . import _call_on, _check, _nbytes, _ptr, _stream, load_library  # noqa: E402  (defined before this module is imported)
+from .grad_ops import check_written  # noqa: E402
 from .norm_ops import DTYPES  # noqa: E402
 
 
@@ -149,7 +150,7 @@ def beam_reorder(states, parents, dims=0, out=None):
     each state), of size B * K, beam j of request b becomes what beam ``parents[b, j]`` of that
     request was. ``parents`` is int32 [B, K] with unit stride along K (the first K columns of
     ``beam_select``'s, say). In place, without a second buffer, or into ``out`` (a list of tensors of the
-    same shapes and types, which share no memory with the states). Returns the reordered tensors.
+    same shapes and types, which share no memory with the states). None may be written twice. Returns the reordered tensors.
 
     States have any type and any strides that leave at most four outer dimensions: a cache's
     first ``length`` positions are reordered alone as ``cache[:, :, :length]``. A parent
@@ -186,6 +187,7 @@ def beam_reorder(states, parents, dims=0, out=None):
                            "new order. Decode under torch.no_grad(), or detach the states")
     if table:
         words = array.array("q", table)
+        check_written(words[0::17], words[1::17])
         _call_on(dev, "flce_beam_reorder", load_library().flce_beam_reorder, words.buffer_info()[0], len(words) // 17,
                  parents.data_ptr(), parents.stride(0) if B > 1 else K, B, K)
         increment_version(dst)  # a backward pass that saved one of them is refused

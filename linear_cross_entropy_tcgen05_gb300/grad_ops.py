@@ -60,16 +60,15 @@ def _dense(t) -> bool:
     return True
 
 
-def _check_written(words) -> None:
-    """Refuses a table in which an entry writes what another one reads or writes."""
-    read, write = words[0::4], [o for o, n in zip(words[1::4], words[2::4]) if n]
+def check_written(read, write) -> None:
+    """Refuses lists of addresses in which an entry writes what another one reads or writes: the kernels work
+    on all entries at once, in no order."""
     if len(set(write)) != len(write):
         raise ValueError("a tensor may not be listed twice")
-    if read != words[1::4]:
-        readers = collections.Counter(g for g, n in zip(read, words[2::4]) if n)
-        for g, o, n in zip(read, words[1::4], words[2::4]):
-            if n and readers[o] != (g == o):
-                raise ValueError("a tensor of out may not be another entry's gradient")
+    if read != write:
+        readers = collections.Counter(read)
+        if any(readers[w] != (w == r) for r, w in zip(read, write)):
+            raise ValueError("a tensor of out may not be another entry's input")
 
 
 def _run(grads, max_norm, norm_type, eps, grad_scale, out):
@@ -101,7 +100,8 @@ def _run(grads, max_norm, norm_type, eps, grad_scale, out):
                 raise ValueError("out must have the gradients' shapes, strides and device")
             words += (p, o.data_ptr(), g.numel(), dt | odt << 32)
     if out is not None:
-        _check_written(words)
+        kept = [k for k in range(0, len(words), 4) if words[k + 2]]  # (entries with elements)
+        check_written([words[k] for k in kept], [words[k + 1] for k in kept])
     lib, table = load_library(), _table(words)
     total = torch.empty((), dtype=torch.float32, device=dev)
     need = lib.flce_clip_grad_norm_workspace_size(len(grads))

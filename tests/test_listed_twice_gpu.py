@@ -37,3 +37,20 @@ def test_clipping_refuses(gpu_lib):
     assert torch.equal(b, c)
     flce.clip_grad_norm([a, a[:0], a[:0]], 1.0)
     flce.clip_grad_norm([a, b], 0.1, out=[a, c])
+
+
+def test_reordering_refuses(gpu_lib):
+    parents = torch.tensor([[1, 0], [0, 1]], dtype=torch.int32, device=DEV)
+    a, b, c = (torch.arange(12.0, device=DEV).view(4, 3).clone() for _ in range(3))
+    before = flce.flce_kernel_launches()
+    for states, out in [([a, a], None), ([a, b, a[:]], None), ([a, b], [c, c]), ([a, b], [b, a]), ([a, b], [b, c]), ([a, a], [a, b])]:
+        with pytest.raises(ValueError):
+            flce.beam_reorder(states, parents, out=out)
+    assert flce.flce_kernel_launches() == before
+    # one state into two others, parts of one buffer, states without elements at one address
+    flce.beam_reorder([a, a], parents, out=[b, c])
+    assert torch.equal(b, c) and b[:, 0].tolist() == [3.0, 0.0, 6.0, 9.0]
+    flce.beam_reorder([a[:, :1], a[:, 1:], a[:, :0], a[:, :0]], parents)
+    assert torch.equal(a, b)
+    flce.beam_reorder([a, b], parents, out=[a, c])
+    assert torch.equal(a, c) and a[:, 0].tolist() == [0.0, 3.0, 6.0, 9.0]
