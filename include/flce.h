@@ -353,7 +353,7 @@ flce_status flce_forward_noalloc(const void* X, const void* W, const int32_t* ta
  * or fp32, the gate one of the two, each parameter any type. gate [gate_rows, D]: gate row g
  * belongs to rows g*N/gate_rows ... (1: a gate for each channel; N: one for each row).
  * Statistics and sums are in 32 bits, y is computed from the unrounded h. h may be the
- * residual's own buffer; the other outputs may not overlap the inputs. D up to 16384; any
+ * residual's own buffer (with ld_residual = D); the other outputs may not overlap the inputs. D up to 16384; any
  * alignment to the elements is taken, rows aligned to eight elements are faster. */
 typedef enum { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_F16 = 1, FLCE_DTYPE_F32 = 2 } flce_dtype;
 typedef enum { FLCE_NORM_RMS = 0, FLCE_NORM_LAYER = 1 } flce_norm;

@@ -273,6 +273,8 @@ flce_status flce_block_norm_forward(const flce_block_norm_desc* d, void* h, void
   if (st != FLCE_OK) return st;
   if (!h) return bad("h", "is null");
   if ((y != nullptr) != (d->weight != nullptr)) return bad("y", "is given exactly when weight is");
+  if (h == d->residual && d->ld_residual != d->D && d->N > 1)  // its rows would be written over ones still to be read
+    return bad("h", "in the residual's buffer, the residual's row stride must be D");
   if (!api_aligned(h, uintptr_t(elem_bytes(d->residual_dtype))) || !api_aligned(y, uintptr_t(elem_bytes(d->x_dtype))) ||
       !api_aligned(stats, 16))
     return FLCE_ERR_ALIGNMENT;
