@@ -8,6 +8,7 @@
 // the device as kernel parameters (no copy, no table kept between calls). The first writes one
 // partial sum a block; every block of the second adds all partial sums in the same fixed order
 // (a few hundred numbers from L2) and so knows the factor without a third launch or an atomic.
+#include <cfloat>
 #include <cmath>
 
 #include "elem_io.cuh"
@@ -181,8 +182,14 @@ __global__ void __launch_bounds__(kClipThreads, kClipPerSm) flce_grad_norm_kerne
   if (threadIdx.x == 0) tb.part[blockIdx.x] = v;
 }
 
+// What the gradients are multiplied with: f, and then tail. A factor below fp32's normal range (gradients
+// near the end of that range, clipped to a small norm) keeps its bits as f 2^-100; else tail is 1.
+struct ClipFactor {
+  float f, tail;
+};
+
 // The total norm and the factor of the gradients, the same in every block.
-template <typename TB> __device__ __forceinline__ float clip_factor(const TB& tb, float* total) {
+template <typename TB> __device__ __forceinline__ ClipFactor clip_factor(const TB& tb, float* total) {
   double v = 0.0;
   for (int i = int(threadIdx.x); i < tb.n_parts; i += kClipThreads) {
     const double w = tb.parts[i];
@@ -193,17 +200,23 @@ template <typename TB> __device__ __forceinline__ float clip_factor(const TB& tb
   *total = float(norm);
   double c = double(tb.max_norm) / (norm + double(tb.eps));
   if (!(c <= 1.0)) c = norm != norm ? norm : 1.0;  // 0 / 0 and inf / inf leave the gradients alone
-  return float(c * double(tb.scale));
+  c *= double(tb.scale);
+  const bool small = fabs(c) < double(FLT_MIN) && c != 0.0;
+  return small ? ClipFactor{float(c * 0x1p100), 0x1p-100f} : ClipFactor{float(c), 1.f};
 }
 
 template <typename T, typename TO>
-__device__ __forceinline__ void chunk_scale(const T* g, TO* out, int64_t n, int64_t e0, int elems, float f) {
+__device__ __forceinline__ void chunk_scale(const T* g, TO* out, int64_t n, int64_t e0, int elems, ClipFactor f) {
   const bool same = misalign(out, sizeof(TO)) == misalign(g, sizeof(T));
   each_vector<T, false>(g, n, e0, elems, [&](const Raw8<T>& r, int64_t e) {
     float2 x[4];
     unpack8(r, x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], both(f));
+    for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], both(f.f));
+    if (f.tail != 1.f) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], both(f.tail));
+    }
     if (same && e >= 0 && e + 8 <= n) {
       raw_store_stream(out + e, pack8<TO>(x));
     } else {
@@ -216,7 +229,7 @@ __device__ __forceinline__ void chunk_scale(const T* g, TO* out, int64_t n, int6
 }
 
 template <typename T>
-__device__ __forceinline__ void chunk_scale_to(const ClipTensor& t, int64_t e0, int elems, float f) {
+__device__ __forceinline__ void chunk_scale_to(const ClipTensor& t, int64_t e0, int elems, ClipFactor f) {
   const T* g = static_cast<const T*>(t.grad);
   if (t.out_dt == ELEM_F32)
     chunk_scale(g, static_cast<float*>(t.out), t.n, e0, elems, f);
@@ -229,14 +242,14 @@ __device__ __forceinline__ void chunk_scale_to(const ClipTensor& t, int64_t e0, 
 template <int CAP>
 __global__ void __launch_bounds__(kClipThreads, kClipPerSm) flce_grad_scale_kernel(const __grid_constant__ ClipTable<CAP> tb) {
   float total;
-  const float f = clip_factor(tb, &total);
+  const ClipFactor f = clip_factor(tb, &total);
   if (blockIdx.x == 0 && threadIdx.x == 0 && tb.total != nullptr) *tb.total = total;
   // a block's chunks of the norm's pass in the opposite order: the last are still in L2, on the
   // side of the device that it is on
   const int grid = int(gridDim.x), b = int(blockIdx.x);
   for (int c = b + (tb.chunks - 1 - b) / grid * grid; b < tb.chunks && c >= 0; c -= grid) {
     const ClipTensor& t = tb.t[find_tensor(tb, c)];
-    if (t.out == nullptr || (f == 1.f && t.out == t.grad)) continue;  // nothing to change
+    if (t.out == nullptr || (f.f == 1.f && f.tail == 1.f && t.out == t.grad)) continue;  // nothing to change
     const int64_t e0 = int64_t(c - t.first) * tb.chunk_elems - misalign(t.grad, elem_bytes(t.dt));
     const int64_t left = t.n - e0;
     const int elems = int(left < tb.chunk_elems ? left : tb.chunk_elems);
