@@ -403,20 +403,28 @@ __device__ __forceinline__ RowThread row_thread(int threads_per_row, int cluster
   return r;
 }
 
-// QUICK: the sigmoid's reciprocal is the instruction's, off by one step at most. With a gate for each
-// row the forward's divisions were a quarter of its time (N = 32768, D = 4096 bf16, layer norms: 427
-// to 312 us); the backward has no registers for eight of these at once (740 to 855 us).
-template <bool QUICK> __device__ __forceinline__ float activate(float g, int act) {
-  if (act != 1) return tanhf(g);
-  const float d = 1.f + expf(-g);
-  if (!QUICK) return 1.f / d;
+// The reciprocal instruction, for d of 1 and more: off by one step at most.
+__device__ __forceinline__ float quick_rcp(float d) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   return r;
 }
-// derivative of the activation, from its value
-__device__ __forceinline__ float activate_d(float a, int act) {
-  return act == 0 ? 1.f : act == 1 ? a * (1.f - a) : 1.f - a * a;
+// QUICK: by that reciprocal. With a gate for each row the forward's divisions were a quarter of its time (N
+// = 32768, D = 4096 bf16, layer norms: 427 to 312 us). The backward takes value and derivative of such a
+// gate from one exponential and one quick reciprocal (702 us with a division and a (1 - a), 649 us so),
+// but for values alone the division: eight of the other at once spill (649 to 883 us).
+template <bool QUICK> __device__ __forceinline__ float activate(float g, int act) {
+  if (act != 1) return tanhf(g);
+  const float d = 1.f + expf(-g);
+  return QUICK ? quick_rcp(d) : 1.f / d;
+}
+// Derivative of the activation, from its argument: with e = exp(-k |g|), k = 1 (sigmoid) or 2 (tanh), it is
+// k^2 e / (1 + e)^2. From the value, a (1 - a) or 1 - a^2, a gate of 8 would lose half its bits and one
+// of 17 all.
+__device__ __forceinline__ float activate_d(float g, int act) {
+  if (act == 0) return 1.f;
+  const float e = expf(act == 1 ? -fabsf(g) : -2.f * fabsf(g)), r = quick_rcp(1.f + e);
+  return act == 1 ? e * r * r : 4.f * e * r * r;
 }
 
 template <bool QUICK> __device__ __forceinline__ void activate8(float2 (&a)[4], int act) {
@@ -424,19 +432,34 @@ template <bool QUICK> __device__ __forceinline__ void activate8(float2 (&a)[4], 
 #pragma unroll
   for (int i = 0; i < 4; ++i) a[i] = make_float2(activate<QUICK>(a[i].x, act), activate<QUICK>(a[i].y, act));
 }
-// derivatives of the activation, from its values
-__device__ __forceinline__ void derive8(const float2 (&a)[4], int act, float2 (&da)[4]) {
+// derivatives of the activation, from its arguments
+__device__ __forceinline__ void derive8(const float2 (&g)[4], int act, float2 (&da)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) da[i] = make_float2(activate_d(a[i].x, act), activate_d(a[i].y, act));
+  for (int i = 0; i < 4; ++i) da[i] = make_float2(activate_d(g[i].x, act), activate_d(g[i].y, act));
 }
 
-template <typename TX, typename TR, bool VEC, bool QUICK>
-__device__ __forceinline__ void load_gate(const BlockNormParams& p, int64_t grow, const Cols& cs, float2 (&a)[4]) {
+// both at once: a's arguments become values
+__device__ __forceinline__ void activate_derive8(float2 (&a)[4], int act, float2 (&da)[4]) {
+  auto one = [&](float& g, float& d) FLCE_INLINE {
+    const float e = expf(act == 1 ? -fabsf(g) : -2.f * fabsf(g)), r = quick_rcp(1.f + e);
+    d = act == 1 ? e * r * r : 4.f * e * r * r;
+    g = act == 2 ? tanhf(g) : g < 0.f ? e * r : r;
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    da[i] = both(1.f);
+    if (act == 0) continue;
+    one(a[i].x, da[i].x);
+    one(a[i].y, da[i].y);
+  }
+}
+
+template <typename TX, typename TR, bool VEC>
+__device__ __forceinline__ void load_gate(const BlockNormParams& p, int64_t grow, const Cols& cs, float2 (&g)[4]) {
   if (p.gate_res_type)
-    unpack8(load8<TR, VEC>(static_cast<const TR*>(p.gate) + grow * p.ld_gate, cs), a);
+    unpack8(load8<TR, VEC>(static_cast<const TR*>(p.gate) + grow * p.ld_gate, cs), g);
   else
-    unpack8(load8<TX, VEC>(static_cast<const TX*>(p.gate) + grow * p.ld_gate, cs), a);
-  activate8<QUICK>(a, p.act);
+    unpack8(load8<TX, VEC>(static_cast<const TX*>(p.gate) + grow * p.ld_gate, cs), g);
 }
 
 // Parameters (zero past the row and where there are none), w + off; read once a block.
@@ -699,7 +722,8 @@ __global__ void __launch_bounds__(bn_max_threads(FEAT, VEC, CLUSTER), 1)
       } else if (gate && row + r >= gate_end) {
         const int g = (row + r) / int(p.gate_group);
         float2 a[4];
-        load_gate<TX, TR, VEC, true>(p, g, cs, a);
+        load_gate<TX, TR, VEC>(p, g, cs, a);
+        activate8<true>(a, p.act);
         set_gate(a);
         gate_end = int((g + 1) * p.gate_group);
       }
@@ -1008,7 +1032,8 @@ __global__ void __launch_bounds__(kBnThreads, 1)
   int slot = 0;
   auto enter = [&](int chunk) FLCE_INLINE {  // a chunk has one gate row
     if (gate && !gate_full && chunk < p.chunks) {
-      load_gate<TX, TR, VEC, false>(p, chunk / int(p.chunks_per_group), cs, a);
+      load_gate<TX, TR, VEC>(p, chunk / int(p.chunks_per_group), cs, a);
+      activate8<false>(a, p.act);
       if (OWN_A) set_own(kA, a);
     }
   };
@@ -1065,10 +1090,11 @@ __global__ void __launch_bounds__(kBnThreads, 1)
           ring.template get<TR>(batch, r, kG, a);
         else
           ring.template get<TX>(batch, r, kG, a);
-        activate8<false>(a, p.act);
-        if (p.dgate != nullptr) {  // d u scale act', u = (x - m) r w1 + b1, or x
+        if (p.dgate == nullptr) {
+          activate8<false>(a, p.act);
+        } else {  // d u scale act', u = (x - m) r w1 + b1, or x
           float2 e[4], da[4];
-          derive8(a, p.act, da);
+          activate_derive8(a, p.act, da);
           if (FULL && post) load_weight<VEC>(p.b1, p.b1_dt, 0.f, cs, e);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -1145,20 +1171,21 @@ __global__ void __launch_bounds__(kBnThreads, 1)
     // the gate, n = (x - m) r), the gate's gradient is (w1 P + b1 Q) scale act', and the chunk's
     // part of w1's and b1's is scale a P and scale a Q.
     if (gate && !gate_full && next.chunk != now.chunk) {
-      float2 e[4], q[4], da[4];
-      if (OWN_A) own(kA, a);
+      float2 e[4], q[4];
       if (OWN_B) own(kDb1, db1);
       if (FULL && POST) param(kW1, w1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = both(0.f);
-      if (FULL && POST) load_weight<VEC>(p.b1, p.b1_dt, 0.f, cs, q);
-      derive8(a, p.act, da);
+      for (int i = 0; i < 4; ++i) e[i] = mul2(dw1[i], w1[i]);
+      if (FULL && POST) {
+        load_weight<VEC>(p.b1, p.b1_dt, 0.f, cs, q);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[i] = mul2(dw1[i], w1[i]);
-        if (FULL && POST) e[i] = fma2(db1[i], q[i], e[i]);
-        e[i] = mul2(e[i], mul2(da[i], both(p.scale)));
+        for (int i = 0; i < 4; ++i) e[i] = fma2(db1[i], q[i], e[i]);
       }
+      load_gate<TX, TR, VEC>(p, now.chunk / int(p.chunks_per_group), cs, q);
+      derive8(q, p.act, q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = mul2(e[i], mul2(q[i], both(p.scale)));
+      if (OWN_A) own(kA, a);
       if (p.dgate == nullptr) {
       } else if (p.part_gate != nullptr) {
         store8<float, VEC>(p.part_gate + int64_t(now.chunk) * D, cs, e);
