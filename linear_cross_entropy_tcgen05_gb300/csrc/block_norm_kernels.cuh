@@ -171,8 +171,7 @@ template <typename T> __device__ __forceinline__ T* row_at(void* base, int64_t r
 // latency, about 500 cycles of shuffles, a barrier and reads, so rows share it). Within a warp
 // the values are spread over the lanes as they are added (NV / 2 + ... + 1 shuffles and one a
 // step after that, instead of five a value). Two scratch buffers take turns, so one barrier a
-// sum is enough: a buffer is written again only after the barrier of the sum between. Words
-// of warps that are not there stay zero.
+// sum is enough: a buffer is written again only after the barrier of the sum between.
 // CLUSTER: blocks share rows; code apart, for its registers.
 template <bool CLUSTER> struct RowSum {
   float* buf;      // [2][kMaxValues * nw] of this row group
@@ -210,13 +209,15 @@ template <bool CLUSTER> struct RowSum {
       named_barrier_sync(uint32_t(bar), uint32_t(threads));
       if constexpr (NV <= 4) {
         float2 lo = both(0.f), hi = both(0.f);
-        const int n4 = (nw * NV + 3) / 4;
+        const int n4 = nw * NV / 4;
 #pragma unroll 4
         for (int w = 0; w < n4; ++w) {
           const float4 q = reinterpret_cast<const float4*>(b)[w];
           lo = add2(lo, make_float2(q.x, q.y));
           hi = add2(hi, make_float2(q.z, q.w));
         }
+        // two values of an odd number of warps: the last one's (what follows is another sum's)
+        if (NV == 2 && (nw & 1)) lo = add2(lo, reinterpret_cast<const float2*>(b)[nw - 1]);
         if constexpr (NV == 2) {
           v[0] = lo.x + hi.x;
           v[1] = lo.y + hi.y;
