@@ -70,3 +70,32 @@ def test_saved_tensors_with_other_strides(gpu_lib, r):
         out = call(t)
     got = torch.autograd.grad(out, leaves, up)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_training_step_in_a_graph(gpu_lib):
+    """The public call and its backward pass, captured and replayed on new contents."""
+    t = make(64, 768, r=torch.float32)
+    leaves = [v.requires_grad_() for v in t.values()]
+    up = [torch.ones(64, 768, device=DEV), torch.ones(64, 768, device=DEV, dtype=torch.bfloat16)]
+
+    def step():
+        out = call(t)
+        return [v.detach() for v in out] + list(torch.autograd.grad(out, leaves, up))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    new = make(64, 768, r=torch.float32, seed=3)
+    with torch.no_grad():
+        for k, v in t.items():
+            v.copy_(new[k])
+    graph.replay()
+    got = [v.clone() for v in out]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, step()))
