@@ -101,6 +101,15 @@ constexpr BnRing bn_ring(const BlockNormShape& s, int planes, bool vec, int feat
   return r;
 }
 
+// Bytes from a line of shared memory to the ring's first row. Half a line for the forward of two RMS norms over
+// 16-bit rows alone: its copies take a line more each (which likely paces reads among writes; N = 65536,
+// D = 4096: 361 us with none, 336 with 16 bytes, 357 with 48, 324 with 64; N = 32768, D = 5120: 228 and 204; up
+// to D = 2048 the same). Other forward kernels lose by it (gates for each row 214 and 224 us, layer norms with
+// gates 276 and 289) or nothing (fp32 rows), the backward 12%.
+__host__ __device__ constexpr int bn_ring_shift(int x_bytes, int residual_bytes, bool vec, int feat, int cluster, bool backward) {
+  return !backward && vec && cluster == 1 && feat == BN_POST && x_bytes == 2 && residual_bytes == 2 ? 64 : 0;
+}
+
 // The features of the kernel that a call with these takes: unaligned rows, and rows shared by
 // clusters unless they have RMS norms alone, take the kernel that has everything, and so do wide
 // blocks of the FULL ones.

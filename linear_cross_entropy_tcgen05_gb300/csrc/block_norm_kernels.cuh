@@ -655,7 +655,8 @@ __global__ void __launch_bounds__(bn_max_threads(FEAT, VEC, CLUSTER), 1)
       }
     }
   };
-  ring.init(ring_smem + (FULL ? kParams * 32 * threads_per_row : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
+  constexpr int kShift = bn_ring_shift(sizeof(TX), sizeof(TR), VEC, FEAT, CLUSTER ? 2 : 1, false);
+  ring.init(ring_smem + kShift + (FULL ? kParams * 32 * threads_per_row : 0), kG + (gate_full ? int(sizeof(TR)) / 2 : 0), batches, per);
   for (uint32_t at = ring.first; at != ring.end; at += ring.batch_bytes) fetch(at);
   if (CLUSTER) cluster_sync_all();
   // Without FULL, c is what a row's value after the first norm is multiplied by: w1 scale
@@ -1260,13 +1261,13 @@ __global__ void __launch_bounds__(kBnThreads, 1)
 }
 
 template <typename K>
-cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& s, unsigned blocks, int planes, bool vec, int feat,
-                      bool backward, cudaStream_t stream) {
+cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& s, unsigned blocks, int planes, int shift, bool vec,
+                      int feat, bool backward, cudaStream_t stream) {
   const int threads = s.threads_per_row * s.rows_per_block;
   const BnRing r = bn_ring(s, planes, vec, feat, backward);
-  size_t smem = size_t(r.params_bytes) + size_t(bn_row_bytes(threads, planes, vec)) * r.per * r.batches;
+  size_t smem = size_t(shift) + size_t(r.params_bytes) + size_t(bn_row_bytes(threads, planes, vec)) * r.per * r.batches;
   if (smem < size_t(threads) * 32) smem = size_t(threads) * 32;  // row groups add up their sums in it
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnSmemBytes + 128);  // (with its shift)
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(blocks * unsigned(s.cluster));
@@ -1286,7 +1287,9 @@ cudaError_t bn_launch(K kernel, const BlockNormParams& p, const BlockNormShape& 
 
 // The kernel of a feature set (as bn_kernel_features gives it); the argument: more of one row a block.
 #define FLCE_BN_CASE(VEC, CLUSTER, FEAT) \
-  case FEAT: return bn_launch(KERNEL<TX, TR, VEC, CLUSTER, FEAT>, p, s, blocks, planes, VEC, FEAT, BACKWARD, stream)
+  case FEAT:                                                                                                          \
+    return bn_launch(KERNEL<TX, TR, VEC, CLUSTER, FEAT>, p, s, blocks, planes,                                        \
+                     bn_ring_shift(sizeof(TX), sizeof(TR), VEC, FEAT, s.cluster, BACKWARD), VEC, FEAT, BACKWARD, stream)
 #define FLCE_BN_WIDE_CASES FLCE_BN_CASE(true, false, 23); FLCE_BN_CASE(true, false, 31)
 #define FLCE_BN_DISPATCH(...)                                                               \
   const int planes = bn_planes(int(sizeof(TX)), int(sizeof(TR)), p.gate_full, BACKWARD);    \
