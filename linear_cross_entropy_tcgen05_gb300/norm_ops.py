@@ -295,7 +295,8 @@ def _forward_mode(args) -> bool:
 
 class BlockNorm(torch.nn.Module):
     """``block_norm`` with parameters of its own: a pre-norm (``weight``), and as asked a post-norm
-    (``post_weight``), a gate for each channel (``gate``, starting at ``gate_init``) and biases."""
+    (``post_weight``), a gate for each channel (``gate``, starting at ``gate_init``) and biases. Parameters may
+    have another type than the activations (fp32 ones, say, by default)."""
 
     def __init__(self, dim: int, norm: str = "rms", eps: float = 1e-6, scale: float = 1.0, post_norm: bool = False,
                  gate_init: float | None = None, gate_activation: str = "none", bias: bool = False, device=None,
@@ -315,6 +316,11 @@ class BlockNorm(torch.nn.Module):
         self.gate = par(torch.full((dim,), float(gate_init), **kw)) if gate_init is not None else None
 
     def forward(self, x, residual=None):
+        gate = self.gate
+        if gate is not None and gate.dtype != x.dtype and (residual is None or gate.dtype != residual.dtype):
+            # the kernels read a gate with the rows, in x's or the residual's type: rounded to x's, half a step
+            # of what its product with x has anyway
+            gate = gate.to(x.dtype)
         return block_norm(x, residual, self.weight, bias=self.bias, post_weight=self.post_weight,
-                          post_bias=self.post_bias, gate=self.gate, gate_activation=self.gate_activation,
+                          post_bias=self.post_bias, gate=gate, gate_activation=self.gate_activation,
                           scale=self.scale, norm=self.norm, eps=self.eps)

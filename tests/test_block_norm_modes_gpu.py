@@ -99,3 +99,19 @@ def test_training_step_in_a_graph(gpu_lib):
     got = [v.clone() for v in out]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+@pytest.mark.parametrize("r", [None, torch.bfloat16, torch.float32])
+def test_module_with_parameters_of_another_type(gpu_lib, r):
+    """Parameters in fp32, as the module makes them unless told, with 16-bit activations."""
+    m = flce.BlockNorm(320, post_norm=True, gate_init=0.3, gate_activation="tanh", device=DEV)
+    x = torch.randn(40, 320, device=DEV).bfloat16()
+    res = None if r is None else torch.randn(40, 320, device=DEV).to(r)
+    h, y = m(x, res)
+    (h.float().sum() + y.float().square().sum()).backward()
+    assert all(p.dtype == p.grad.dtype == torch.float32 and bool(p.grad.isfinite().all()) for p in m.parameters())
+    assert bool(m.gate.grad.any())
+    gate = m.gate.detach()
+    want = flce.block_norm(x, res, m.weight.detach(), post_weight=m.post_weight.detach(), gate_activation="tanh",
+                           gate=gate if r == torch.float32 else gate.bfloat16())
+    assert torch.equal(h, want[0]) and torch.equal(y, want[1])
