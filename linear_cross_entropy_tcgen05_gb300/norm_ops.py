@@ -98,6 +98,13 @@ def _has_rows(t, D: int) -> bool:
         return False
 
 
+def _joined(t):
+    """t, or a copy of one whose rows have more than one stride between them (x[:, 1:] of three dimensions)."""
+    if t is None or t.dim() < 3 or t.is_contiguous() or t.stride(-1) != 1 or _has_rows(t, t.shape[-1]):
+        return t
+    return t.contiguous()
+
+
 def _gate_rows(gate, x) -> int:
     """Rows of the gate: it is shared by all rows ([D]), by equal runs of rows ([G, D], or x's
     shape with ones between the leading dimensions and the last), or has one for each."""
@@ -270,15 +277,18 @@ def block_norm(x, residual=None, weight=None, *, bias=None, post_weight=None, po
     to (x's type or f32; None: nothing is added), ``y`` the next block's or the head's input in
     x's type (None without a ``weight``), ``h`` the new stream in the residual's type. ``gate``
     (x's or the residual's type) has one row for all rows ([D]), one for each equal run of rows
-    ([G, D]; for x [B, T, D] also [B, 1, D]) or x's shape, and goes through
+    ([G, D] for x [N, D], [B, 1, D] for x [B, T, D]) or x's shape, and goes through
     ``gate_activation`` ("none", "sigmoid", "tanh"). ``norm`` is "rms" or "layer"; weights are
-    used as ``weight + weight_offset``. D is at most 16384.
+    used as ``weight + weight_offset``. D is at most 16384. x, residual and gate have unit stride along
+    D; rows with one stride between them are read in place, others are copied first.
 
     Differentiable in every tensor (by backward passes; forward-mode inputs raise); a gradient has its
-    input's type. With a 16-bit residual
-    stream the backward pass reads the rounded h.
+    input's type. With a 16-bit residual stream the backward pass reads the h that was rounded to it, so that
+    the weight's gradient has that rounding too (2.4e-3 of it off in bf16, 1.7e-3 by its own); with an fp32
+    stream nothing is rounded between the passes.
     """
-    args = (x, residual, weight, bias, post_weight, post_bias, gate)
+    args = (_joined(x), _joined(residual), weight, bias, post_weight, post_bias, _joined(gate))
+    x = args[0]
     if torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in args]) or _forward_mode(args):
         return BlockNormFunction.apply(*args, norm, eps, scale, gate_activation, weight_offset)
     desc = _describe(*args, norm, eps, scale, gate_activation, weight_offset)

@@ -115,3 +115,21 @@ def test_module_with_parameters_of_another_type(gpu_lib, r):
     want = flce.block_norm(x, res, m.weight.detach(), post_weight=m.post_weight.detach(), gate_activation="tanh",
                            gate=gate if r == torch.float32 else gate.bfloat16())
     assert torch.equal(h, want[0]) and torch.equal(y, want[1])
+
+
+def test_rows_of_more_than_one_stride(gpu_lib):
+    """All positions but the first of [B, T, D], for the rows and for gates of their shape."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    n = lambda: torch.empty(3, 7, 264, device=DEV, dtype=torch.bfloat16).normal_(generator=g)[:, 1:]  # noqa: E731
+    x, res, gate, w = n(), n(), n(), torch.ones(264, device=DEV)
+    up = n()
+    outs = []
+    for f in (lambda t: t, lambda t: t.contiguous()):
+        leaves = [f(t).detach().requires_grad_() for t in (x, res, gate)]
+        h, y = flce.block_norm(leaves[0], leaves[1], w, gate=leaves[2], gate_activation="sigmoid")
+        assert h.shape == y.shape == (3, 6, 264)
+        outs.append([h.detach(), y.detach(), *torch.autograd.grad([h, y], leaves, [up, up])])
+    assert all(a.shape == b.shape and torch.equal(a, b) for a, b in zip(*outs))
+    assert torch.equal(flce.block_norm(x, res, w, gate=gate, gate_activation="sigmoid")[1], outs[0][1])
+    with pytest.raises(ValueError):  # another stride along D stays refused
+        flce.block_norm(x.transpose(1, 2), None, torch.ones(6, device=DEV))
