@@ -249,7 +249,7 @@ def _call_on(dev: torch.device, where: str, fn, *args) -> None:
     an error. What the small calls spend on the host counts, so the device is switched only
     where it has to be and the stream's handle is asked for without a Stream object. A trace would
     have the outputs' allocation but not what fills them."""
-    if torch.jit.is_tracing():
+    if torch._C._is_tracing():
         raise RuntimeError(f"{where} cannot be traced")
     if dev.index == torch.cuda.current_device():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))

@@ -63,9 +63,10 @@ def _dense(t) -> bool:
 def check_written(read, write) -> None:
     """Refuses lists of addresses in which an entry writes what another one reads or writes: the kernels work
     on all entries at once, in no order."""
-    if len(set(write)) != len(write):
+    written = set(write)
+    if len(written) != len(write):
         raise ValueError("a tensor may not be listed twice")
-    if read != write:
+    if read != write and not written.isdisjoint(read):
         readers = collections.Counter(read)
         if any(readers[w] != (w == r) for r, w in zip(read, write)):
             raise ValueError("a tensor of out may not be another entry's input")
@@ -100,8 +101,10 @@ def _run(grads, max_norm, norm_type, eps, grad_scale, out):
                 raise ValueError("out must have the gradients' shapes, strides and device")
             words += (p, o.data_ptr(), g.numel(), dt | odt << 32)
     if out is not None:
-        kept = [k for k in range(0, len(words), 4) if words[k + 2]]  # (entries with elements)
-        check_written([words[k] for k in kept], [words[k + 1] for k in kept])
+        sizes, read, write = words[2::4], words[0::4], words[1::4]
+        if 0 in sizes:  # (tensors without elements may have one address)
+            read, write = ([a for a, n in zip(t, sizes) if n] for t in (read, write))
+        check_written(read, write)
     lib, table = load_library(), _table(words)
     total = torch.empty((), dtype=torch.float32, device=dev)
     need = lib.flce_clip_grad_norm_workspace_size(len(grads))

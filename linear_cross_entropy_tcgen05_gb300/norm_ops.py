@@ -100,7 +100,7 @@ def _has_rows(t, D: int) -> bool:
 
 def _joined(t):
     """t, or a copy of one whose rows have more than one stride between them (x[:, 1:] of three dimensions)."""
-    if t is None or t.dim() < 3 or t.is_contiguous() or t.stride(-1) != 1 or _has_rows(t, t.shape[-1]):
+    if t is None or t.is_contiguous() or t.stride(-1) != 1 or _has_rows(t, t.shape[-1]):
         return t
     return t.contiguous()
 
@@ -225,11 +225,12 @@ class BlockNormFunction(torch.autograd.Function):
             return (None,) * 12
         # a saved-tensor hook may have brought them back elsewhere or with other strides: described anew
         # (the residual may be gone, h stands in for its type), and copied where the kernels need it
-        x, weight, bias, post_weight, post_bias, gate, h, stats = ctx.saved_tensors
+        saved = ctx.saved_tensors
+        if not all([t is None or t.is_contiguous() for t in saved]):
+            rows = saved[0], saved[5]  # x and the gate are read with strides between their rows
+            saved = [t if t is None or any(t is r for r in rows) and _has_rows(t, t.shape[-1]) else t.contiguous() for t in saved]
+        x, weight, bias, post_weight, post_bias, gate, h, stats = saved
         want, dev, D = ctx.needs_input_grad, x.device, x.shape[-1]
-        x, gate = (t if t is None or t.is_contiguous() or _has_rows(t, D) else t.contiguous() for t in (x, gate))
-        weight, bias, post_weight, post_bias, h, stats = (t if t is None else t.contiguous() for t in (
-            weight, bias, post_weight, post_bias, h, stats))
         words, N, gate_rows = _describe(x, h, weight, bias, post_weight, post_bias, gate, *ctx.opts)
         out = [None] * 12
         at = [0] * 7
@@ -287,8 +288,9 @@ def block_norm(x, residual=None, weight=None, *, bias=None, post_weight=None, po
     the weight's gradient has that rounding too (2.4e-3 of it off in bf16, 1.7e-3 by its own); with an fp32
     stream nothing is rounded between the passes.
     """
-    args = (_joined(x), _joined(residual), weight, bias, post_weight, post_bias, _joined(gate))
-    x = args[0]
+    if x.dim() > 2:
+        x, residual, gate = _joined(x), _joined(residual), _joined(gate)
+    args = (x, residual, weight, bias, post_weight, post_bias, gate)
     if torch.is_grad_enabled() and any([t is not None and t.requires_grad for t in args]) or _forward_mode(args):
         return BlockNormFunction.apply(*args, norm, eps, scale, gate_activation, weight_offset)
     desc = _describe(*args, norm, eps, scale, gate_activation, weight_offset)
