@@ -398,8 +398,9 @@ flce_status flce_block_norm_backward(const flce_block_norm_desc* desc, const voi
  *   out   = g * grad_scale * min(1, max_norm / (total + eps))
  * `tensors` is a host array, read before the call returns. A tensor is n elements in one run
  * of memory; out may be grad (in place, the same type) or NULL (only the norm counts it); a
- * buffer may not be listed twice. total_norm: device fp32 scalar. The sum of squares is held
- * in 64 bits and added in a fixed order. A NaN norm makes every output NaN. The workspace is
+ * buffer may not be listed twice. total_norm: device fp32 scalar. Squares are added in 32 bits by
+ * sixteens (in 64 where these overflow or underflow), their sums in 64 bits, in a fixed order; the factor
+ * is applied in fp32, in two steps where it is below its normal range. A NaN norm makes every output NaN. The workspace is
  * 256-byte aligned and needs no preparation. */
 typedef struct {
   const void* grad;

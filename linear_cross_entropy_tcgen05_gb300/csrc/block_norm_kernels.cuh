@@ -11,9 +11,9 @@
 // parameter; a second kernel adds them in a fixed order, so the gradients do not depend on
 // timing. Statistics and sums are in 32 bits; h and y are rounded once, y from the 32-bit h.
 //
-// Measured (of 6.8 TB/s that a copy reaches): N = 65536, D = 4096 bf16, two RMS norms, forward 355 us (6.0
-// TB/s), backward 485 us (6.6). N = 16384, D = 2304 bf16 with an fp32 residual, layer norms, 16 gate
-// rows: 106 us (4.3), 198 us (3.4): latency and instructions, not memory. Rows shared by
+// Measured (of 6.8 TB/s that a copy reaches): N = 65536, D = 4096 bf16, two RMS norms, forward 324 us (6.6
+// TB/s), backward 479 us (6.7). N = 16384, D = 2304 bf16 with an fp32 residual, layer norms, 16 gate
+// rows: 104 us (4.4), 194 us (3.5): latency and instructions, not memory. Rows shared by
 // clusters, D = 16384: 394 us, 590 us (16384 rows, 5.5). Unaligned rows, D = 4095: bf16 2.6 and 2.2
 // TB/s, fp32 4.0 and 3.0 (bound by instructions: 600 and 1000 for a warp's 256 columns).
 #pragma once
@@ -815,6 +815,10 @@ __global__ void __launch_bounds__(bn_max_threads(FEAT, VEC, CLUSTER), 1)
   if (CLUSTER) cluster_sync_all();  // no block leaves while another may still write to it
 }
 
+// The rows that it reads are x and the stored h: with a 16-bit residual stream that is h rounded to it, while
+// the statistics (and the forward's y) are of the unrounded one. The stream's gradient hardly sees it; the
+// weight's gradient, a sum of dy n, has that rounding beside its own (bf16: 2.4e-3 off, 1.7e-3 without). A
+// caller that wants neither keeps the stream in fp32.
 // With n = (v - m) r and g = upstream * w, a norm's gradient is r (g - mean(g) - n mean(g n)) =
 // r g - r mean(g) - (v - m) r^3 mean(g (v - m)): it is computed in the last form, from the row's
 // own values, so a norm costs two sums in which no normalised row is formed.

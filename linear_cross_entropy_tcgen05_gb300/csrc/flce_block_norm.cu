@@ -39,7 +39,7 @@ int64_t bn_resident(const BlockNormShape& s) {
 
 // How a call's rows are shared out, and the features of its kernel. Wide blocks are taken by rows
 // that 512 threads would share in clusters, and by FULL kernels where they have room for more
-// rows, if there are rows for more (N = 32768, D = 5120 bf16: 230 us against 297 in clusters; N =
+// rows, if there are rows for more (N = 32768, D = 5120 bf16: 204 us against 297 in clusters; N =
 // 16384, D = 2304, layer norms: 106 us against 122; but N = 48, D = 5120: 12.5 us against 11.3; and
 // RMS norms at N = 32768, D = 2560: 126 us against 117). Blocks have half as many threads where
 // rows of 512 would leave no room for two batches of them (fp32 rows of 4096 columns with a

@@ -95,7 +95,7 @@ __device__ __forceinline__ void each_vector(const T* g, int64_t n, int64_t e0, i
   for (int v = int(threadIdx.x) * 8; v < elems; v += kClipThreads * 8) f(clip_load(g, e0 + v, n), e0 + v);
 }
 
-// Squares of a chunk in 32 bits (at most 64 of a thread), chunks in 64 bits. Where a thread's
+// Squares of a chunk in 32 bits (at most 64 of a thread, in four sums of 16), chunks in 64 bits. Where a thread's
 // 32-bit sum may have lost something (overflow, or squares below the normal range) it takes
 // its values once more in 64 bits.
 template <typename T, bool STREAM>

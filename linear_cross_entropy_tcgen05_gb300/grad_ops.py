@@ -123,8 +123,9 @@ def clip_grad_norm(grads, max_norm: float, norm_type: float = 2.0, eps: float = 
 
     ``norm_type`` is 2 or infinity, ``grad_scale`` what every gradient is multiplied with first
     (one over the loss scale or the number of micro-batches), ``out`` a list of tensors of the
-    gradients' shapes that get the result, of any of the three types (None: in place). The
-    sum of squares is held in 64 bits and does not overflow or underflow where the norm does not. As in
+    gradients' shapes that get the result, of any of the three types (None: in place). Squares
+    are added in 32 bits by sixteens, and their sums in 64; nothing overflows or underflows where the norm
+    does not. As in
     torch, a NaN norm makes every gradient NaN, and an infinite one makes them 0 or NaN. A
     tensor may not be listed twice. Runs as under ``no_grad``: the norm and the results carry no gradient.
     """

@@ -15,7 +15,7 @@ def pytest_configure(config):
 
 # Tests whose expected value is wrong. They stay as they are, run, and have to fail.
 WRONG_VALUES = {
-    f"tests/test_beam_gpu.py::test_masked_tokens[{t}]":
+    f"test_beam_gpu.py::test_masked_tokens[{t}]":
         "expects 0 for a row of the type's lowest value: its reference forms score + z - lse in 64 bits, where z and lse are "
         "-3.4e38 and a step is 2^75, so log V = 8.5 and the score of about -5 are lost. Such a row is uniform: log_softmax in 64 "
         "bits gives -log V, the candidate is score - log V (test_beam_scores_gpu.py), below the beam's score, as a "
@@ -26,8 +26,9 @@ WRONG_VALUES = {
 
 def pytest_collection_modifyitems(items):
     for item in items:
-        if item.nodeid in WRONG_VALUES:
-            item.add_marker(pytest.mark.xfail(reason=WRONG_VALUES[item.nodeid], strict=True))
+        reason = WRONG_VALUES.get(item.nodeid.split("/")[-1])
+        if reason:
+            item.add_marker(pytest.mark.xfail(reason=reason, strict=True))
 
 
 def have_gpu() -> bool:
